@@ -77,6 +77,19 @@ class KvParams(ctypes.Structure):
     ]
 
 
+class LinearI8Params(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("d_in", ctypes.c_int32),
+        ("d_out", ctypes.c_int32),
+        ("x_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
 class HstuError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -139,6 +152,25 @@ def load() -> ctypes.CDLL:
     lib.hstu_kv_append.restype = ctypes.c_int
     lib.hstu_kv_evict.argtypes = [KP] + [P] * 6 + [sz, P]
     lib.hstu_kv_evict.restype = ctypes.c_int
+    LI = ctypes.POINTER(LinearI8Params)
+    lib.hstu_linear_i8_workspace_size.argtypes = [LI]
+    lib.hstu_linear_i8_workspace_size.restype = sz
+    lib.hstu_quant_i8_weight.argtypes = [P, i32, i32, i32, P, P, P]
+    lib.hstu_quant_i8_weight.restype = ctypes.c_int
+    lib.hstu_linear_i8.argtypes = [LI] + [P] * 6 + [sz, P]
+    lib.hstu_linear_i8.restype = ctypes.c_int
+    lib.hstu_kv_q4_workspace_size.argtypes = [KP]
+    lib.hstu_kv_q4_workspace_size.restype = sz
+    lib.hstu_kv_append_q4.argtypes = [KP] + [P] * 13 + [sz, P]
+    lib.hstu_kv_append_q4.restype = ctypes.c_int
+    lib.hstu_kv_read_q4.argtypes = [KP] + [P] * 11 + [sz, P]
+    lib.hstu_kv_read_q4.restype = ctypes.c_int
+    lib.hstu_attn_paged_q4_workspace_size.argtypes = [PP, i32]
+    lib.hstu_attn_paged_q4_workspace_size.restype = sz
+    lib.hstu_attn_paged_q4_default_splits.argtypes = [PP, i32]
+    lib.hstu_attn_paged_q4_default_splits.restype = i32
+    lib.hstu_attn_fwd_paged_q4.argtypes = ([PP] + [P] * 16 + [i32, P, i32, i32, P, i32, P, P, sz, P])
+    lib.hstu_attn_fwd_paged_q4.restype = ctypes.c_int
     lib.hstu_version.argtypes = []
     lib.hstu_version.restype = ctypes.c_int
     _lib = lib

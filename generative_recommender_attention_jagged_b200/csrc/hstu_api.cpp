@@ -140,6 +140,7 @@ struct Common {
   const int32_t* num_cand;
   const float *rab_pos, *rab_ts, *gamma, *beta;
   const void *k_pool, *v_pool;
+  const void *k_scales, *v_scales;  // 4-bit pools; null otherwise
   int32_t num_pages;
   const int32_t* page_table;
   int32_t max_pages, page_size;
@@ -164,10 +165,12 @@ int run(const hstu_attn_params* p, const Common& c) {
                   c.num_pages <= 0 || c.max_pages <= 0))
     return HSTU_ERR_INVALID_ARG;
   if (c.splits < 1 || c.splits > kMaxSplits) return HSTU_ERR_INVALID_ARG;
-  const void* ptrs[] = {c.q, c.k, c.v, c.u, c.out, c.ws, c.k_pool, c.v_pool, c.gamma, c.beta};
+  const bool q4 = c.k_scales != nullptr;
+  if (q4 && p->head_dim % 32) return HSTU_ERR_UNSUPPORTED;
+  const void* ptrs[] = {c.q, c.k, c.v, c.u, c.out, c.ws, c.k_pool, c.v_pool, c.k_scales, c.v_scales, c.gamma, c.beta};
   for (const void* ptr : ptrs)
     if (ptr && !aligned16(ptr)) return HSTU_ERR_ALIGNMENT;
-  const bool tc = use_tensor_cores(p);
+  const bool tc = !q4 && use_tensor_cores(p);
   // tensor-core path: whole pages land as 1024-byte-aligned swizzled boxes
   if (tc && c.paged && (c.page_size < 8 || c.page_size > kTile || kTile % c.page_size)) return HSTU_ERR_UNSUPPORTED;
   const int item_tiles = item_tiles_for(p, c.paged);
@@ -223,6 +226,8 @@ int run(const hstu_attn_params* p, const Common& c) {
   a.v_pool = c.v_pool;
   a.page_table = c.page_table;
   a.cached_lens = c.cached_lens;
+  a.k_scales = static_cast<const uint32_t*>(c.k_scales);
+  a.v_scales = static_cast<const uint32_t*>(c.v_scales);
   a.out = c.out;
   a.hdr = static_cast<WsHeader*>(c.ws);
   a.items = reinterpret_cast<WorkItem*>(static_cast<char*>(c.ws) + l.items_off);
@@ -339,6 +344,56 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
   c.beta = ln_beta;
   c.k_pool = k_pool;
   c.v_pool = v_pool;
+  c.num_pages = num_pages;
+  c.page_table = kv_page_table;
+  c.max_pages = max_pages_per_user;
+  c.page_size = page_size;
+  c.cached_lens = cached_lens;
+  c.splits = num_splits;
+  c.out = out;
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  c.stream = reinterpret_cast<cudaStream_t>(stream);
+  c.paged = true;
+  return run(p, c);
+}
+
+size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_splits) {
+  if (check_params(p) != HSTU_OK || p->head_dim % 32 || num_splits < 1 || num_splits > kMaxSplits) return 0;
+  return layout_for(p, 1, false, 1).total;
+}
+
+int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len) {
+  return hstu_attn_paged_default_splits(p, max_cached_len);
+}
+
+int hstu_attn_fwd_paged_q4(const hstu_attn_params* p, const void* q_new, const void* k_new, const void* v_new,
+                           const void* u_new, const int32_t* new_offsets, const int64_t* timestamps,
+                           const int32_t* ts_offsets, const int32_t* num_candidates, const float* rab_pos,
+                           const float* rab_ts, const float* ln_gamma, const float* ln_beta, const void* k_pool,
+                           const void* v_pool, const void* k_scales, const void* v_scales, int32_t num_pages,
+                           const int32_t* kv_page_table, int32_t max_pages_per_user, int32_t page_size,
+                           const int32_t* cached_lens, int32_t num_splits, void* out, void* workspace,
+                           size_t workspace_bytes, hstu_stream_t stream) {
+  if (!k_scales || !v_scales) return HSTU_ERR_INVALID_ARG;
+  Common c;
+  std::memset(&c, 0, sizeof c);
+  c.q = q_new;
+  c.k = k_new;
+  c.v = v_new;
+  c.u = u_new;
+  c.q_offsets = new_offsets;
+  c.ts = timestamps;
+  c.ts_offsets = ts_offsets;
+  c.num_cand = num_candidates;
+  c.rab_pos = rab_pos;
+  c.rab_ts = rab_ts;
+  c.gamma = ln_gamma;
+  c.beta = ln_beta;
+  c.k_pool = k_pool;
+  c.v_pool = v_pool;
+  c.k_scales = k_scales;
+  c.v_scales = v_scales;
   c.num_pages = num_pages;
   c.page_table = kv_page_table;
   c.max_pages = max_pages_per_user;

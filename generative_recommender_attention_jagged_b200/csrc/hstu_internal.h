@@ -89,6 +89,8 @@ struct AttnArgs {
   const void* v_pool;
   const int32_t* page_table;
   const int32_t* cached_lens; // [B] or null (not paged)
+  const uint32_t* k_scales;   // 4-bit pools (quant_common.cuh): a (scale, zero) word per page, head and
+  const uint32_t* v_scales;   // slot; null: the pool holds in_bf16 / fp32 rows
   void* out;
   WsHeader* hdr;
   WorkItem* items;

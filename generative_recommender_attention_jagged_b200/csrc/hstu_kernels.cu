@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "device_common.cuh"
+#include "quant_common.cuh"
 
 namespace hstu {
 
@@ -205,7 +206,9 @@ __device__ __forceinline__ int find_user(const int32_t* off, int B, int row) {
   return lo;
 }
 
-template <typename T>
+// Q4: the cached rows are in 4 bits (quant_common.cuh) and are widened one
+// element at a time: scale * (code - zero), exact to one fp32 rounding.
+template <typename T, bool Q4>
 __global__ void __launch_bounds__(256) attn_simt_kernel(const AttnArgs a, const BucketTable tab) {
   __shared__ long long thr[kMaxBuckets];
   for (int x = threadIdx.x; x < kMaxBuckets; x += blockDim.x) thr[x] = tab.thr[x];
@@ -249,9 +252,19 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(const AttnArgs a, const 
         if (i < hist) break;  // history rows: the loop already covered j = i
         j = i;                // candidate self term
       }
-      const T* kr;
-      const T* vr;
-      if (j < L) {
+      const T* kr = nullptr;
+      const T* vr = nullptr;
+      const uint8_t* kr4 = nullptr;
+      const uint8_t* vr4 = nullptr;
+      float ks = 0.f, kz = 0.f, vs = 0.f, vz = 0.f;
+      if (Q4 && j < L) {
+        const int pid = a.page_table[(size_t)u * a.max_pages + j / a.page_size];
+        const size_t slot = ((size_t)pid * a.H + head) * a.page_size + (j % a.page_size);
+        kr4 = static_cast<const uint8_t*>(a.k_pool) + slot * (d / 2);
+        vr4 = static_cast<const uint8_t*>(a.v_pool) + slot * (d / 2);
+        const uint32_t km = a.k_scales[slot], vm = a.v_scales[slot];
+        ks = meta_scale(km), kz = meta_zero(km), vs = meta_scale(vm), vz = meta_zero(vm);
+      } else if (j < L) {
         const int pid = a.page_table[(size_t)u * a.max_pages + j / a.page_size];
         const size_t base = (((size_t)pid * a.H + head) * a.page_size + (j % a.page_size)) * d;
         kr = kp + base;
@@ -261,11 +274,19 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(const AttnArgs a, const 
         kr = k + base;
         vr = v + base;
       }
+      // element e of a cached or new row
+      auto elem = [&](const T* row, const uint8_t* row4, float sc, float z, int e) -> float {
+        if (Q4 && row4 != nullptr) {
+          const int sh = nibble_shift(e & 7);
+          return sc * ((float)((row4[(e >> 3) * 4 + (sh >> 3)] >> (sh & 4)) & 15) - z);
+        }
+        return to_f(row[e]);
+      };
       float part = 0.f;
 #pragma unroll
       for (int x = 0; x < kSimtMaxPerLane; ++x) {
         const int e = lane + 32 * x;
-        if (x < per_lane && e < d) part = fmaf(qv[x], to_f(kr[e]), part);
+        if (x < per_lane && e < d) part = fmaf(qv[x], elem(kr, kr4, ks, kz, e), part);
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
@@ -276,7 +297,7 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(const AttnArgs a, const 
 #pragma unroll
       for (int x = 0; x < kSimtMaxPerLane; ++x) {
         const int e = lane + 32 * x;
-        if (x < per_lane && e < d) acc[x] = fmaf(wgt, to_f(vr[e]), acc[x]);
+        if (x < per_lane && e < d) acc[x] = fmaf(wgt, elem(vr, vr4, vs, vz, e), acc[x]);
       }
     }
     float* orow = a.o_ws + ((size_t)row * a.H + head) * d;
@@ -598,8 +619,14 @@ cudaError_t launch_plan(const AttnArgs& a, bool schedule, int max_seq_len, cudaS
 cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStream_t s) {
   const long long warps = (long long)a.T_q * a.H;
   const int blocks = (int)std::min<long long>((warps + 7) / 8, (long long)num_sms() * 16);
-  if (a.in_bf16) attn_simt_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(a, thr);
-  else attn_simt_kernel<float><<<blocks, 256, 0, s>>>(a, thr);
+  if (a.k_scales) {
+    if (a.in_bf16) attn_simt_kernel<__nv_bfloat16, true><<<blocks, 256, 0, s>>>(a, thr);
+    else attn_simt_kernel<float, true><<<blocks, 256, 0, s>>>(a, thr);
+  } else if (a.in_bf16) {
+    attn_simt_kernel<__nv_bfloat16, false><<<blocks, 256, 0, s>>>(a, thr);
+  } else {
+    attn_simt_kernel<float, false><<<blocks, 256, 0, s>>>(a, thr);
+  }
   return cudaGetLastError();
 }
 

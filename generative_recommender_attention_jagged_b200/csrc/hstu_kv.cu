@@ -23,30 +23,13 @@
 #include "hstu.h"
 #include "hstu_internal.h"
 #include "device_common.cuh"
+#include "kv_common.h"
 
 namespace hstu {
 namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int32_t kErrPool = -10;
-
-struct KvArgs {
-  int32_t B, H, d, P, num_pages, max_pages, esize, total_new;
-  long long kv_stride;  // elements between tokens of k_new / v_new
-  const uint8_t* k_new;
-  const uint8_t* v_new;
-  const int32_t* new_offsets;
-  const int32_t* num_append;
-  uint8_t* k_pool;
-  uint8_t* v_pool;
-  int32_t* page_table;
-  int32_t* cached_lens;
-  int32_t* free_pages;
-  int32_t* free_count;
-  WsHeader* hdr;     // status word; pad[0] = 1 once the plan was applied
-  int32_t* l_old;    // [B] lengths before the append
-  int32_t* n_app;    // [B] tokens appended
-};
 
 // Exclusive prefix sum of v over the block (all threads call it), with the total.
 __device__ int block_exclusive_scan(int v, int* warp_sums, int& total) {
@@ -247,6 +230,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_evict_kernel(KvArgs a, const 
   if (threadIdx.x == 0) *a.free_count = fc + s_total;
 }
 
+}  // namespace
+
+cudaError_t launch_kv_append_plan(const KvArgs& a, cudaStream_t s) {
+  kv_append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+namespace {
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 size_t ws_bytes_for(const hstu_kv_params* p) {
@@ -310,8 +302,7 @@ int hstu_kv_append(const hstu_kv_params* p, const void* k_new, const void* v_new
   a.l_old = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + sizeof(WsHeader));
   a.n_app = a.l_old + p->batch;
   if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return HSTU_ERR_CUDA;
-  kv_append_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return HSTU_ERR_CUDA;
+  if (launch_kv_append_plan(a, s) != cudaSuccess) return HSTU_ERR_CUDA;
   kv_append_copy_kernel<<<dim3(p->batch, 8), 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }

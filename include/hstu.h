@@ -204,6 +204,34 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
                         hstu_stream_t stream);
 
 /*
+ * Incremental forward over a paged K/V cache held in 4 bits
+ * (hstu_kv_append_q4 writes it).  The definition and every argument of
+ * hstu_attn_fwd_paged, except that a cached key or value element is
+ * scale * (code - zero) of its row:
+ *   k_pool, v_pool [num_pages, H, page_size, head_dim / 2] bytes, two codes each
+ *   k_scales, v_scales [num_pages, H, page_size, 2] bf16: scale, zero point
+ * (format: hstu_kv_append_q4).  The new tokens' k_new and v_new are attended
+ * to as they are given; slots past a user's cached length are not read.
+ * head_dim a multiple of 32, any positive page_size.  A cached row with scale
+ * NaN makes the rows that attend to it NaN.
+ * The products use the codes as exact integers (code - zero is exact in bf16)
+ * and apply the scales to the fp32 sums, so bf16 calls round what
+ * hstu_attn_fwd_paged rounds (the weights a) and the cache adds no rounding.
+ */
+size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_splits);
+int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len);
+int hstu_attn_fwd_paged_q4(const hstu_attn_params* p, const void* q_new, const void* k_new,
+                           const void* v_new, const void* u_new, const int32_t* new_offsets,
+                           const int64_t* timestamps, const int32_t* ts_offsets,
+                           const int32_t* num_candidates, const float* rab_pos,
+                           const float* rab_ts, const float* ln_gamma, const float* ln_beta,
+                           const void* k_pool, const void* v_pool, const void* k_scales,
+                           const void* v_scales, int32_t num_pages, const int32_t* kv_page_table,
+                           int32_t max_pages_per_user, int32_t page_size,
+                           const int32_t* cached_lens, int32_t num_splits, void* out,
+                           void* workspace, size_t workspace_bytes, hstu_stream_t stream);
+
+/*
  * Time buckets of n time differences: out[i] = clamp(floor(ln(|dt[i]|+1)/0.301),
  * 0, num_buckets-1), bit-exact for every int64 input.
  *   dt [n] int64 device; out [n] int32 device; num_buckets 1..128.
@@ -272,6 +300,44 @@ int hstu_layer_f1(const hstu_linear_params* p, const void* x, const void* w1, co
 /* f2 of the layer: hstu_linear without activation (w = W2 [H*d, d_model]). */
 int hstu_layer_f2(const hstu_linear_params* p, const void* y, const void* w2, const float* b2, void* x_next,
                   void* workspace, size_t workspace_bytes, hstu_stream_t stream);
+
+/* ---- Linear layer in 8-bit integers ---------------------------------------
+ *
+ * hstu_linear for serving with W held in 8 bits: x is quantised token by
+ * token inside the call, W channel by channel once (hstu_quant_i8_weight), and
+ * the integer products are summed exactly in int32 on the tensor cores:
+ *   scale_x[t] = max_k |x[t,k]| / 127             (fp32; 0 if below 2^-126)
+ *   code[t,k]  = x[t,k] / scale_x[t] to the nearest integer, ties to even
+ *   out[t,n]   = act(scale_x[t] * scale_w[n] * sum_k code[t,k] w_q[n,k] + bias[n])
+ * with scale, bias and activation in fp32 and one rounding to out's type.  A
+ * row of x with an infinity or NaN gives a row of NaN.
+ */
+#define HSTU_I8_MAX_D_IN 131072 /* 127 * 127 * d_in stays below 2^31 */
+
+typedef struct {
+  int64_t rows;          /* T (0 is allowed: nothing to do)                              */
+  int32_t d_in;          /* K: a multiple of 16, at most HSTU_I8_MAX_D_IN                */
+  int32_t d_out;         /* N: a multiple of 8                                           */
+  int64_t x_stride;      /* elements between rows of x; 0 = d_in; rows 16-byte aligned   */
+  int64_t out_stride;    /* elements between rows of out; 0 = d_out; 16-byte aligned     */
+  hstu_dtype dtype;      /* x: bf16 or fp32                                              */
+  hstu_dtype out_dtype;  /* out: bf16 or fp32                                            */
+  uint32_t flags;        /* HSTU_LIN_SILU                                                */
+} hstu_linear_i8_params;
+
+/* Bytes of workspace: a 256-byte status header, the rows' codes and scales. */
+size_t hstu_linear_i8_workspace_size(const hstu_linear_i8_params* p);
+
+/* w [d_in, d_out] row-major (bf16 or fp32) -> w_q [d_out, d_in] int8 codes (the
+ * rows are W's columns) and w_scale [d_out] fp32, by the rule for x above. */
+int hstu_quant_i8_weight(const void* w, int32_t d_in, int32_t d_out, hstu_dtype dtype, int8_t* w_q, float* w_scale,
+                         hstu_stream_t stream);
+
+/* x [rows, d_in] dtype, w_q and w_scale as hstu_quant_i8_weight writes them,
+ * bias [d_out] fp32 or NULL, out [rows, d_out] out_dtype (must not overlap the
+ * inputs); all 16-byte aligned device pointers. */
+int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* w_q, const float* w_scale,
+                   const float* bias, void* out, void* workspace, size_t workspace_bytes, hstu_stream_t stream);
 
 /* ---- Backward of the attention core ----------------------------------------
  *
@@ -398,6 +464,44 @@ int hstu_kv_append(const hstu_kv_params* p, const void* k_new, const void* v_new
 int hstu_kv_evict(const hstu_kv_params* p, const int32_t* evict_mask, int32_t* page_table, int32_t* cached_lens,
                   int32_t* free_pages, int32_t* free_count, void* workspace, size_t workspace_bytes,
                   hstu_stream_t stream);
+
+/* ---- Paged KV cache in 4 bits ---------------------------------------------
+ *
+ * The cache of the calls above at 4.25 bits an element (d = 128).  Pages, page
+ * table, lengths, free stack, allocation policy and all-or-nothing failures
+ * are those of hstu_kv_append; hstu_kv_evict serves both kinds of pool.
+ *   k_pool, v_pool      [num_pages, H, page_size, d / 2] bytes
+ *   k_scales, v_scales  [num_pages, H, page_size, 2] bf16: scale, zero point
+ * A row (one token and head; K and V by themselves) of elements x_0 .. x_{d-1},
+ * with lo = min(0, min x) and hi = max(0, max x), is held as
+ *   scale = bf16((hi - lo) / 15),  zero = clamp(rint(-lo / scale), 0, 15),
+ *   code  = clamp(rint(x / scale) + zero, 0, 15)
+ * (rint: nearest, ties to even, of the exact quotient) and stands for
+ * scale * (code - zero).  A scale below 2^-126 is stored as 0 with codes and zero
+ * point 0; a row with an infinity or NaN as scale NaN with codes 0.  In each
+ * group of 8 elements (4 bytes) nibble i holds element 2 i and nibble i + 4
+ * element 2 i + 1; nibble 0 is the low half of the first byte.
+ * d a multiple of 32, at most 256; any positive page_size.  hstu_kv_params as
+ * for hstu_kv_append, dtype being that of k_new / v_new (or of the read-back).
+ */
+size_t hstu_kv_q4_workspace_size(const hstu_kv_params* p);
+
+/* hstu_kv_append into a 4-bit pool; k_new and v_new may be NULL when total_new = 0. */
+int hstu_kv_append_q4(const hstu_kv_params* p, const void* k_new, const void* v_new, const int32_t* new_offsets,
+                      const int32_t* num_append, void* k_pool, void* v_pool, void* k_scales, void* v_scales,
+                      int32_t* page_table, int32_t* cached_lens, int32_t* free_pages, int32_t* free_count,
+                      void* workspace, size_t workspace_bytes, hstu_stream_t stream);
+
+/* Dense rows of cached tokens (to move a user to another cache or to recompute
+ * from it): row offsets[u] + i of k_out, v_out [total_new, H, d] (p->dtype) is
+ * token starts[u] + i of user u, i < offsets[u+1] - offsets[u].  A range outside
+ * 0 .. cached_lens[u]-1 or a bad page id is reported in the workspace's status
+ * word (HSTU_ERR_LENGTH, HSTU_ERR_PAGE); the rows it names are left as they
+ * were, and so are rows behind offsets[batch]. */
+int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_pool, const void* k_scales,
+                    const void* v_scales, const int32_t* page_table, const int32_t* cached_lens,
+                    const int32_t* starts, const int32_t* offsets, void* k_out, void* v_out, void* workspace,
+                    size_t workspace_bytes, hstu_stream_t stream);
 
 /* Synchronises `stream`, then returns the status word the device wrote into
  * `workspace` during the last call that used it (HSTU_OK if none). */
