@@ -1,0 +1,528 @@
+// HSTU attention of a few new rows a user over the 4-bit paged cache.
+//
+//   s_ij = alpha ks_j sum_e q_ie (c_je - kz_j) + rab_pos[..] + rab_ts[..]
+//   o_i  = sum_j SiLU(s_ij) vs_j (c'_j - vz_j)
+//
+// with ks, kz (vs, vz) the scale and zero point of key (value) row j and c its
+// codes.  Incremental serving: one or a few new actions of each user against a
+// history of thousands of cached tokens, so every cached byte is read once for
+// a handful of rows and the kernel is bound by those reads (136 bytes a token
+// and head at d = 128).  What follows from that:
+//
+//   - A CTA takes one (user, head, part of the cached keys); its warps walk
+//     tiles of 32 keys by themselves, with no block-wide barrier.  Each warp
+//     keeps a ring of tiles in shared memory filled by cp.async (codes, scale
+//     words and timestamps), so that about 10 KB a warp are in flight while it
+//     computes.
+//   - The products run on mma.sync with the keys as M and the rows as N (8
+//     rows, or 16 in two N tiles): S^T = K Q^T, then O^T = V^T P^T.  With so few
+//     rows the 128-row tiles of tcgen05 would be mostly empty, and the codes
+//     would have to be widened into shared memory; here they are widened in
+//     registers, in the layout the instruction wants: a thread reads 16 bytes
+//     of a key row as they lie (32 codes), and (w >> 4 i) & 0x000F000F with the
+//     exponent of 128 in front is already the bf16 pair 128 + code of two
+//     neighbouring dimensions.  For V^T the pair has to be two keys of one
+//     dimension: one byte permute of two keys' words makes four such pairs.
+//   - The order of the dimensions (of the keys) inside a product is free as
+//     long as both operands agree, so every load is contiguous and no operand
+//     is shuffled; only P^T changes its layout (movmatrix, 8 x 8 a time).
+//   - For K the 128 + kz of each element is taken off after the product, as
+//     (128 + kz) sum_e q_ie in fp32 (8 sums of 16 products: the error stays
+//     near 2^-20 of s, against 2^-9 of the rounding of the weights); for V
+//     before it (the sum runs over thousands of keys), one packed subtraction.
+//   - Weights: SiLU in fp32; a_ij vs_j is rounded once to bf16 for the second
+//     product, sums are fp32.
+//
+// The new rows' own keys are a few: each warp takes rows and does the allowed
+// pairs in fp32 FMAs, so that what a mask hides is never touched.  The CTA that
+// finishes a user last (a counter in the workspace) adds the parts in order,
+// normalises and gates: one launch besides the clearing of the counters.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "device_common.cuh"
+#include "hstu_internal.h"
+#include "quant_common.cuh"
+
+namespace hstu {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRing = 3;       // key tiles a warp has in shared memory
+constexpr int kKeys = 32;      // keys of a tile
+constexpr int kMinPart = 256;  // keys below which a part is not split further
+
+template <int D>
+struct Stage {
+  static constexpr int kRowBytes = D / 2;
+  static constexpr int kVRow = D / 2 + 16;  // padded: the V reads of a warp then hit 32 different banks
+  uint8_t k[kKeys * kRowBytes];
+  uint8_t v[kKeys * kVRow];
+  uint32_t km[kKeys];
+  uint32_t vm[kKeys];
+  long long ts[kKeys];
+};
+
+template <int D, int NQ>
+struct __align__(16) SmallSmem {
+  union {
+    Stage<D> ring[kWarps][kRing];
+    float red[kWarps][8 * NQ][D];
+  };
+  float self[8 * NQ][D];  // the new rows' sums over the new keys
+  long long thr[kMaxBuckets];
+  float rts[kMaxBuckets];
+  uint4 oct[32];
+  int last;
+};
+
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp8(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t add_bf16x2_(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hadd2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// bf16 pair 128 + nibble i of each 16-bit half
+__device__ __forceinline__ uint32_t widen(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+
+__device__ __forceinline__ float silu_exact(float s) { return __fdividef(s, 1.f + __expf(-s)); }
+
+__device__ __forceinline__ float time_bias(const long long* thr, const float* rts, const uint4* oct, long long dt) {
+  const unsigned long long x = abs_dt_plus1(dt);
+  return rts[x < (1ull << 32) ? bucket_oct(oct, (unsigned int)x) : bucket_of_dt(thr, dt)];
+}
+
+__device__ __forceinline__ float warp_add(float x) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+  return x;
+}
+
+// Keys of one part of a user with L cached tokens, and how many parts it has.
+__device__ __forceinline__ int part_keys(int L, int splits) {
+  return max(kMinPart, ((L + splits - 1) / splits + kKeys - 1) / kKeys * kKeys);
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
+                                                                 int32_t* counters) {
+  constexpr int kWords = D / 32;   // words of a K row a thread reads (its quarter of the dimensions)
+  constexpr int kSteps = D / 16;   // products of 16 dimensions
+  constexpr int kTilesM = D / 16;  // 16-dimension tiles of O^T
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SmallSmem<D, NQ>& sm = *reinterpret_cast<SmallSmem<D, NQ>*>(smem_raw);
+  const int split = blockIdx.x, head = blockIdx.y, u = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  int n, tso, pages;
+  if (!check_user(a, u, n, tso, pages)) {
+    if (threadIdx.x == 0) report_error(a.hdr, kErrLength, u);
+    return;
+  }
+  const int q0 = a.q_offsets[u], rows = a.q_offsets[u + 1] - q0;
+  const int L = a.cached_lens[u];
+  const int part = part_keys(L, a.num_splits);
+  const int parts = max(1, (L + part - 1) / part);
+  if (split >= parts) return;
+  const int k_lo = split * part, k_hi = min(L, k_lo + part);
+  const int hist = n - (a.num_cand ? a.num_cand[u] : 0);
+  const int32_t* table = a.page_table + (size_t)u * a.max_pages;
+  const int64_t* ts = a.ts + tso;
+
+  if (head == 0) {
+    // this part's page ids and timestamps (the first part also has the new tokens')
+    for (int x = k_lo / a.page_size + threadIdx.x; x < (k_hi + a.page_size - 1) / a.page_size; x += kThreads) {
+      const int pid = table[x];
+      if (pid < 0 || pid >= a.num_pages) report_error(a.hdr, kErrPage, u);
+    }
+    auto check_ts = [&](int lo, int hi) {
+      for (int j = lo + threadIdx.x; j < hi; j += kThreads) {
+        const long long x = ts[j];
+        if (x > kTsLimit || x < -kTsLimit || (j > 0 && x < ts[j - 1])) report_error(a.hdr, kErrUnsorted, u);
+      }
+    };
+    check_ts(k_lo, k_hi);
+    if (split == 0) check_ts(L, n);
+  }
+  if (rows == 0) return;
+
+  for (int x = threadIdx.x; x < kMaxBuckets; x += kThreads) {
+    sm.thr[x] = tab.thr[x];
+    sm.rts[x] = x < a.nb ? a.rab_ts[x] : 0.f;
+  }
+  if (threadIdx.x < 32)
+    sm.oct[threadIdx.x] = make_uint4(tab.oct[threadIdx.x][0], tab.oct[threadIdx.x][1], tab.oct[threadIdx.x][2],
+                                     tab.oct[threadIdx.x][3]);
+  __syncthreads();
+
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+  const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k);
+  const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v);
+  const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool);
+  const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool);
+  Stage<D>* ring = sm.ring[warp];
+  const int tiles = (k_hi - k_lo + kKeys - 1) / kKeys;
+  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;  // tiles warp, warp + 4, ...
+
+  for (int r0 = 0; r0 < rows; r0 += 8 * NQ) {
+    const int nr = min(8 * NQ, rows - r0);
+    // ---- the rows: fragments of Q^T, their sums, times and positions
+    uint32_t qf[NQ][kSteps][2];
+    float qsum[NQ][2];
+    long long t_i[NQ][2];
+    const float* rp[NQ][2];  // rp[.][.][-j]: position bias of key j
+#pragma unroll
+    for (int w = 0; w < NQ; ++w) {
+      const int r = 8 * w + g;
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint2 x = make_uint2(0, 0);
+        if (r < nr)
+          x = *reinterpret_cast<const uint2*>(q + (size_t)(q0 + r0 + r) * a.qkv_stride + head * D + (D / 4) * t + 4 * k);
+        qf[w][k][0] = x.x;
+        qf[w][k][1] = x.y;
+        s += __uint_as_float(x.x << 16) + __uint_as_float(x.x & 0xFFFF0000u) + __uint_as_float(x.y << 16) +
+             __uint_as_float(x.y & 0xFFFF0000u);
+      }
+      s += __shfl_xor_sync(~0u, s, 1);
+      s += __shfl_xor_sync(~0u, s, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qsum[w][e] = __shfl_sync(~0u, s, 4 * (2 * t + e));  // rows 2 t, 2 t + 1 of this N tile
+        const int i = L + r0 + min(8 * w + 2 * t + e, nr - 1);
+        t_i[w][e] = ts[i];
+        rp[w][e] = a.rab_pos + min(i, hist) + a.n_max - 1;
+      }
+    }
+    float o[NQ][kTilesM][4];
+#pragma unroll
+    for (int w = 0; w < NQ; ++w)
+#pragma unroll
+      for (int m = 0; m < kTilesM; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[w][m][e] = 0.f;
+
+    // page id of this lane's key of the warp's m-th tile (loaded one tile ahead of its copy)
+    auto page_of = [&](int m) -> int {
+      const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
+      return m < mine && j < k_hi ? table[j / a.page_size] : 0;
+    };
+    auto fetch = [&](int m, int pid) {
+      if (m < mine) {
+        const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
+        // a page id out of range is reported above; its rows are not touched
+        const bool on = j < k_hi && pid >= 0 && pid < a.num_pages;
+        Stage<D>& st = ring[m % kRing];
+        const long long slot = on ? ((long long)pid * a.H + head) * a.page_size + j % a.page_size : -1;
+        constexpr int kPieces = D / 32;  // 16-byte pieces of a row
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+          const int c = 32 * x + lane, row = c / kPieces, piece = c % kPieces;
+          const long long s = __shfl_sync(~0u, slot, row);
+          cp16(st.k + row * (D / 2) + piece * 16, kp + (s < 0 ? 0 : s) * (D / 2) + piece * 16, s >= 0);
+          cp16(st.v + row * Stage<D>::kVRow + piece * 16, vp + (s < 0 ? 0 : s) * (D / 2) + piece * 16, s >= 0);
+        }
+        cp4(&st.km[lane], a.k_scales + (on ? slot : 0), on);
+        cp4(&st.vm[lane], a.v_scales + (on ? slot : 0), on);
+        cp8(&st.ts[lane], ts + min(j, n - 1), true);
+      }
+      cp_commit();
+    };
+
+    int pid = page_of(0);
+#pragma unroll
+    for (int m = 0; m < kRing - 1; ++m) {
+      const int next = page_of(m + 1);
+      fetch(m, pid);
+      pid = next;
+    }
+    for (int m = 0; m < mine; ++m) {
+      {
+        const int next = page_of(m + kRing);
+        fetch(m + kRing - 1, pid);
+        pid = next;
+      }
+      cp_wait<kRing - 1>();
+      __syncwarp();
+      const Stage<D>& st = ring[m % kRing];
+      const int j0 = k_lo + (warp + m * kWarps) * kKeys;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // 16 keys
+        // ---- S^T = (128 + codes) Q^T
+        float s[NQ][4];
+#pragma unroll
+        for (int w = 0; w < NQ; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[w][e] = 0.f;
+        uint32_t ka[kWords], kb[kWords];
+        const uint8_t* krow = st.k + (16 * half + g) * (D / 2) + t * (D / 8);
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(krow);
+          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(krow + 8 * (D / 2));
+        } else {
+          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(krow);
+          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(krow + 8 * (D / 2));
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int i = 2 * (k & 1);
+          const uint32_t a0 = widen(ka[k >> 1], i), a1 = widen(kb[k >> 1], i), a2 = widen(ka[k >> 1], i + 1),
+                         a3 = widen(kb[k >> 1], i + 1);
+#pragma unroll
+          for (int w = 0; w < NQ; ++w) mma16816(s[w], a0, a1, a2, a3, qf[w][k][0], qf[w][k][1]);
+        }
+        // ---- weights: s[.][0], s[.][1] are key g of the 16, [2], [3] key g + 8
+        uint32_t p[NQ][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = 16 * half + 8 * x + g, j = j0 + key;
+          const uint32_t km = st.km[key], vm = st.vm[key];
+          const float ks = a.alpha * meta_scale(km), kz = 128.f + meta_zero(km), vs = meta_scale(vm);
+          const long long tj = st.ts[key];
+#pragma unroll
+          for (int w = 0; w < NQ; ++w) {
+            float wt[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float bias = __ldg(rp[w][e] - min(j, L)) + time_bias(sm.thr, sm.rts, sm.oct, t_i[w][e] - tj);
+              const float sc = fmaf(ks, fmaf(-kz, qsum[w][e], s[w][2 * x + e]), bias);
+              wt[e] = j < k_hi ? silu_exact(sc) * vs : 0.f;
+            }
+            p[w][x] = transpose8x8(pack_bf16x2(wt[0], wt[1]));
+          }
+        }
+        // ---- O^T += (codes' - vz) P^T: keys 2 t, 2 t + 1 (lo) and 2 t + 8, 2 t + 9 (hi) of the 16
+        constexpr int kVWords = D / 64;  // words of a V row a thread reads (its eighth of the dimensions)
+        uint32_t vw[4][kVWords], vz[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = 16 * half + 8 * x + 2 * t;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* vrow = st.v + (key + e) * Stage<D>::kVRow + g * (D / 16);
+            if constexpr (D == 128) *reinterpret_cast<uint2*>(vw[2 * x + e]) = *reinterpret_cast<const uint2*>(vrow);
+            else vw[2 * x + e][0] = *reinterpret_cast<const uint32_t*>(vrow);
+          }
+          vz[x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
+        }
+        // word halves of two keys side by side: nibbles 0..3 (elements 0, 2, 4, 6) and 4..7 (1, 3, 5, 7)
+        uint32_t lo[2][kVWords], hi[2][kVWords];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int c = 0; c < kVWords; ++c) {
+            lo[x][c] = __byte_perm(vw[2 * x][c], vw[2 * x + 1][c], 0x5410);
+            hi[x][c] = __byte_perm(vw[2 * x][c], vw[2 * x + 1][c], 0x7632);
+          }
+#pragma unroll
+        for (int m2 = 0; m2 < kTilesM; ++m2) {
+          // d = 128: row g of tile m2 is nibble m2 of the first word, row g + 8 of the second;
+          // d = 64: nibbles m2 and m2 + 4 of the only word
+          uint32_t a0, a1, a2, a3;
+          if constexpr (D == 128) {
+            a0 = widen(m2 < 4 ? lo[0][0] : hi[0][0], m2 & 3);
+            a1 = widen(m2 < 4 ? lo[0][kVWords - 1] : hi[0][kVWords - 1], m2 & 3);
+            a2 = widen(m2 < 4 ? lo[1][0] : hi[1][0], m2 & 3);
+            a3 = widen(m2 < 4 ? lo[1][kVWords - 1] : hi[1][kVWords - 1], m2 & 3);
+          } else {
+            a0 = widen(lo[0][0], m2);
+            a1 = widen(hi[0][0], m2);
+            a2 = widen(lo[1][0], m2);
+            a3 = widen(hi[1][0], m2);
+          }
+          a0 = sub_bf16x2(a0, vz[0]);
+          a1 = sub_bf16x2(a1, vz[0]);
+          a2 = sub_bf16x2(a2, vz[1]);
+          a3 = sub_bf16x2(a3, vz[1]);
+#pragma unroll
+          for (int w = 0; w < NQ; ++w) mma16816(o[w][m2], a0, a1, a2, a3, p[w][0], p[w][1]);
+        }
+      }
+      __syncwarp();  // the tile's slot may be filled again
+    }
+    cp_wait<0>();
+
+    // ---- the new rows' own keys: row r by worker r of the user's parts x warps, fp32
+    for (int x = threadIdx.x; x < 8 * NQ * D; x += kThreads) (&sm.self[0][0])[x] = 0.f;
+    __syncthreads();
+    for (int r = split + parts * warp; r < nr; r += parts * kWarps) {
+      constexpr int kPer = D / 32;
+      const int i = L + r0 + r;
+      const size_t row = (size_t)(q0 + r0 + r) * a.qkv_stride + head * D + kPer * lane;
+      float qv[kPer], acc[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        qv[e] = __bfloat162float(q[row + e]);
+        acc[e] = 0.f;
+      }
+      const bool cand = i >= hist;
+      const int j_end = cand ? hist : i + 1;
+      const long long ti = ts[i];
+      for (int jj = L; jj <= j_end; ++jj) {
+        int j = jj;
+        if (jj == j_end) {
+          if (!cand) break;
+          j = i;
+        }
+        const size_t kr = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) dot = fmaf(qv[e], __bfloat162float(kn[kr + e]), dot);
+        const float sc = a.alpha * warp_add(dot) + a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1] +
+                         time_bias(sm.thr, sm.rts, sm.oct, ti - ts[j]);
+        const float wt = silu_exact(sc);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, __bfloat162float(vn[kr + e]), acc[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) sm.self[r][kPer * lane + e] = acc[e];
+    }
+    // ---- the warps' sums meet in shared memory (the ring is idle) and go out in order
+#pragma unroll
+    for (int w = 0; w < NQ; ++w)
+#pragma unroll
+      for (int m = 0; m < kTilesM; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int nib = (D == 128 ? m : m + 4 * (e >> 1));
+          const int el = nib < 4 ? 2 * nib : 2 * (nib - 4) + 1;
+          const int dim = (D / 8) * g + (D == 128 ? 8 * (e >> 1) : 0) + el;
+          sm.red[warp][8 * w + 2 * t + (e & 1)][dim] = o[w][m][e];
+        }
+    __syncthreads();
+    float* out = a.o_ws + (((size_t)split * a.T_q + q0 + r0) * a.H + head) * D;
+    for (int x = threadIdx.x; x < nr * D; x += kThreads) {
+      const int r = x / D, e = x % D;
+      float s = sm.self[r][e];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += sm.red[w][r][e];
+      out[(size_t)r * a.H * D + e] = s;
+    }
+    __syncthreads();
+  }
+
+  // ---- the last CTA of the user adds the parts, normalises and gates
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u], 1) == a.H * parts - 1;
+  __syncthreads();
+  if (!sm.last) return;
+  __threadfence();
+  const int HD = a.H * D;  // a multiple of 64, at most 1024
+  const float inv_n = 1.f / (float)a.n_max;
+  for (int r = warp; r < rows; r += kWarps) {
+    const size_t row = q0 + r;
+    float2 x[16];
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      x[k] = make_float2(0.f, 0.f);
+      if (64 * k < HD) {
+        const float* src = a.o_ws + row * HD + 64 * k + 2 * lane;
+        for (int s = 0; s < parts; ++s) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + (size_t)s * a.T_q * HD));
+          x[k].x += y.x;
+          x[k].y += y.y;
+        }
+        x[k].x *= inv_n;
+        x[k].y *= inv_n;
+        sum += x[k].x + x[k].y;
+      }
+    }
+    if (a.out_raw) {
+      float* out = static_cast<float*>(a.out) + row * HD + 2 * lane;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (64 * k < HD) *reinterpret_cast<float2*>(out + 64 * k) = x[k];
+      continue;
+    }
+    const float mean = warp_add(sum) / (float)HD;
+    float sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (64 * k < HD) {
+        const float c0 = x[k].x - mean, c1 = x[k].y - mean;
+        sq = fmaf(c0, c0, fmaf(c1, c1, sq));
+      }
+    const float rstd = rsqrtf(warp_add(sq) / (float)HD + a.ln_eps);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * HD + 2 * lane;
+    const __nv_bfloat16* uu = static_cast<const __nv_bfloat16*>(a.u) + row * a.u_stride + 2 * lane;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (64 * k < HD) {
+        const int e = 64 * k + 2 * lane;
+        const float2 ga = a.ln_gamma ? *reinterpret_cast<const float2*>(a.ln_gamma + e) : make_float2(1.f, 1.f);
+        const float2 be = a.ln_beta ? *reinterpret_cast<const float2*>(a.ln_beta + e) : make_float2(0.f, 0.f);
+        const __nv_bfloat162 uv = *reinterpret_cast<const __nv_bfloat162*>(uu + 64 * k);
+        const float y0 = ((x[k].x - mean) * rstd * ga.x + be.x) * __low2float(uv);
+        const float y1 = ((x[k].y - mean) * rstd * ga.y + be.y) * __high2float(uv);
+        *reinterpret_cast<__nv_bfloat162*>(out + 64 * k) = __floats2bfloat162_rn(y0, y1);
+      }
+  }
+}
+
+template <int D, int NQ>
+cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s) {
+  constexpr size_t smem = sizeof(SmallSmem<D, NQ>);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  static unsigned long long attr_set = 0;  // one bit per device
+  if (!(attr_set & (1ull << dev))) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem);
+    if (e != cudaSuccess) return e;
+    attr_set |= 1ull << dev;
+  }
+  attn_q4_small_kernel<D, NQ><<<dim3(a.num_splits, a.H, a.B), kThreads, smem, s>>>(a, thr, counters);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_q4_small_supported(const AttnArgs& a) { return a.in_bf16 && (a.d == 64 || a.d == 128) && a.B <= 65535; }
+
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows_per_tile,
+                                 cudaStream_t s) {
+  if (a.d == 64) return rows_per_tile == 8 ? launch<64, 1>(a, thr, counters, s) : launch<64, 2>(a, thr, counters, s);
+  return rows_per_tile == 8 ? launch<128, 1>(a, thr, counters, s) : launch<128, 2>(a, thr, counters, s);
+}
+
+}  // namespace hstu

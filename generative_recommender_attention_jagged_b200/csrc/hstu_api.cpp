@@ -80,6 +80,12 @@ bool device_is_sm100() {
   return cached[dev] == 1;
 }
 
+int num_sms() {
+  int sms = 148, dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_params(const hstu_attn_params* p) {
@@ -132,6 +138,33 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
   return l;
 }
 
+// ---- the 4-bit cache's kernels ----
+// kQ4Small: bf16, d = 64 or 128, on average at most 16 new rows a user (one
+// pass over the cached bytes serves 8 or 16 rows; with more the rows would
+// re-read them).  kQ4Simt: everything else.
+enum Q4Kernel { kQ4Simt, kQ4Small };
+
+Q4Kernel q4_kernel_for(const hstu_attn_params* p) {
+  if ((p->flags & HSTU_F_FORCE_SIMT) || p->dtype != HSTU_DT_BF16) return kQ4Simt;
+  if ((p->head_dim == 64 || p->head_dim == 128) && p->batch <= 65535 &&
+      (long long)p->total_tokens <= 16ll * p->batch)
+    return kQ4Small;
+  return kQ4Simt;
+}
+
+// rows one pass of the small kernel takes
+int q4_small_rows(const hstu_attn_params* p) { return (long long)p->total_tokens <= 8ll * p->batch ? 8 : 16; }
+
+Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
+  if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
+  Layout l;  // header, a counter per user, partial sums
+  l.max_items = 0;
+  l.items_off = sizeof(WsHeader);
+  l.o_off = align_up(l.items_off + (size_t)p->batch * sizeof(int32_t));
+  l.total = align_up(l.o_off + (size_t)splits * p->total_tokens * p->num_heads * p->head_dim * sizeof(float));
+  return l;
+}
+
 struct Common {
   const void *q, *k, *v, *u;
   const int32_t* q_offsets;
@@ -174,7 +207,8 @@ int run(const hstu_attn_params* p, const Common& c) {
   // tensor-core path: whole pages land as 1024-byte-aligned swizzled boxes
   if (tc && c.paged && (c.page_size < 8 || c.page_size > kTile || kTile % c.page_size)) return HSTU_ERR_UNSUPPORTED;
   const int item_tiles = item_tiles_for(p, c.paged);
-  const Layout l = layout_for(p, tc ? c.splits : 1, tc, item_tiles);
+  const Q4Kernel q4_kernel = q4 ? q4_kernel_for(p) : kQ4Simt;
+  const Layout l = q4 ? q4_layout_for(p, c.splits, q4_kernel) : layout_for(p, tc ? c.splits : 1, tc, item_tiles);
   if (c.ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
 
   uint32_t stages = p->flags & (HSTU_F_STAGE_PLAN | HSTU_F_STAGE_ATTN | HSTU_F_STAGE_EPILOGUE);
@@ -235,6 +269,12 @@ int run(const hstu_attn_params* p, const Common& c) {
 
   const BucketTable& thr = bucket_table(a.nb);
   cudaError_t e = cudaSuccess;
+  if (q4_kernel == kQ4Small) {
+    a.num_splits = c.splits;
+    int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
+    if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
+    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  }
   if (stages & HSTU_F_STAGE_PLAN) {
     if ((e = cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
     if ((e = launch_plan(a, tc, p->max_seq_len, c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
@@ -282,8 +322,7 @@ size_t hstu_attn_paged_workspace_size(const hstu_attn_params* p, int32_t num_spl
 
 int32_t hstu_attn_paged_default_splits(const hstu_attn_params* p, int32_t max_cached_len) {
   if (check_params(p) != HSTU_OK) return 1;
-  int sms = 148, dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = num_sms();
   // work items before splitting: every user has at least one block of query rows
   const long long rows = (long long)item_tiles_for(p, true) * kTile;
   const long long qblocks = std::max<long long>(p->batch, (p->total_tokens + rows - 1) / rows);
@@ -360,11 +399,16 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
 
 size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_splits) {
   if (check_params(p) != HSTU_OK || p->head_dim % 32 || num_splits < 1 || num_splits > kMaxSplits) return 0;
-  return layout_for(p, 1, false, 1).total;
+  return q4_layout_for(p, num_splits, q4_kernel_for(p)).total;
 }
 
 int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len) {
-  return hstu_attn_paged_default_splits(p, max_cached_len);
+  if (check_params(p) != HSTU_OK) return 1;
+  if (q4_kernel_for(p) != kQ4Small) return 1;
+  const long long units = (long long)p->batch * p->num_heads;
+  const long long s = std::max<long long>(1, (long long)num_sms() * 8 / units);
+  const long long most = std::max(1, (max_cached_len + 255) / 256);  // parts of 256 keys or more
+  return (int32_t)std::min<long long>({s, most, kMaxSplits});
 }
 
 int hstu_attn_fwd_paged_q4(const hstu_attn_params* p, const void* q_new, const void* k_new, const void* v_new,
@@ -376,6 +420,7 @@ int hstu_attn_fwd_paged_q4(const hstu_attn_params* p, const void* q_new, const v
                            const int32_t* cached_lens, int32_t num_splits, void* out, void* workspace,
                            size_t workspace_bytes, hstu_stream_t stream) {
   if (!k_scales || !v_scales) return HSTU_ERR_INVALID_ARG;
+  if (p && (p->flags & (HSTU_F_STAGE_PLAN | HSTU_F_STAGE_ATTN | HSTU_F_STAGE_EPILOGUE))) return HSTU_ERR_UNSUPPORTED;
   Common c;
   std::memset(&c, 0, sizeof c);
   c.q = q_new;

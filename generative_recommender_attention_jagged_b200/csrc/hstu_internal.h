@@ -130,6 +130,13 @@ cudaError_t launch_attn_sm100_single(const AttnArgs& a, const BucketTable& thr, 
                                      const CUtensorMap& tm_kpool, const CUtensorMap& tm_vpool, cudaStream_t s);
 cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStream_t s);
 
+// A few new rows a user over a 4-bit pool (attn_q4_small.cu): validation,
+// attention and the LayerNorm gate in one launch; counters [B] zeroed before.
+// bf16, d = 64 or 128; rows_per_tile 8 or 16.
+bool attn_q4_small_supported(const AttnArgs& a);
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows_per_tile,
+                                 cudaStream_t s);
+
 // Backward of the attention core on CUDA cores (hstu_bwd.cu); gradients fp32,
 // d_rp / d_rt must be zeroed by the caller.
 cudaError_t launch_attn_bwd(const AttnArgs& a, const BucketTable& thr, const float* d_o, float* dq, float* dk,

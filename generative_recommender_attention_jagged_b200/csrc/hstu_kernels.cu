@@ -18,40 +18,12 @@ namespace hstu {
 
 namespace {
 
-constexpr long long kTsLimit = 1ll << 61;  // |timestamp| bound that keeps t_i + 1 - thr in range
-
 // ---------------------------------------------------------------------------
 // plan: validation by a grid of (user, part) blocks; the last block to finish
 // builds the work list, longest query blocks first
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 constexpr int kCostBins = 1024;
-
-// checks of one user's offsets, lengths and candidate count (0 = bad)
-__device__ __forceinline__ int check_user(const AttnArgs& a, int u, int& n, int& tso, int& pages) {
-  int ok = 1;
-  const int q0 = a.q_offsets[u], q1 = a.q_offsets[u + 1];
-  if (u == 0 && q0 != 0) ok = 0;
-  if (u == a.B - 1 && q1 != a.T_q) ok = 0;
-  if (q0 < 0 || q1 < q0 || q1 > a.T_q) ok = 0;
-  const int L = a.paged ? a.cached_lens[u] : 0;
-  if (L < 0) ok = 0;
-  const long long nn = (long long)L + (q1 - q0);
-  if (nn > a.n_max) ok = 0;
-  const int c = a.num_cand ? a.num_cand[u] : 0;
-  if (c < 0 || c > q1 - q0) ok = 0;
-  tso = q0;
-  pages = 0;
-  if (a.paged) {
-    tso = a.ts_offsets[u];
-    if (u == 0 && tso != 0) ok = 0;
-    if ((long long)a.ts_offsets[u + 1] - tso != nn) ok = 0;
-    pages = ceil_div(L, a.page_size);
-    if (pages > a.max_pages) ok = 0;
-  }
-  n = (int)nn;
-  return ok;
-}
 
 // work list: per user, blocks of item_tiles * kTile query rows, each expanded to
 // H heads x num_splits splits; counting sort by cost (key tiles per split).

@@ -212,8 +212,9 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
  *   k_scales, v_scales [num_pages, H, page_size, 2] bf16: scale, zero point
  * (format: hstu_kv_append_q4).  The new tokens' k_new and v_new are attended
  * to as they are given; slots past a user's cached length are not read.
- * head_dim a multiple of 32, any positive page_size.  A cached row with scale
- * NaN makes the rows that attend to it NaN.
+ * head_dim a multiple of 32, any positive page_size; the HSTU_F_STAGE_* flags
+ * are not taken (HSTU_ERR_UNSUPPORTED).  A cached row with scale NaN makes the
+ * rows that attend to it NaN.  After a device error `out` holds nothing of use.
  * The products use the codes as exact integers (code - zero is exact in bf16)
  * and apply the scales to the fp32 sums, so bf16 calls round what
  * hstu_attn_fwd_paged rounds (the weights a) and the cache adds no rounding.
