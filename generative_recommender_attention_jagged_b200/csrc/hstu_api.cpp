@@ -141,15 +141,16 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
 // ---- the 4-bit cache's kernels ----
 // kQ4Small: bf16, d = 64 or 128, on average at most 16 new rows a user (one
 // pass over the cached bytes serves 8 or 16 rows; with more the rows would
-// re-read them).  kQ4Simt: everything else.
-enum Q4Kernel { kQ4Simt, kQ4Small };
+// re-read them).  kQ4Tc: bf16, d = 128, more rows than that.  kQ4Simt:
+// everything else.
+enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 
 Q4Kernel q4_kernel_for(const hstu_attn_params* p) {
   if ((p->flags & HSTU_F_FORCE_SIMT) || p->dtype != HSTU_DT_BF16) return kQ4Simt;
   if ((p->head_dim == 64 || p->head_dim == 128) && p->batch <= 65535 &&
       (long long)p->total_tokens <= 16ll * p->batch)
     return kQ4Small;
-  return kQ4Simt;
+  return use_tensor_cores(p) ? kQ4Tc : kQ4Simt;
 }
 
 // rows one pass of the small kernel takes
@@ -160,7 +161,7 @@ Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   Layout l;  // header, a counter per user, partial sums
   l.max_items = 0;
   l.items_off = sizeof(WsHeader);
-  l.o_off = align_up(l.items_off + (size_t)p->batch * sizeof(int32_t));
+  l.o_off = align_up(l.items_off + (kernel == kQ4Small ? (size_t)p->batch * sizeof(int32_t) : 0));
   l.total = align_up(l.o_off + (size_t)splits * p->total_tokens * p->num_heads * p->head_dim * sizeof(float));
   return l;
 }
@@ -274,6 +275,16 @@ int run(const hstu_attn_params* p, const Common& c) {
     int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
     if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
     return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  }
+  if (q4_kernel == kQ4Tc) {
+    a.num_splits = c.splits;
+    a.self_term = 1;
+    CUtensorMap tq;
+    if (!encode_rows(&tq, c.q, a.T_q, a.H, a.d, a.qkv_stride)) return HSTU_ERR_CUDA;
+    if (cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream) != cudaSuccess ||
+        launch_attn_q4_sm100(a, thr, tq, c.stream) != cudaSuccess || launch_epilogue(a, c.stream) != cudaSuccess)
+      return HSTU_ERR_CUDA;
+    return HSTU_OK;
   }
   if (stages & HSTU_F_STAGE_PLAN) {
     if ((e = cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
@@ -404,7 +415,17 @@ size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_
 
 int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len) {
   if (check_params(p) != HSTU_OK) return 1;
-  if (q4_kernel_for(p) != kQ4Small) return 1;
+  const Q4Kernel kernel = q4_kernel_for(p);
+  if (kernel == kQ4Simt) return 1;
+  if (kernel == kQ4Tc) {
+    // one wave of CTAs while there are few tiles; otherwise two halves of every
+    // tile, so that the last wave is short
+    const long long tiles = std::max<long long>(p->batch, (p->total_tokens + kTile - 1) / kTile);
+    const long long units = tiles * p->num_heads;
+    const long long key_tiles = std::max(1, (max_cached_len + kTile - 1) / kTile);
+    const long long s = std::max<long long>(units >= num_sms() ? 2 : 1, num_sms() / units);
+    return (int32_t)std::max<long long>(1, std::min<long long>({s, (key_tiles + 1) / 2, kMaxSplits}));
+  }
   const long long units = (long long)p->batch * p->num_heads;
   const long long s = std::max<long long>(1, (long long)num_sms() * 8 / units);
   const long long most = std::max(1, (max_cached_len + 255) / 256);  // parts of 256 keys or more

@@ -137,6 +137,10 @@ bool attn_q4_small_supported(const AttnArgs& a);
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows_per_tile,
                                  cudaStream_t s);
 
+// Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128;
+// partial sums to o_ws, then launch_epilogue.
+cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const CUtensorMap& tm_q, cudaStream_t s);
+
 // Backward of the attention core on CUDA cores (hstu_bwd.cu); gradients fp32,
 // d_rp / d_rt must be zeroed by the caller.
 cudaError_t launch_attn_bwd(const AttnArgs& a, const BucketTable& thr, const float* d_o, float* dq, float* dk,
