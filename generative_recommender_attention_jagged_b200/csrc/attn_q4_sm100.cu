@@ -222,37 +222,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool sorted = true;
     auto in_range = [](long long x) { return x <= kTsLimit && x >= -kTsLimit; };
     long long last_ts = LLONG_MIN;  // timestamp of the key before the tile
+    // page ids of a tile's keys, loaded a tile before the scales that they lead to; no branch
+    // stands between the loads of the four keys, so that their latencies overlap
+    int pid[4];
+    auto load_pages = [&](int t) {
+      int k0, width;
+      key_tile(g, tb + t, k0, width);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        pid[k] = k0 < g.L ? table[page_index(a, k0 + min(lane + 32 * k, width - 1))] : 0;
+    };
     auto look_up = [&](int t) {
       int k0, width;
       key_tile(g, tb + t, k0, width);
       const bool cached = k0 < g.L;
+      uint32_t km[4], vm[4];
+      bool bad = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k, j = k0 + min(c, width - 1);
+        const int c = lane + 32 * k, j = k0 + min(c, width - 1), page = page_index(a, j);
         kts[k] = a.ts[g.tso + j];
-        krow[k] = -1;
-        kks[k] = 0.f;
-        kvs[k] = 0u;
-        kzz[k] = 0x43004300u;
-        if (c < width) {
-          if (cached) {
-            const int pid = table[j / a.page_size];
-            if (pid >= 0 && pid < a.num_pages) {
-              const long long row = ((long long)pid * a.H + head) * a.page_size + j % a.page_size;
-              const uint32_t km = a.k_scales[row], vm = a.v_scales[row];
-              krow[k] = row;
-              kks[k] = 0.5f * a.alpha * meta_scale(km);
-              kvs[k] = vm & 0xFFFFu;
-              // 128 + zero in bf16, exact
-              kzz[k] = pack_bf16x2(128.f + meta_zero(km), 128.f + meta_zero(vm));
-            } else {
-              report_error(a.hdr, kErrPage, user);
-            }
-          } else {
-            kks[k] = 0.5f * a.alpha;
-            kvs[k] = 0x3F80u;
-          }
-        }
+        const bool in = pid[k] >= 0 && pid[k] < a.num_pages;
+        bad |= !in;
+        krow[k] = ((long long)(in ? pid[k] : 0) * a.H + head) * a.page_size + (cached ? j - page * a.page_size : 0);
+        km[k] = a.k_scales[krow[k]];
+        vm[k] = a.v_scales[krow[k]];
+        if (!in || !cached || c >= width) krow[k] = -1;
+      }
+      if (bad) report_error(a.hdr, kErrPage, user);
+      if (t + 1 < cnt) load_pages(t + 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool fresh = !cached && lane + 32 * k < width;  // a new token
+        const bool held = krow[k] >= 0;
+        kks[k] = held ? 0.5f * a.alpha * meta_scale(km[k]) : fresh ? 0.5f * a.alpha : 0.f;
+        kvs[k] = held ? vm[k] & 0xFFFFu : fresh ? 0x3F80u : 0u;
+        // 128 + zero in bf16, exact
+        kzz[k] = held ? pack_bf16x2(128.f + meta_zero(km[k]), 128.f + meta_zero(vm[k])) : 0x43004300u;
         if (checks) {
           long long before = __shfl_up_sync(~0u, kts[k], 1);
           if (lane == 0) before = last_ts;
@@ -266,7 +272,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       key_tile(g, tb, k0, width);
       if (k0 > 0) last_ts = a.ts[g.tso + k0 - 1];
     }
-    if (cnt > 0) look_up(0);
+    if (cnt > 0) {
+      load_pages(0);
+      look_up(0);
+    }
     for (int t = 0; t < cnt; ++t) {
       const int s = t % kKeyStages;
       bool ok = true;

@@ -15,7 +15,7 @@
 //     words and timestamps), so that about 10 KB a warp are in flight while it
 //     computes.
 //   - The products run on mma.sync with the keys as M and the rows as N (8
-//     rows, or 16 in two N tiles): S^T = K Q^T, then O^T = V^T P^T.  With so few
+//     rows, or 16 in two N tiles): S^T = K Q^T, then O^T = V^T P^T.  With few
 //     rows the 128-row tiles of tcgen05 would be mostly empty, and the codes
 //     would have to be widened into shared memory; here they are widened in
 //     registers, in the layout the instruction wants: a thread reads 16 bytes
@@ -25,13 +25,25 @@
 //     dimension: one byte permute of two keys' words makes four such pairs.
 //   - The order of the dimensions (of the keys) inside a product is free as
 //     long as both operands agree, so every load is contiguous and no operand
-//     is shuffled; only P^T changes its layout (movmatrix, 8 x 8 a time).
+//     is shuffled.
+//   - Between the products the scores go through shared memory once, to one key
+//     a lane: the key's scale, time and position are then one load each and only
+//     the rows there are cost anything (a request with one new action has one of
+//     eight); the weights come back by a transposing ldmatrix.
 //   - For K the 128 + kz of each element is taken off after the product, as
 //     (128 + kz) sum_e q_ie in fp32 (8 sums of 16 products: the error stays
 //     near 2^-20 of s, against 2^-9 of the rounding of the weights); for V
 //     before it (the sum runs over thousands of keys), one packed subtraction.
 //   - Weights: SiLU in fp32; a_ij vs_j is rounded once to bf16 for the second
 //     product, sums are fp32.
+//   - fp32 calls split each row element and each weight into three bf16 terms
+//     (8 + 8 + 8 bits: what is left is below 2^-24 of it) and run each product
+//     three times, smallest terms first; code - zero is exact as it is, and every
+//     tile's O^T is summed from zero and added to the running sum in fp32, since
+//     the tensor core's own sums are not rounded to nearest.
+//
+// Calls with more rows than a tile (fp32, or a head size that the tcgen05 kernel
+// does not take) run a CTA per group of row tiles.
 //
 // The new rows' own keys are a few: each warp takes rows and does the allowed
 // pairs in fp32 FMAs, so that what a mask hides is never touched.  The CTA that
@@ -42,6 +54,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "device_common.cuh"
 #include "hstu_internal.h"
@@ -52,7 +65,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 3;       // key tiles a warp has in shared memory
+constexpr int kRing = 2;       // key tiles a warp has in shared memory
 constexpr int kKeys = 32;      // keys of a tile
 constexpr int kMinPart = 256;  // keys below which a part is not split further
 
@@ -67,13 +80,22 @@ struct Stage {
   long long ts[kKeys];
 };
 
-template <int D, int NQ>
+// Bytes of a key's row in the exchange buffer: fp32 scores, then over them the
+// weights in bf16 (three terms of 16 bytes per 8 rows for fp32 calls).
+template <typename T, int NQ>
+constexpr int kXRow = (sizeof(T) == 4 ? 48 : 32) * NQ;
+
+template <typename T, int D, int NQ>
 struct __align__(16) SmallSmem {
   union {
     Stage<D> ring[kWarps][kRing];
     float red[kWarps][8 * NQ][D];
   };
   float self[8 * NQ][D];  // the new rows' sums over the new keys
+  uint8_t xs[kWarps][kKeys][kXRow<T, NQ>];
+  float qsum[8 * NQ];     // sum_e q_ie
+  long long t_i[8 * NQ];
+  int rp[8 * NQ];         // rab_pos index of key position 0
   long long thr[kMaxBuckets];
   float rts[kMaxBuckets];
   uint4 oct[32];
@@ -105,11 +127,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -121,7 +138,25 @@ __device__ __forceinline__ uint32_t add_bf16x2_(uint32_t a, uint32_t b) {
 // bf16 pair 128 + nibble i of each 16-bit half
 __device__ __forceinline__ uint32_t widen(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
 
-__device__ __forceinline__ float silu_exact(float s) { return __fdividef(s, 1.f + __expf(-s)); }
+template <typename T>
+__device__ __forceinline__ float silu_of(float s) {
+  if constexpr (sizeof(T) == 4) return s / (1.f + expf(-s));
+  else return __fdividef(s, 1.f + __expf(-s));  // a few ulp, far below the weight's rounding to bf16
+}
+
+__device__ __forceinline__ float as_f(float x) { return x; }
+__device__ __forceinline__ float as_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// x as three bf16 terms, largest first; their sum is x to 2^-24 |x| (exact for
+// the usual range: each term takes 8 of the 24 bits)
+__device__ __forceinline__ void split3(float x, float (&y)[3]) {
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    y[p] = __bfloat162float(__float2bfloat16_rn(x));
+    // an infinity or NaN (or what rounds to one) stays in the first term
+    x = fabsf(y[p]) <= FLT_MAX ? x - y[p] : 0.f;
+  }
+}
 
 __device__ __forceinline__ float time_bias(const long long* thr, const float* rts, const uint4* oct, long long dt) {
   const unsigned long long x = abs_dt_plus1(dt);
@@ -139,15 +174,17 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
   return max(kMinPart, ((L + splits - 1) / splits + kKeys - 1) / kKeys * kKeys);
 }
 
-template <int D, int NQ>
+template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
-                                                                 int32_t* counters) {
+                                                                 int32_t* counters, int row_groups) {
+  constexpr bool kF32 = sizeof(T) == 4;
+  constexpr int kTerms = kF32 ? 3 : 1;
   constexpr int kWords = D / 32;   // words of a K row a thread reads (its quarter of the dimensions)
   constexpr int kSteps = D / 16;   // products of 16 dimensions
   constexpr int kTilesM = D / 16;  // 16-dimension tiles of O^T
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SmallSmem<D, NQ>& sm = *reinterpret_cast<SmallSmem<D, NQ>*>(smem_raw);
-  const int split = blockIdx.x, head = blockIdx.y, u = blockIdx.z;
+  SmallSmem<T, D, NQ>& sm = *reinterpret_cast<SmallSmem<T, D, NQ>*>(smem_raw);
+  const int split = blockIdx.x % a.num_splits, rg = blockIdx.x / a.num_splits, head = blockIdx.y, u = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
@@ -166,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
   const int32_t* table = a.page_table + (size_t)u * a.max_pages;
   const int64_t* ts = a.ts + tso;
 
-  if (head == 0) {
+  if (head == 0 && rg == 0) {
     // this part's page ids and timestamps (the first part also has the new tokens')
     for (int x = k_lo / a.page_size + threadIdx.x; x < (k_hi + a.page_size - 1) / a.page_size; x += kThreads) {
       const int pid = table[x];
@@ -192,46 +229,60 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
                                      tab.oct[threadIdx.x][3]);
   __syncthreads();
 
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-  const __nv_bfloat16* kn = static_cast<const __nv_bfloat16*>(a.k);
-  const __nv_bfloat16* vn = static_cast<const __nv_bfloat16*>(a.v);
+  const T* q = static_cast<const T*>(a.q);
+  const T* kn = static_cast<const T*>(a.k);
+  const T* vn = static_cast<const T*>(a.v);
   const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool);
   const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool);
   Stage<D>* ring = sm.ring[warp];
   const int tiles = (k_hi - k_lo + kKeys - 1) / kKeys;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;  // tiles warp, warp + 4, ...
 
-  for (int r0 = 0; r0 < rows; r0 += 8 * NQ) {
+  for (int r0 = 8 * NQ * rg; r0 < rows; r0 += 8 * NQ * row_groups) {
     const int nr = min(8 * NQ, rows - r0);
     // ---- the rows: fragments of Q^T, their sums, times and positions
-    uint32_t qf[NQ][kSteps][2];
-    float qsum[NQ][2];
-    long long t_i[NQ][2];
-    const float* rp[NQ][2];  // rp[.][.][-j]: position bias of key j
+    uint32_t qf[NQ][kSteps][2][kTerms];
 #pragma unroll
     for (int w = 0; w < NQ; ++w) {
       const int r = 8 * w + g;
+      const T* qr = q + (size_t)(q0 + r0 + min(r, nr - 1)) * a.qkv_stride + head * D + (D / 4) * t;
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        uint2 x = make_uint2(0, 0);
-        if (r < nr)
-          x = *reinterpret_cast<const uint2*>(q + (size_t)(q0 + r0 + r) * a.qkv_stride + head * D + (D / 4) * t + 4 * k);
-        qf[w][k][0] = x.x;
-        qf[w][k][1] = x.y;
-        s += __uint_as_float(x.x << 16) + __uint_as_float(x.x & 0xFFFF0000u) + __uint_as_float(x.y << 16) +
-             __uint_as_float(x.y & 0xFFFF0000u);
+        float x[4];
+        if constexpr (kF32) {
+          const float4 f = *reinterpret_cast<const float4*>(qr + 4 * k);
+          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+          const uint2 f = *reinterpret_cast<const uint2*>(qr + 4 * k);
+          x[0] = __uint_as_float(f.x << 16), x[1] = __uint_as_float(f.x & 0xFFFF0000u);
+          x[2] = __uint_as_float(f.y << 16), x[3] = __uint_as_float(f.y & 0xFFFF0000u);
+        }
+        s += (x[0] + x[1]) + (x[2] + x[3]);
+        if constexpr (kF32) {
+          float y[4][3];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split3(x[e], y[e]);
+#pragma unroll
+          for (int p = 0; p < kTerms; ++p) {
+            qf[w][k][0][p] = pack_bf16x2(y[0][p], y[1][p]);
+            qf[w][k][1][p] = pack_bf16x2(y[2][p], y[3][p]);
+          }
+        } else {
+          qf[w][k][0][0] = pack_bf16x2(x[0], x[1]);
+          qf[w][k][1][0] = pack_bf16x2(x[2], x[3]);
+        }
       }
       s += __shfl_xor_sync(~0u, s, 1);
       s += __shfl_xor_sync(~0u, s, 2);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        qsum[w][e] = __shfl_sync(~0u, s, 4 * (2 * t + e));  // rows 2 t, 2 t + 1 of this N tile
-        const int i = L + r0 + min(8 * w + 2 * t + e, nr - 1);
-        t_i[w][e] = ts[i];
-        rp[w][e] = a.rab_pos + min(i, hist) + a.n_max - 1;
+      if (warp == 0 && t == 0) {  // what the weights need of row r
+        const int i = L + r0 + min(r, nr - 1);
+        sm.qsum[r] = s;
+        sm.t_i[r] = ts[i];
+        sm.rp[r] = min(i, hist) + a.n_max - 1;
       }
     }
+    __syncthreads();
     float o[NQ][kTilesM][4];
 #pragma unroll
     for (int w = 0; w < NQ; ++w)
@@ -243,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
     // page id of this lane's key of the warp's m-th tile (loaded one tile ahead of its copy)
     auto page_of = [&](int m) -> int {
       const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
-      return m < mine && j < k_hi ? table[j / a.page_size] : 0;
+      return m < mine && j < k_hi ? table[page_index(a, j)] : 0;
     };
     auto fetch = [&](int m, int pid) {
       if (m < mine) {
@@ -251,7 +302,8 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
         // a page id out of range is reported above; its rows are not touched
         const bool on = j < k_hi && pid >= 0 && pid < a.num_pages;
         Stage<D>& st = ring[m % kRing];
-        const long long slot = on ? ((long long)pid * a.H + head) * a.page_size + j % a.page_size : -1;
+        const long long slot =
+            on ? ((long long)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : -1;
         constexpr int kPieces = D / 32;  // 16-byte pieces of a row
 #pragma unroll
         for (int x = 0; x < kPieces; ++x) {
@@ -284,9 +336,10 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       __syncwarp();
       const Stage<D>& st = ring[m % kRing];
       const int j0 = k_lo + (warp + m * kWarps) * kKeys;
+      uint8_t(&xs)[kKeys][kXRow<T, NQ>] = sm.xs[warp];
+      // ---- S^T = (128 + codes) Q^T (fp32: (codes - kz) Q^T), 16 keys at a time
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // 16 keys
-        // ---- S^T = (128 + codes) Q^T
+      for (int half = 0; half < 2; ++half) {
         float s[NQ][4];
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
@@ -298,83 +351,148 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
           *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(krow);
           *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(krow + 8 * (D / 2));
         } else {
-          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(krow);
-          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(krow + 8 * (D / 2));
-        }
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const int i = 2 * (k & 1);
-          const uint32_t a0 = widen(ka[k >> 1], i), a1 = widen(kb[k >> 1], i), a2 = widen(ka[k >> 1], i + 1),
-                         a3 = widen(kb[k >> 1], i + 1);
-#pragma unroll
-          for (int w = 0; w < NQ; ++w) mma16816(s[w], a0, a1, a2, a3, qf[w][k][0], qf[w][k][1]);
-        }
-        // ---- weights: s[.][0], s[.][1] are key g of the 16, [2], [3] key g + 8
-        uint32_t p[NQ][2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = 16 * half + 8 * x + g, j = j0 + key;
-          const uint32_t km = st.km[key], vm = st.vm[key];
-          const float ks = a.alpha * meta_scale(km), kz = 128.f + meta_zero(km), vs = meta_scale(vm);
-          const long long tj = st.ts[key];
-#pragma unroll
-          for (int w = 0; w < NQ; ++w) {
-            float wt[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float bias = __ldg(rp[w][e] - min(j, L)) + time_bias(sm.thr, sm.rts, sm.oct, t_i[w][e] - tj);
-              const float sc = fmaf(ks, fmaf(-kz, qsum[w][e], s[w][2 * x + e]), bias);
-              wt[e] = j < k_hi ? silu_exact(sc) * vs : 0.f;
-            }
-            p[w][x] = transpose8x8(pack_bf16x2(wt[0], wt[1]));
+          for (int c = 0; c < kWords; ++c) {
+            ka[c] = reinterpret_cast<const uint32_t*>(krow)[c];
+            kb[c] = reinterpret_cast<const uint32_t*>(krow + 8 * (D / 2))[c];
           }
         }
-        // ---- O^T += (codes' - vz) P^T: keys 2 t, 2 t + 1 (lo) and 2 t + 8, 2 t + 9 (hi) of the 16
-        constexpr int kVWords = D / 64;  // words of a V row a thread reads (its eighth of the dimensions)
-        uint32_t vw[4][kVWords], vz[2];
+        uint32_t za = 0, zb = 0;
+        if constexpr (kF32) {
+          const uint32_t ma = st.km[16 * half + g], mb = st.km[16 * half + g + 8];
+          za = add_bf16x2_(__byte_perm(ma, ma, 0x3232), 0x43004300u);
+          zb = add_bf16x2_(__byte_perm(mb, mb, 0x3232), 0x43004300u);
+        }
+#pragma unroll
+        for (int p = kTerms - 1; p >= 0; --p)
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int i = 2 * (k & 1);
+            uint32_t a0 = widen(ka[k >> 1], i), a1 = widen(kb[k >> 1], i), a2 = widen(ka[k >> 1], i + 1),
+                     a3 = widen(kb[k >> 1], i + 1);
+            if constexpr (kF32) {
+              a0 = sub_bf16x2(a0, za), a1 = sub_bf16x2(a1, zb), a2 = sub_bf16x2(a2, za), a3 = sub_bf16x2(a3, zb);
+            }
+#pragma unroll
+            for (int w = 0; w < NQ; ++w) mma16816(s[w], a0, a1, a2, a3, qf[w][k][0][p], qf[w][k][1][p]);
+          }
+#pragma unroll
+        for (int w = 0; w < NQ; ++w)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            *reinterpret_cast<float2*>(xs[16 * half + 8 * x + g] + 4 * (8 * w + 2 * t)) =
+                make_float2(s[w][2 * x], s[w][2 * x + 1]);
+      }
+      __syncwarp();
+      // ---- weights: lane = key, only the rows there are
+      uint32_t p[kTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
+      {
+        const int j = j0 + lane;
+        const uint32_t km = st.km[lane], vm = st.vm[lane];
+        const float ks = a.alpha * meta_scale(km), kz = kF32 ? 0.f : -(128.f + meta_zero(km));
+        const float vs = meta_scale(vm);
+        const long long tj = st.ts[lane];
+        const float* bias_of = a.rab_pos - min(j, L);
+        const float* sc_of = reinterpret_cast<const float*>(xs[lane]);
+        uint32_t pk[kTerms][4 * NQ];
+#pragma unroll
+        for (int r = 0; r < 8 * NQ; r += 2) {
+          float wt[2] = {0.f, 0.f};
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (r + e < nr) {
+              const float bias = __ldg(bias_of + sm.rp[r + e]) + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
+              const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
+              wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
+            }
+          if constexpr (kF32) {
+            float y[2][3];
+            split3(wt[0], y[0]);
+            split3(wt[1], y[1]);
+#pragma unroll
+            for (int x = 0; x < kTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
+          } else {
+            pk[0][r / 2] = pack_bf16x2(wt[0], wt[1]);
+          }
+        }
+        // the lane's weights over its own scores, then transposed by ldmatrix
+#pragma unroll
+        for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+          for (int w = 0; w < NQ; ++w)
+            *reinterpret_cast<uint4*>(xs[lane] + 16 * (NQ * x + w)) =
+                make_uint4(pk[x][4 * w], pk[x][4 * w + 1], pk[x][4 * w + 2], pk[x][4 * w + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+          for (int w = 0; w < NQ; ++w)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(p[x][w][0]), "=r"(p[x][w][1]), "=r"(p[x][w][2]), "=r"(p[x][w][3])
+                         : "r"(smem_u32(xs[lane] + 16 * (NQ * x + w)))
+                         : "memory");
+      }
+      // ---- O^T += (codes' - vz) P^T
+      constexpr int kHalves = D / 32;  // 16-bit pieces (4 codes) of a V row a thread reads: its eighth of the dimensions
+      uint32_t vh[2][2][kHalves];      // [16 keys][lo, hi]: keys 2 t, 2 t + 1 (lo) or 2 t + 8, 2 t + 9 (hi) side by side
+      uint32_t vz[2][2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int key = 16 * half + 8 * x + 2 * t;
+          const uint8_t* va = st.v + key * Stage<D>::kVRow + g * (D / 16);
+          const uint8_t* vb = va + Stage<D>::kVRow;
+          if constexpr (kHalves % 2 == 0) {
+            uint32_t wa[kHalves / 2], wb[kHalves / 2];
+            if constexpr (D == 128) {
+              *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(va);
+              *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(vb);
+            } else {
+              wa[0] = *reinterpret_cast<const uint32_t*>(va);
+              wb[0] = *reinterpret_cast<const uint32_t*>(vb);
+            }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint8_t* vrow = st.v + (key + e) * Stage<D>::kVRow + g * (D / 16);
-            if constexpr (D == 128) *reinterpret_cast<uint2*>(vw[2 * x + e]) = *reinterpret_cast<const uint2*>(vrow);
-            else vw[2 * x + e][0] = *reinterpret_cast<const uint32_t*>(vrow);
-          }
-          vz[x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
-        }
-        // word halves of two keys side by side: nibbles 0..3 (elements 0, 2, 4, 6) and 4..7 (1, 3, 5, 7)
-        uint32_t lo[2][kVWords], hi[2][kVWords];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int c = 0; c < kVWords; ++c) {
-            lo[x][c] = __byte_perm(vw[2 * x][c], vw[2 * x + 1][c], 0x5410);
-            hi[x][c] = __byte_perm(vw[2 * x][c], vw[2 * x + 1][c], 0x7632);
-          }
-#pragma unroll
-        for (int m2 = 0; m2 < kTilesM; ++m2) {
-          // d = 128: row g of tile m2 is nibble m2 of the first word, row g + 8 of the second;
-          // d = 64: nibbles m2 and m2 + 4 of the only word
-          uint32_t a0, a1, a2, a3;
-          if constexpr (D == 128) {
-            a0 = widen(m2 < 4 ? lo[0][0] : hi[0][0], m2 & 3);
-            a1 = widen(m2 < 4 ? lo[0][kVWords - 1] : hi[0][kVWords - 1], m2 & 3);
-            a2 = widen(m2 < 4 ? lo[1][0] : hi[1][0], m2 & 3);
-            a3 = widen(m2 < 4 ? lo[1][kVWords - 1] : hi[1][kVWords - 1], m2 & 3);
+            for (int c = 0; c < kHalves / 2; ++c) {
+              vh[half][x][2 * c] = __byte_perm(wa[c], wb[c], 0x5410);
+              vh[half][x][2 * c + 1] = __byte_perm(wa[c], wb[c], 0x7632);
+            }
           } else {
-            a0 = widen(lo[0][0], m2);
-            a1 = widen(hi[0][0], m2);
-            a2 = widen(lo[1][0], m2);
-            a3 = widen(hi[1][0], m2);
-          }
-          a0 = sub_bf16x2(a0, vz[0]);
-          a1 = sub_bf16x2(a1, vz[0]);
-          a2 = sub_bf16x2(a2, vz[1]);
-          a3 = sub_bf16x2(a3, vz[1]);
 #pragma unroll
-          for (int w = 0; w < NQ; ++w) mma16816(o[w][m2], a0, a1, a2, a3, p[w][0], p[w][1]);
+            for (int c = 0; c < kHalves; ++c)
+              vh[half][x][c] = (uint32_t)reinterpret_cast<const uint16_t*>(va)[c] |
+                               ((uint32_t)reinterpret_cast<const uint16_t*>(vb)[c] << 16);
+          }
+          vz[half][x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
         }
+      // row g of tile m is the thread's nibble m of its D / 8, row g + 8 its nibble m + D / 16
+#pragma unroll
+      for (int m2 = 0; m2 < kTilesM; ++m2) {
+        constexpr int kSecond = D / 16;
+        float f[NQ][4];
+#pragma unroll
+        for (int w = 0; w < NQ; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[w][e] = kF32 ? 0.f : o[w][m2][e];
+        uint32_t av[2][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          av[half][0] = sub_bf16x2(widen(vh[half][0][m2 >> 2], m2 & 3), vz[half][0]);
+          av[half][1] = sub_bf16x2(widen(vh[half][0][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][0]);
+          av[half][2] = sub_bf16x2(widen(vh[half][1][m2 >> 2], m2 & 3), vz[half][1]);
+          av[half][3] = sub_bf16x2(widen(vh[half][1][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][1]);
+        }
+#pragma unroll
+        for (int x = kTerms - 1; x >= 0; --x)
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int w = 0; w < NQ; ++w)
+              mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half], p[x][w][2 * half + 1]);
+#pragma unroll
+        for (int w = 0; w < NQ; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[w][m2][e] = kF32 ? o[w][m2][e] + f[w][e] : f[w][e];
       }
       __syncwarp();  // the tile's slot may be filled again
     }
@@ -390,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       float qv[kPer], acc[kPer];
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        qv[e] = __bfloat162float(q[row + e]);
+        qv[e] = as_f(q[row + e]);
         acc[e] = 0.f;
       }
       const bool cand = i >= hist;
@@ -405,12 +523,12 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
         const size_t kr = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
         float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) dot = fmaf(qv[e], __bfloat162float(kn[kr + e]), dot);
+        for (int e = 0; e < kPer; ++e) dot = fmaf(qv[e], as_f(kn[kr + e]), dot);
         const float sc = a.alpha * warp_add(dot) + a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1] +
                          time_bias(sm.thr, sm.rts, sm.oct, ti - ts[j]);
-        const float wt = silu_exact(sc);
+        const float wt = silu_of<T>(sc);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, __bfloat162float(vn[kr + e]), acc[e]);
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, as_f(vn[kr + e]), acc[e]);
       }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) sm.self[r][kPer * lane + e] = acc[e];
@@ -422,9 +540,9 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       for (int m = 0; m < kTilesM; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int nib = (D == 128 ? m : m + 4 * (e >> 1));
-          const int el = nib < 4 ? 2 * nib : 2 * (nib - 4) + 1;
-          const int dim = (D / 8) * g + (D == 128 ? 8 * (e >> 1) : 0) + el;
+          const int idx = m + (e >> 1) * (D / 16), half = idx >> 2, nib = idx & 3;
+          // 16-bit piece (D / 32) g + half of the row: elements 0, 2, 4, 6 of its word, or 1, 3, 5, 7
+          const int piece = (D / 32) * g + half, dim = 8 * (piece >> 1) + 2 * nib + (piece & 1);
           sm.red[warp][8 * w + 2 * t + (e & 1)][dim] = o[w][m][e];
         }
     __syncthreads();
@@ -442,11 +560,11 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
   // ---- the last CTA of the user adds the parts, normalises and gates
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u], 1) == a.H * parts - 1;
+  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u], 1) == a.H * parts * row_groups - 1;
   __syncthreads();
   if (!sm.last) return;
   __threadfence();
-  const int HD = a.H * D;  // a multiple of 64, at most 1024
+  const int HD = a.H * D;  // a multiple of 32, at most 1024
   const float inv_n = 1.f / (float)a.n_max;
   for (int r = warp; r < rows; r += kWarps) {
     const size_t row = q0 + r;
@@ -455,7 +573,7 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       x[k] = make_float2(0.f, 0.f);
-      if (64 * k < HD) {
+      if (64 * k + 2 * lane < HD) {
         const float* src = a.o_ws + row * HD + 64 * k + 2 * lane;
         for (int s = 0; s < parts; ++s) {
           const float2 y = __ldcg(reinterpret_cast<const float2*>(src + (size_t)s * a.T_q * HD));
@@ -471,58 +589,79 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       float* out = static_cast<float*>(a.out) + row * HD + 2 * lane;
 #pragma unroll
       for (int k = 0; k < 16; ++k)
-        if (64 * k < HD) *reinterpret_cast<float2*>(out + 64 * k) = x[k];
+        if (64 * k + 2 * lane < HD) *reinterpret_cast<float2*>(out + 64 * k) = x[k];
       continue;
     }
     const float mean = warp_add(sum) / (float)HD;
     float sq = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if (64 * k < HD) {
+      if (64 * k + 2 * lane < HD) {
         const float c0 = x[k].x - mean, c1 = x[k].y - mean;
         sq = fmaf(c0, c0, fmaf(c1, c1, sq));
       }
     const float rstd = rsqrtf(warp_add(sq) / (float)HD + a.ln_eps);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * HD + 2 * lane;
-    const __nv_bfloat16* uu = static_cast<const __nv_bfloat16*>(a.u) + row * a.u_stride + 2 * lane;
+    T* out = static_cast<T*>(a.out) + row * HD + 2 * lane;
+    const T* uu = static_cast<const T*>(a.u) + row * a.u_stride + 2 * lane;
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if (64 * k < HD) {
+      if (64 * k + 2 * lane < HD) {
         const int e = 64 * k + 2 * lane;
         const float2 ga = a.ln_gamma ? *reinterpret_cast<const float2*>(a.ln_gamma + e) : make_float2(1.f, 1.f);
         const float2 be = a.ln_beta ? *reinterpret_cast<const float2*>(a.ln_beta + e) : make_float2(0.f, 0.f);
-        const __nv_bfloat162 uv = *reinterpret_cast<const __nv_bfloat162*>(uu + 64 * k);
-        const float y0 = ((x[k].x - mean) * rstd * ga.x + be.x) * __low2float(uv);
-        const float y1 = ((x[k].y - mean) * rstd * ga.y + be.y) * __high2float(uv);
-        *reinterpret_cast<__nv_bfloat162*>(out + 64 * k) = __floats2bfloat162_rn(y0, y1);
+        const float y0 = ((x[k].x - mean) * rstd * ga.x + be.x) * as_f(uu[64 * k]);
+        const float y1 = ((x[k].y - mean) * rstd * ga.y + be.y) * as_f(uu[64 * k + 1]);
+        if constexpr (kF32) *reinterpret_cast<float2*>(out + 64 * k) = make_float2(y0, y1);
+        else *reinterpret_cast<__nv_bfloat162*>(out + 64 * k) = __floats2bfloat162_rn(y0, y1);
       }
   }
 }
 
-template <int D, int NQ>
-cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s) {
-  constexpr size_t smem = sizeof(SmallSmem<D, NQ>);
+template <typename T, int D, int NQ>
+cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
+  constexpr size_t smem = sizeof(SmallSmem<T, D, NQ>);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<T, D, NQ>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  attn_q4_small_kernel<D, NQ><<<dim3(a.num_splits, a.H, a.B), kThreads, smem, s>>>(a, thr, counters);
+  attn_q4_small_kernel<T, D, NQ>
+      <<<dim3(a.num_splits * row_groups, a.H, a.B), kThreads, smem, s>>>(a, thr, counters, row_groups);
   return cudaGetLastError();
+}
+
+template <typename T, int NQ>
+cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
+  switch (a.d) {
+    case 32: return launch<T, 32, NQ>(a, thr, counters, row_groups, s);
+    case 64: return launch<T, 64, NQ>(a, thr, counters, row_groups, s);
+    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ>(a, thr, counters, row_groups, s);
+    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ>(a, thr, counters, row_groups, s);
+  }
 }
 
 }  // namespace
 
-bool attn_q4_small_supported(const AttnArgs& a) { return a.in_bf16 && (a.d == 64 || a.d == 128) && a.B <= 65535; }
+bool attn_q4_small_supported(int head_dim, int batch) { return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535; }
 
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows_per_tile,
-                                 cudaStream_t s) {
-  if (a.d == 64) return rows_per_tile == 8 ? launch<64, 1>(a, thr, counters, s) : launch<64, 2>(a, thr, counters, s);
-  return rows_per_tile == 8 ? launch<128, 1>(a, thr, counters, s) : launch<128, 2>(a, thr, counters, s);
+// Rows of one pass over the cached bytes: 16 where users have more than 8 on
+// average (fp32 calls with d > 64: 8, their three-term fragments fill the registers).
+int attn_q4_small_rows(const AttnArgs& a) {
+  return (long long)a.T_q <= 8ll * a.B || (!a.in_bf16 && a.d > 64) ? 8 : 16;
+}
+
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s) {
+  const int rows = attn_q4_small_rows(a);
+  const int groups = (int)std::max<long long>(1, std::min<long long>(64, ((long long)a.T_q + (long long)a.B * rows - 1) /
+                                                                             ((long long)a.B * rows)));
+  if (a.in_bf16)
+    return rows == 8 ? launch_d<__nv_bfloat16, 1>(a, thr, counters, groups, s)
+                     : launch_d<__nv_bfloat16, 2>(a, thr, counters, groups, s);
+  return rows == 8 ? launch_d<float, 1>(a, thr, counters, groups, s) : launch_d<float, 2>(a, thr, counters, groups, s);
 }
 
 }  // namespace hstu

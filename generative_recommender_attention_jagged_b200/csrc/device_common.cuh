@@ -86,6 +86,11 @@ __device__ __forceinline__ TileGeom tile_geom(const AttnArgs& a, int user, int q
   return g;
 }
 
+// page of position j and j's slot in it (a division is ~20 instructions)
+__device__ __forceinline__ int page_index(const AttnArgs& a, int j) {
+  return a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
+}
+
 // key tile t of a query tile: first key position and number of keys
 __device__ __forceinline__ void key_tile(const TileGeom& g, int t, int& k0, int& width) {
   if (t < g.n_pre) {

@@ -139,22 +139,15 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
 }
 
 // ---- the 4-bit cache's kernels ----
-// kQ4Small: bf16, d = 64 or 128, on average at most 16 new rows a user (one
-// pass over the cached bytes serves 8 or 16 rows; with more the rows would
-// re-read them).  kQ4Tc: bf16, d = 128, more rows than that.  kQ4Simt:
-// everything else.
+// kQ4Tc: bf16, d = 128 and on average more than 16 new rows a user: 128-row
+// tiles on tcgen05.  kQ4Small: the others up to d = 128, 8 or 16 rows a pass.
+// kQ4Simt: d > 128, or on request.
 enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 
 Q4Kernel q4_kernel_for(const hstu_attn_params* p) {
-  if ((p->flags & HSTU_F_FORCE_SIMT) || p->dtype != HSTU_DT_BF16) return kQ4Simt;
-  if ((p->head_dim == 64 || p->head_dim == 128) && p->batch <= 65535 &&
-      (long long)p->total_tokens <= 16ll * p->batch)
-    return kQ4Small;
-  return use_tensor_cores(p) ? kQ4Tc : kQ4Simt;
+  if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, p->batch)) return kQ4Simt;
+  return use_tensor_cores(p) && (long long)p->total_tokens > 16ll * p->batch ? kQ4Tc : kQ4Small;
 }
-
-// rows one pass of the small kernel takes
-int q4_small_rows(const hstu_attn_params* p) { return (long long)p->total_tokens <= 8ll * p->batch ? 8 : 16; }
 
 Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
@@ -230,6 +223,9 @@ int run(const hstu_attn_params* p, const Common& c) {
   a.paged = c.paged ? 1 : 0;
   a.num_splits = tc ? c.splits : 1;
   a.page_size = c.page_size;
+  a.page_shift = -1;
+  for (int b = 0; b < 31; ++b)
+    if (c.page_size == 1 << b) a.page_shift = b;
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;
   a.max_items = l.max_items;
@@ -274,7 +270,7 @@ int run(const hstu_attn_params* p, const Common& c) {
     a.num_splits = c.splits;
     int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
     if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
-    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+    return launch_attn_q4_small(a, thr, counters, c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
     a.num_splits = c.splits;
@@ -426,8 +422,9 @@ int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max
     const long long s = std::max<long long>(units >= num_sms() ? 2 : 1, num_sms() / units);
     return (int32_t)std::max<long long>(1, std::min<long long>({s, (key_tiles + 1) / 2, kMaxSplits}));
   }
-  const long long units = (long long)p->batch * p->num_heads;
-  const long long s = std::max<long long>(1, (long long)num_sms() * 8 / units);
+  // about eight CTAs an SM: two waves of them even out users of different length
+  const long long tiles = std::max<long long>(p->batch, p->total_tokens / 16);
+  const long long s = std::max<long long>(1, (long long)num_sms() * 8 / (tiles * p->num_heads));
   const long long most = std::max(1, (max_cached_len + 255) / 256);  // parts of 256 keys or more
   return (int32_t)std::min<long long>({s, most, kMaxSplits});
 }

@@ -65,6 +65,7 @@ struct AttnArgs {
   int32_t paged;        // 0 = jagged full sequence, 1 = paged prefix + new tokens
   int32_t num_splits;
   int32_t page_size, num_pages, max_pages;
+  int32_t page_shift;   // log2(page_size), or -1 where it is no power of two (4-bit kernels)
   int32_t max_items;
   int32_t item_tiles;   // query tiles per work item: 2 (two-tile kernel) or 1 (one-tile kernel)
   int32_t out_raw;      // write o (fp32 [T,H,d]) instead of y
@@ -132,10 +133,9 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStre
 
 // A few new rows a user over a 4-bit pool (attn_q4_small.cu): validation,
 // attention and the LayerNorm gate in one launch; counters [B] zeroed before.
-// bf16, d = 64 or 128; rows_per_tile 8 or 16.
-bool attn_q4_small_supported(const AttnArgs& a);
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows_per_tile,
-                                 cudaStream_t s);
+// bf16 and fp32, d = 32, 64, 96 or 128.
+bool attn_q4_small_supported(int head_dim, int batch);
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s);
 
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128;
 // partial sums to o_ws, then launch_epilogue.
