@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "device_common.cuh"
+#include "pair_common.cuh"
 #include "hstu.h"
 #include "hstu_internal.h"
 #include "quant_common.cuh"
@@ -288,6 +289,323 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, BN);
 }
 
+// ---- GEMM on SM pairs -----------------------------------------------------------
+// Large calls: the structure of gemm_sm100.cu (a cluster of two CTAs shares a
+// 256 x 256 output tile, M = 256 MMAs issued by the even CTA, persistent over the
+// tiles, two accumulators so that a tile's epilogue overlaps the next one's MMAs)
+// with 8-bit operands, both K-major: a 128-code row is one 128-byte swizzled line,
+// so a stage of 128 codes has the bytes of one of 64 bf16 and the MMAs take the
+// same time for twice the K.
+//
+// At K = 512 the epilogue has as much to do as the tensor core: 128 x 256 sums per
+// CTA and 2048 cycles of MMAs leave 8 cycles a warp row of 32.  The special-function
+// unit gives one of tanh and int-to-float conversion in that time, so the conversion
+// is done on the other pipes: the halves of the int32 go into the mantissa of 2^23
+// (exact), 65536 hi + lo is one rounded FMA, and the multiplications are packed in
+// pairs.  Each half of the epilogue (4 warps) has its own two staging boxes.
+constexpr int kPairStages = 5;
+constexpr int kPairStage = kBM * kBK;   // 16 KB: this CTA's 128 rows of x, or 128 channels of w
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
+constexpr int kPairBN = 256;
+constexpr int kBox = kBM * 128;         // 128 rows x 128 bytes of output
+
+struct __align__(1024) SmemPair {
+  uint8_t x[kPairStages][kPairStage];
+  uint8_t w[kPairStages][kPairStage];
+  uint8_t out[2][2][kBox];              // [half][in turn]
+  uint64_t full[kPairStages];           // even CTA: both CTAs' bytes of the stage landed
+  uint64_t empty[kPairStages];          // both CTAs: the MMAs that read the stage completed
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];                // even CTA: both CTAs' epilogues read accumulator b
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort;
+  int issued;
+};
+constexpr size_t kSmemPair = sizeof(SmemPair) + 1024;
+static_assert(kSmemPair <= 227 * 1024, "shared memory budget");
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// the 128 threads of an epilogue half agree on a flag
+__device__ __forceinline__ bool half_all(bool ok, int half) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "r"(3 + half)
+      : "memory");
+  return r != 0;
+}
+
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// two int32 as fp32, each rounded once: the signed upper and unsigned lower 16 bits sit
+// exactly in the mantissa of 2^23
+__device__ __forceinline__ uint64_t ints_to_float2(uint32_t a, uint32_t b) {
+  const uint64_t hi = pack2(__uint_as_float(__byte_perm(a ^ 0x80000000u, 0x4B000000u, 0x7632)),
+                            __uint_as_float(__byte_perm(b ^ 0x80000000u, 0x4B000000u, 0x7632)));
+  const uint64_t lo = pack2(__uint_as_float((a & 0xFFFFu) | 0x4B000000u), __uint_as_float((b & 0xFFFFu) | 0x4B000000u));
+  const uint64_t h = add2(hi, pack2(-8421376.f, -8421376.f));  // 2^23 + 2^15
+  return fma2(h, pack2(65536.f, 65536.f), add2(lo, pack2(-8388608.f, -8388608.f)));
+}
+
+template <typename TOut>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_i8_pair_kernel(const GemmI8Args a, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_out) {
+  extern __shared__ uint8_t smem_raw[];
+  SmemPair& sm = aligned_smem<SmemPair>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int tiles_n = (a.N + kPairBN - 1) / kPairBN;
+  const int n_units = (int)((a.T + 2 * kBM - 1) / (2 * kBM)) * tiles_n;
+  const int nk = (a.K + kBK - 1) / kBK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.acc_full[b], 1);
+      mbar_init(&sm.acc_empty[b], 2 * kPairEpiWarps);
+    }
+    mbar_init(&sm.done, 1);
+    sm.abort = 0;
+    sm.issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(&sm.tmem_base, 2 * kPairBN);
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_x);
+    prefetch_tmap(&tm_w);
+    prefetch_tmap(&tm_out);
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- TMA producer (both CTAs)
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < n_units; u += n_pairs) {
+        const int m0 = (u / tiles_n) * 2 * kBM + rank * kBM;
+        const int n0 = (u % tiles_n) * kPairBN + rank * (kPairBN / 2);
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kPairStages;
+          ok = mbar_wait(&sm.empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag, a.hdr, 31);
+          if (!ok) break;
+          if (leader) mbar_arrive_expect_tx(&sm.full[s], 4 * kPairStage);
+          tma_load_2d_pair(sm.x[s], &tm_x, &sm.full[s], kb * kBK, m0);
+          tma_load_2d_pair(sm.w[s], &tm_w, &sm.full[s], kb * kBK, n0);
+          sm.issued = it + 1;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (even CTA)
+    if (lane == 0 && leader) {
+      constexpr uint32_t idesc = idesc_i8(2 * kBM, kPairBN);
+      int it = 0, tc = 0;
+      bool ok = true;
+      for (int u = pair; ok && u < n_units; u += n_pairs, ++tc) {
+        const int b = tc & 1;
+        ok = mbar_wait(&sm.acc_empty[b], ((tc >> 1) & 1) ^ 1, abort_flag, a.hdr, 32);
+        if (!ok) break;
+        tc_fence_after();
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kPairStages;
+          ok = mbar_wait(&sm.full[s], (it / kPairStages) & 1, abort_flag, a.hdr, 33);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t xb = smem_u32(sm.x[s]), wb = smem_u32(sm.w[s]);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 32; ++kk)
+            mma_i8_pair(tmem + b * kPairBN, sw128_desc(xb + kk * 32, 16, 1024), sw128_desc(wb + kk * 32, 16, 1024),
+                        idesc, (kb | kk) != 0);
+          mma_commit_pair(&sm.empty[s]);
+        }
+        if (ok) mma_commit_pair(&sm.acc_full[b]);
+      }
+      mma_commit_pair(&sm.done);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    constexpr int kCols = 128 / (int)sizeof(TOut);   // columns of a box: 64 bf16 or 32 fp32
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const bool issuer = (warp == 2 || warp == 6) && lane == 0;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t empty_addr0 = map_shared(smem_u32(&sm.acc_empty[0]), 0);
+    const uint32_t empty_addr1 = map_shared(smem_u32(&sm.acc_empty[1]), 0);
+    int tc = 0, boxes = 0;
+    for (int u = pair; u < n_units; u += n_pairs, ++tc) {
+      const int b = tc & 1;
+      const int row0 = (u / tiles_n) * 2 * kBM + rank * kBM;
+      const int n0 = (u % tiles_n) * kPairBN;
+      // half the scale and bias where SiLU wants x / 2
+      const bool halved = sizeof(TOut) == 2 && a.silu;
+      float xs = row0 + r < a.T ? a.x_scale[row0 + r] : 0.f;
+      if (halved) xs *= 0.5f;
+      const uint64_t xs2 = pack2(xs, xs);
+      const float bf = halved ? 0.5f : 1.f;
+      const bool ok = half_all(mbar_wait(&sm.acc_full[b], (tc >> 1) & 1, abort_flag, a.hdr, 34), half);
+      if (!ok) break;
+      tc_fence_after();
+      // this half's boxes: 2 i + half
+#pragma unroll 1
+      for (int i = 0; i < kPairBN / kCols / 2; ++i, ++boxes) {
+        const int c0 = (2 * i + half) * kCols;
+        uint8_t* box = sm.out[half][boxes & 1];
+        // the store issued two boxes ago has read this buffer
+        if (boxes >= 2) {
+          if (issuer) bulk_wait_read1();
+          named_bar_sync(1 + half, 128);
+        }
+        const uint32_t dst = smem_u32(box) + r * 128;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t acc[32];
+          tmem_ld32(tmem + lane_base + b * kPairBN + c0 + c, acc);
+          tmem_wait_ld(acc);
+          if (i == kPairBN / kCols / 2 - 1 && c + 32 == kCols) {
+            // this warp's part of accumulator b is read: tell the even CTA's issuer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(b ? empty_addr1 : empty_addr0);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const int n = n0 + c0 + c + e;
+            float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0, b0 = w0, b1 = w0;
+            if (n < a.N) {  // N is a multiple of 8
+              w0 = __ldg(reinterpret_cast<const float4*>(a.w_scale + n));
+              w1 = __ldg(reinterpret_cast<const float4*>(a.w_scale + n + 4));
+              if (a.bias) {
+                b0 = __ldg(reinterpret_cast<const float4*>(a.bias + n));
+                b1 = __ldg(reinterpret_cast<const float4*>(a.bias + n + 4));
+              }
+            }
+            const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+              const uint64_t v2 = fma2(ints_to_float2(acc[e + k], acc[e + k + 1]),
+                                       mul2(xs2, pack2(wv[k], wv[k + 1])), pack2(bf * bv[k], bf * bv[k + 1]));
+              float v0, v1;
+              unpack2(v2, v0, v1);
+              if constexpr (sizeof(TOut) == 2) {
+                y[k] = a.silu ? fmaf(v0, tanh_approx(v0), v0) : v0;
+                y[k + 1] = a.silu ? fmaf(v1, tanh_approx(v1), v1) : v1;
+              } else {
+                y[k] = act_i8<TOut>(v0, a.silu);
+                y[k + 1] = act_i8<TOut>(v1, a.silu);
+              }
+            }
+            // 16-byte chunk j of the box row at j ^ (r & 7) (the store's 128-byte swizzle)
+            if constexpr (sizeof(TOut) == 2) {
+              const int j = (c + e) / 8;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((j ^ (r & 7)) << 4)),
+                           "r"(pack_bf16x2(y[0], y[1])), "r"(pack_bf16x2(y[2], y[3])), "r"(pack_bf16x2(y[4], y[5])),
+                           "r"(pack_bf16x2(y[6], y[7]))
+                           : "memory");
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; k += 4) {
+                const int j = (c + e + k) / 4;
+                asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((j ^ (r & 7)) << 4)), "f"(y[k]),
+                             "f"(y[k + 1]), "f"(y[k + 2]), "f"(y[k + 3])
+                             : "memory");
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(1 + half, 128);
+        if (issuer) {
+          if (n0 + c0 < a.N && row0 < a.T) tma_store_2d(&tm_out, box, n0 + c0, row0);  // rows and columns outside are dropped
+          bulk_commit();
+        }
+      }
+    }
+    if (issuer) bulk_wait_all();
+  }
+
+  // as in gemm_sm100.cu: every MMA completed and every copy into either CTA is
+  // accounted for before tensor memory is freed and either CTA exits
+  if (warp == 1 && lane == 0) mbar_wait(&sm.done, 0, nullptr, a.hdr, 38);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (leader && warp == 0 && lane == 0) {
+    const int mine = sm.issued;
+    const int peer = (int)ld_shared_cluster_u32(map_shared(smem_u32(&sm.issued), 1));
+    const int last = max(mine, peer);
+    for (int t = max(0, last - kPairStages); t < last; ++t) {
+      uint64_t* bar = &sm.full[t % kPairStages];
+      if (t < mine && t >= peer) mbar_complete_tx(bar, 2 * kPairStage);
+      if (t >= mine && t < peer) mbar_arrive_expect_tx(bar, 2 * kPairStage);
+      mbar_wait(bar, (t / kPairStages) & 1, nullptr, a.hdr, 39);
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 2 * kPairBN);
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -318,6 +636,8 @@ bool encode_codes(CUtensorMap* m, const void* base, long long rows, int K, int b
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+long long pair_units(long long T, int N) { return ((T + 2 * kBM - 1) / (2 * kBM)) * ((N + kPairBN - 1) / kPairBN); }
+
 template <int BN, typename TOut>
 cudaError_t launch_single(const GemmI8Args& a, const void* xq, const void* wq, int dev, cudaStream_t s) {
   constexpr size_t smem = sizeof(SmemI8<BN>) + 1024;
@@ -333,6 +653,50 @@ cudaError_t launch_single(const GemmI8Args& a, const void* xq, const void* wq, i
   const long long tiles = ((a.T + kBM - 1) / kBM) * ((a.N + BN - 1) / BN);
   gemm_i8_kernel<BN, TOut><<<(unsigned)tiles, kThreads, smem, s>>>(a, tx, tw);
   return cudaGetLastError();
+}
+
+// out [rows, N] with a row stride: box = 128 rows x 128 bytes, 128B swizzle
+bool encode_out(CUtensorMap* m, void* base, long long rows, int N, long long stride, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int es = bf16 ? 2 : 4;
+  cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(stride * es)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / es), (cuuint32_t)kBM};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename TOut>
+cudaError_t launch_pair(const GemmI8Args& a, const void* xq, const void* wq, int dev, int sms, cudaStream_t s) {
+  static unsigned long long attr_set = 0;  // one bit per device
+  if (!(attr_set & (1ull << dev))) {
+    cudaError_t e = cudaFuncSetAttribute(gemm_i8_pair_kernel<TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemPair);
+    if (e != cudaSuccess) return e;
+    attr_set |= 1ull << dev;
+  }
+  CUtensorMap tx, tw, to;
+  if (!encode_codes(&tx, xq, a.T, a.K, kBM) || !encode_codes(&tw, wq, a.N, a.K, kBM) ||
+      !encode_out(&to, a.out, a.T, a.N, a.out_stride, sizeof(TOut) == 2))
+    return cudaErrorInvalidValue;
+  const long long units = pair_units(a.T, a.N);
+  const int pairs = (int)std::max<long long>(1, std::min<long long>(units, sms / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kSmemPair;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<TOut>, a, tx, tw, to);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -417,8 +781,15 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   a.bias = bias;
   a.out = out;
   a.hdr = hdr;
-  const cudaError_t e = p->out_dtype == HSTU_DT_BF16 ? launch_single<128, __nv_bfloat16>(a, xq, w_q, dev, s)
-                                                     : launch_single<128, float>(a, xq, w_q, dev, s);
+  // 256 x 256 tiles on SM pairs once they fill most of the GPU; 128 x 128 tiles on
+  // single SMs below (four times as many)
+  cudaError_t e;
+  if (pair_units(p->rows, p->d_out) * 2 >= sms)
+    e = p->out_dtype == HSTU_DT_BF16 ? launch_pair<__nv_bfloat16>(a, xq, w_q, dev, sms, s)
+                                     : launch_pair<float>(a, xq, w_q, dev, sms, s);
+  else
+    e = p->out_dtype == HSTU_DT_BF16 ? launch_single<128, __nv_bfloat16>(a, xq, w_q, dev, s)
+                                     : launch_single<128, float>(a, xq, w_q, dev, s);
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
