@@ -2,13 +2,19 @@
 //
 // The pool has the paged layout of hstu_kv.cu with a row of d / 2 bytes for
 // each token and head and one (scale, zero) word beside it; the row format is
-// in quant_common.cuh.  Append = the plan of hstu_kv.cu (pages, new lengths)
-// and a kernel that quantises every appended token's K and V rows into their
-// slots; read = the same walk backwards, dense rows out.  Both move each row
-// once and are bound by the bytes of k_new / v_new (or of the dense output).
+// in quant_common.cuh.  Both kernels move each row once and are bound by the
+// bytes of k_new / v_new (or of the dense output).
 //
-// A group of G lanes owns a row (one token, one head, K or V): each lane holds
-// W words of 8 elements, the extremes meet in log2(G) shuffles.
+// A warp takes a token: G lanes hold a row (8 W elements each), so 32 / G heads
+// go at once, K and V of two such groups of heads together (four independent
+// 16-byte loads a lane); page and user are looked up once a token.
+//
+// Append is one launch for up to 256 users: every block works the allocation out
+// for itself (one user a thread, one block-wide scan) from lengths, table and
+// stack as they were, copies its tokens, and the block that finishes last writes
+// the new table entries, lengths and stack height.  Nothing is changed before every
+// block has read it, and nothing at all if the batch does not fit.  More users take
+// the plan launch of hstu_kv.cu first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,6 +31,9 @@ namespace hstu {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kFusedUsers = kRowThreads;
+constexpr int32_t kErrPool = -10;
 
 struct Q4Pool {
   uint8_t* k;
@@ -33,68 +42,184 @@ struct Q4Pool {
   uint32_t* v_meta;
 };
 
-// Quantises the appended tokens of user blockIdx.x into the pool.
+// The users of a batch as a block of the one-launch append sees them.
+struct FusedPlan {
+  int32_t off[kFusedUsers + 1];  // rows of k_new
+  int32_t old[kFusedUsers];      // cached tokens before
+  int32_t app[kFusedUsers];      // appended tokens
+  int32_t pre[kFusedUsers];      // pages taken by the users before
+  int32_t warp_sum[kRowWarps];
+  int32_t err, total, fc, last;
+};
+
+// The allocation of kv_append_plan_kernel (same checks, same order of pages), in shared memory.
+__device__ void plan_append(const KvArgs& a, FusedPlan& p) {
+  const int u = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (u == 0) {
+    p.err = 0;
+    p.fc = *a.free_count;
+  }
+  if (u <= a.B) p.off[u] = a.new_offsets[u];
+  if (u == 0 && a.B == kFusedUsers) p.off[a.B] = a.new_offsets[a.B];
+  __syncthreads();
+  int need = 0;
+  if (u < a.B) {
+    const int L = a.cached_lens[u], r0 = p.off[u], r1 = p.off[u + 1], n_new = r1 - r0;
+    const int app = a.num_append ? a.num_append[u] : n_new;
+    p.old[u] = L;
+    p.app[u] = app;
+    if (L < 0 || r0 < 0 || r1 > a.total_new || n_new < 0 || app < 0 || app > n_new) {
+      atomicCAS(&p.err, 0, kErrLength);
+    } else {
+      const long long have = ((long long)L + a.P - 1) / a.P, want = ((long long)L + app + a.P - 1) / a.P;
+      if (want > a.max_pages) {
+        atomicCAS(&p.err, 0, kErrPool);
+      } else {
+        need = (int)(want - have);
+        if (app > 0 && L % a.P != 0) {  // the partly filled last page receives tokens
+          const int pid = a.page_table[(size_t)u * a.max_pages + L / a.P];
+          if (pid < 0 || pid >= a.num_pages) atomicCAS(&p.err, 0, kErrPage);
+        }
+      }
+    }
+  }
+  int incl = need;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) p.warp_sum[warp] = incl;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kRowWarps; ++w) {
+    if (w < warp) before += p.warp_sum[w];
+    total += p.warp_sum[w];
+  }
+  if (u < a.B) p.pre[u] = before + incl - need;
+  if (u == 0) {
+    p.total = total;
+    if (p.err == 0 && (total > p.fc || p.fc > a.num_pages)) p.err = kErrPool;
+  }
+  __syncthreads();
+  if (p.err == 0)  // the pages about to be taken must be pool pages
+    for (int x = p.fc - total + u; x < p.fc; x += kRowThreads) {
+      const int pid = a.free_pages[x];
+      if (pid < 0 || pid >= a.num_pages) atomicCAS(&p.err, 0, kErrPage);
+    }
+  __syncthreads();
+}
+
+// largest u with off[u] <= row
+__device__ __forceinline__ int user_of(const int32_t* off, int B, int row) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Rows of one token (K and V, all heads) into slot rows slot0 + h * P of the pool.
 template <typename T, int G, int W>
-__global__ void __launch_bounds__(kRowThreads) kv_append_q4_kernel(const KvArgs a, const Q4Pool pool) {
-  if (a.hdr->pad[0] != 1) return;
-  const int u = blockIdx.x;
-  const int app = a.n_app[u];
-  if (app <= 0) return;
-  const int L = a.l_old[u];
-  const int row0 = a.new_offsets[u];
-  const int32_t* prow = a.page_table + (size_t)u * a.max_pages;
+__device__ __forceinline__ void quantise_token(const KvArgs& a, const Q4Pool& pool, int row, size_t page_row, int slot) {
+  const int lane = threadIdx.x & 31, g = lane % G;
   const int words = a.d / 8;
-  const int g = threadIdx.x % G;
-  constexpr int kRows = kRowThreads / G;  // rows per block and step
-  const long long items = 2ll * app * a.H;
-  for (long long base = (long long)blockIdx.y * kRows; base < items; base += (long long)gridDim.y * kRows) {
-    const long long it = base + threadIdx.x / G;
-    const bool on = it < items;  // all lanes stay for the shuffles
-    const int is_v = on && it >= (long long)app * a.H;
-    const int y = on ? (int)(it - (is_v ? (long long)app * a.H : 0)) : 0;
-    const int j = y / a.H, h = y - j * a.H;
-    const T* src = reinterpret_cast<const T*>(is_v ? a.v_new : a.k_new) + (size_t)(row0 + j) * a.kv_stride +
-                   (size_t)h * a.d;
-    float x[W][8];
-    float lo = 0.f, hi = 0.f;
-    uint32_t bits = 0;
+  constexpr int kHeads = 32 / G;
+  const size_t src0 = (size_t)row * a.kv_stride;
+  for (int h0 = lane / G; h0 - lane / G < a.H; h0 += 2 * kHeads) {
+    float x[2][2][W][8];  // [heads][K, V]
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const int wi = g + G * w;
-      if (on && wi < words) {
-        load8(src + 8 * wi, x[w]);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo = fminf(lo, x[w][e]);
-          hi = fmaxf(hi, x[w][e]);
-          bits = max(bits, __float_as_uint(x[w][e]) & 0x7FFFFFFFu);
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int h = h0 + i * kHeads, wi = g + G * w;
+          if (h < a.H && wi < words) {
+            load8(reinterpret_cast<const T*>(v ? a.v_new : a.k_new) + src0 + (size_t)h * a.d + 8 * wi, x[i][v][w]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[i][v][w][e] = 0.f;
+          }
+        }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float lo = 0.f, hi = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            lo = min_nan(lo, x[i][v][w][e]);
+            hi = max_nan(hi, x[i][v][w][e]);
+          }
+#pragma unroll
+        for (int o = G / 2; o >= 1; o >>= 1) {
+          lo = min_nan(lo, __shfl_xor_sync(~0u, lo, o));
+          hi = max_nan(hi, __shfl_xor_sync(~0u, hi, o));
+        }
+        const int h = h0 + i * kHeads;
+        if (h < a.H) {
+          const Quant4 f = quant4_of(lo, hi);
+          const size_t at = (page_row + h) * a.P + slot;
+          uint32_t* dst = reinterpret_cast<uint32_t*>((v ? pool.v : pool.k) + at * (a.d / 2));
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            if (g + G * w < words) dst[g + G * w] = quant4_word(f, x[i][v][w]);
+          if (g == 0) (v ? pool.v_meta : pool.k_meta)[at] = f.meta;
         }
       }
+  }
+}
+
+template <typename T, int G, int W, bool FUSED>
+__global__ void __launch_bounds__(kRowThreads) kv_append_q4_kernel(const KvArgs a, const Q4Pool pool) {
+  __shared__ FusedPlan p;
+  if constexpr (FUSED) {
+    plan_append(a, p);
+    if (p.err != 0) {  // the same in every block
+      if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.hdr, p.err, 0);
+      return;
     }
-#pragma unroll
-    for (int o = G / 2; o >= 1; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
-      bits = max(bits, __shfl_xor_sync(~0u, bits, o));
+  } else {
+    if (a.hdr->pad[0] != 1) return;
+  }
+  const int32_t* off = FUSED ? p.off : a.new_offsets;
+  const int32_t* app = FUSED ? p.app : a.n_app;
+  const int32_t* old = FUSED ? p.old : a.l_old;
+  const int end = off[a.B];
+  for (int row = off[0] + blockIdx.x * kRowWarps + (threadIdx.x >> 5); row < end; row += gridDim.x * kRowWarps) {
+    const int u = user_of(off, a.B, row), j = row - off[u];
+    if (j >= app[u]) continue;
+    const int pos = old[u] + j, page = pos / a.P;
+    int pid;
+    if constexpr (FUSED) {
+      const int have = (old[u] + a.P - 1) / a.P;
+      pid = page < have ? a.page_table[(size_t)u * a.max_pages + page] : a.free_pages[p.fc - 1 - p.pre[u] - (page - have)];
+    } else {
+      pid = a.page_table[(size_t)u * a.max_pages + page];
     }
-    if (!on) continue;
-    const Quant4 f = quant4_of(lo, hi, bits < 0x7F800000u);
-    const int pos = L + j;
-    const size_t slot = ((size_t)prow[pos / a.P] * a.H + h) * a.P + pos % a.P;
-    uint32_t* dst = reinterpret_cast<uint32_t*>((is_v ? pool.v : pool.k) + slot * (a.d / 2));
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const int wi = g + G * w;
-      if (wi < words) {
-        uint32_t word = 0;
-        if (f.live) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) word |= quant4_code(f, x[w][e]) << nibble_shift(e);
-        }
-        dst[wi] = word;
-      }
+    quantise_token<T, G, W>(a, pool, row, (size_t)pid * a.H, pos - page * a.P);
+  }
+  if constexpr (FUSED) {
+    // the block that is last to have read everything writes the new state
+    __syncthreads();
+    if (threadIdx.x == 0) p.last = atomicAdd(&a.hdr->blocks_done, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!p.last) return;
+    const int u = threadIdx.x;
+    if (u < a.B) {
+      const int have = (p.old[u] + a.P - 1) / a.P;
+      const int need = (int)(((long long)p.old[u] + p.app[u] + a.P - 1) / a.P) - have;
+      int32_t* row = a.page_table + (size_t)u * a.max_pages + have;
+      for (int j = 0; j < need; ++j) row[j] = a.free_pages[p.fc - 1 - p.pre[u] - j];
+      a.cached_lens[u] = p.old[u] + p.app[u];
     }
-    if (g == 0) (is_v ? pool.v_meta : pool.k_meta)[slot] = f.meta;
+    if (u == 0) *a.free_count = p.fc - p.total;
   }
 }
 
@@ -110,68 +235,102 @@ struct ReadArgs {
   WsHeader* hdr;
 };
 
-// One step of a thread: 8 elements of one row.  Rows are independent: a user
-// whose range or page is bad reports its error and its rows stay as they were.
-template <typename T>
+// Rows are independent: a user whose range or page is bad reports its error and
+// its rows stay as they were.
+template <typename T, int G, int W>
 __global__ void __launch_bounds__(kRowThreads) kv_read_q4_kernel(const ReadArgs a, const Q4Pool pool) {
+  const int lane = threadIdx.x & 31, g = lane % G;
   const int words = a.d / 8;
-  const long long per_token = (long long)a.H * words;
-  const long long items = (long long)a.total * per_token;
-  for (long long x = blockIdx.x * (long long)kRowThreads + threadIdx.x; x < 2 * items;
-       x += (long long)gridDim.x * kRowThreads) {
-    const bool is_v = x >= items;
-    const long long y = is_v ? x - items : x;
-    const int row = (int)(y / per_token);
-    const int rem = (int)(y - row * per_token);
-    const int h = rem / words, w = rem - h * words;
-    // user of the row: the last one whose rows start at or before it
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.offsets[mid] <= row) lo = mid;
-      else hi = mid - 1;
-    }
-    const int r0 = a.offsets[lo], r1 = a.offsets[lo + 1];
+  constexpr int kHeads = 32 / G;
+  for (int row = blockIdx.x * kRowWarps + (threadIdx.x >> 5); row < a.total; row += gridDim.x * kRowWarps) {
+    const int u = user_of(a.offsets, a.B, row);
+    const int r0 = a.offsets[u], r1 = a.offsets[u + 1];
     if (row < r0 || row >= r1) {
       // before the first user, behind the last, or offsets that decrease
-      if (a.offsets[0] != 0 || r1 < r0) report_error(a.hdr, kErrLength, lo);
+      if (lane == 0 && (a.offsets[0] != 0 || r1 < r0)) report_error(a.hdr, kErrLength, u);
       continue;
     }
-    const long long pos = (long long)a.starts[lo] + (row - r0);
-    if (pos < 0 || a.starts[lo] < 0 || pos >= a.cached_lens[lo] || pos / a.P >= a.max_pages) {
-      report_error(a.hdr, kErrLength, lo);
+    const long long pos = (long long)a.starts[u] + (row - r0);
+    const int page = (int)(pos / a.P);
+    if (a.starts[u] < 0 || pos >= a.cached_lens[u] || page >= a.max_pages) {
+      if (lane == 0) report_error(a.hdr, kErrLength, u);
       continue;
     }
-    const int pid = a.page_table[(size_t)lo * a.max_pages + pos / a.P];
+    const int pid = a.page_table[(size_t)u * a.max_pages + page];
     if (pid < 0 || pid >= a.num_pages) {
-      report_error(a.hdr, kErrPage, lo);
+      if (lane == 0) report_error(a.hdr, kErrPage, u);
       continue;
     }
-    const size_t slot = ((size_t)pid * a.H + h) * a.P + (int)(pos % a.P);
-    const uint32_t meta = (is_v ? pool.v_meta : pool.k_meta)[slot];
-    const uint32_t code = reinterpret_cast<const uint32_t*>((is_v ? pool.v : pool.k) + slot * (a.d / 2))[w];
-    const float s = meta_scale(meta), z = meta_zero(meta);
-    float v[8];
+    const int slot = (int)(pos - (long long)page * a.P);
+    for (int h0 = lane / G; h0 < a.H; h0 += 2 * kHeads) {
+      uint32_t meta[2][2], code[2][2][W];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = s * ((float)((code >> nibble_shift(e)) & 15u) - z);
-    T* out = static_cast<T*>(is_v ? a.v_out : a.k_out) + ((size_t)row * a.H + h) * a.d + 8 * w;
-    store8(out, v);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int h = h0 + i * kHeads;
+          const size_t at = ((size_t)pid * a.H + (h < a.H ? h : h0)) * a.P + slot;
+          meta[i][v] = (v ? pool.v_meta : pool.k_meta)[at];
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            code[i][v][w] = g + G * w < words
+                                ? reinterpret_cast<const uint32_t*>((v ? pool.v : pool.k) + at * (a.d / 2))[g + G * w]
+                                : 0u;
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int h = h0 + i * kHeads;
+          const float s = meta_scale(meta[i][v]), z = meta_zero(meta[i][v]);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            if (h >= a.H || g + G * w >= words) continue;
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)  // 2^23 + code, exact
+              y[e] = s * (__uint_as_float(((code[i][v][w] >> nibble_shift(e)) & 15u) | 0x4B000000u) - (8388608.f + z));
+            store8(static_cast<T*>(v ? a.v_out : a.k_out) + ((size_t)row * a.H + h) * a.d + 8 * (g + G * w), y);
+          }
+        }
+    }
   }
 }
 
-template <typename T, int G, int W>
-cudaError_t launch_append_q4(const KvArgs& a, const Q4Pool& pool, int parts, cudaStream_t s) {
-  kv_append_q4_kernel<T, G, W><<<dim3(a.B, parts), kRowThreads, 0, s>>>(a, pool);
-  return cudaGetLastError();
+// lanes of a row and words of a lane for a head size
+template <template <int, int> class F, typename... Args>
+cudaError_t by_head_dim(int d, Args&&... args) {
+  if (d <= 32) return F<4, 1>::run(args...);
+  if (d <= 64) return F<8, 1>::run(args...);
+  if (d <= 128) return F<16, 1>::run(args...);
+  return F<16, 2>::run(args...);
 }
 
-template <typename T>
-cudaError_t launch_append_q4(const KvArgs& a, const Q4Pool& pool, int parts, cudaStream_t s) {
-  if (a.d <= 32) return launch_append_q4<T, 4, 1>(a, pool, parts, s);
-  if (a.d <= 64) return launch_append_q4<T, 8, 1>(a, pool, parts, s);
-  if (a.d <= 128) return launch_append_q4<T, 16, 1>(a, pool, parts, s);
-  return launch_append_q4<T, 16, 2>(a, pool, parts, s);
-}
+template <int G, int W>
+struct Append {
+  static cudaError_t run(const KvArgs& a, const Q4Pool& pool, bool bf16, bool fused, int blocks, cudaStream_t s) {
+    if (fused) {
+      if (bf16) kv_append_q4_kernel<__nv_bfloat16, G, W, true><<<blocks, kRowThreads, 0, s>>>(a, pool);
+      else kv_append_q4_kernel<float, G, W, true><<<blocks, kRowThreads, 0, s>>>(a, pool);
+    } else {
+      if (bf16) kv_append_q4_kernel<__nv_bfloat16, G, W, false><<<blocks, kRowThreads, 0, s>>>(a, pool);
+      else kv_append_q4_kernel<float, G, W, false><<<blocks, kRowThreads, 0, s>>>(a, pool);
+    }
+    return cudaGetLastError();
+  }
+};
+
+template <int G, int W>
+struct Read {
+  static cudaError_t run(const ReadArgs& a, const Q4Pool& pool, bool bf16, int blocks, cudaStream_t s) {
+    if (bf16) kv_read_q4_kernel<__nv_bfloat16, G, W><<<blocks, kRowThreads, 0, s>>>(a, pool);
+    else kv_read_q4_kernel<float, G, W><<<blocks, kRowThreads, 0, s>>>(a, pool);
+    return cudaGetLastError();
+  }
+};
+
+// a warp a token, up to 16 blocks of 8 warps an SM
+int row_blocks(int rows) { return std::max(1, std::min((rows + kRowWarps - 1) / kRowWarps, 148 * 16)); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -237,12 +396,15 @@ int hstu_kv_append_q4(const hstu_kv_params* p, const void* k_new, const void* v_
   const Q4Pool pool{static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), static_cast<uint32_t*>(k_scales),
                     static_cast<uint32_t*>(v_scales)};
   if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (launch_kv_append_plan(a, s) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (p->total_new == 0) return HSTU_OK;
-  const int parts = 8;
-  const cudaError_t e = p->dtype == HSTU_DT_BF16 ? launch_append_q4<__nv_bfloat16>(a, pool, parts, s)
-                                                 : launch_append_q4<float>(a, pool, parts, s);
-  return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  const bool fused = p->batch <= kFusedUsers;
+  if (!fused) {
+    if (launch_kv_append_plan(a, s) != cudaSuccess) return HSTU_ERR_CUDA;
+    if (p->total_new == 0) return HSTU_OK;
+  }
+  return by_head_dim<Append>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, fused, row_blocks(p->total_new), s) ==
+                 cudaSuccess
+             ? HSTU_OK
+             : HSTU_ERR_CUDA;
 }
 
 int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_pool, const void* k_scales,
@@ -278,13 +440,9 @@ int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_p
   const Q4Pool pool{static_cast<uint8_t*>(const_cast<void*>(k_pool)), static_cast<uint8_t*>(const_cast<void*>(v_pool)),
                     static_cast<uint32_t*>(const_cast<void*>(k_scales)),
                     static_cast<uint32_t*>(const_cast<void*>(v_scales))};
-  const long long steps = 2ll * p->total_new * p->num_heads * (p->head_dim / 8);
-  const int blocks = (int)std::min<long long>((steps + kRowThreads - 1) / kRowThreads, 148 * 16);
-  if (p->dtype == HSTU_DT_BF16)
-    kv_read_q4_kernel<__nv_bfloat16><<<blocks, kRowThreads, 0, s>>>(a, pool);
-  else
-    kv_read_q4_kernel<float><<<blocks, kRowThreads, 0, s>>>(a, pool);
-  return cudaGetLastError() == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+  return by_head_dim<Read>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, row_blocks(p->total_new), s) == cudaSuccess
+             ? HSTU_OK
+             : HSTU_ERR_CUDA;
 }
 
 }  // extern "C"

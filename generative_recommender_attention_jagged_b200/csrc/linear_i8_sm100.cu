@@ -27,8 +27,12 @@ namespace {
 constexpr size_t kHeaderBytes = sizeof(WsHeader);
 
 // ---- quantise rows ------------------------------------------------------------
-constexpr int kRowRegs = 4;  // a warp keeps up to 4 x 256 elements of its row in registers
+// A warp a row (two rows of up to 512 elements at once, so that one row's loads
+// cover the other's reduction); rows of up to 1024 elements stay in registers, longer
+// ones are read twice (the second time from L1 or L2).
+constexpr int kRowRegs = 4;  // 4 x 256 elements
 
+// the largest absolute value's bits (a NaN or infinity is above every finite one)
 __device__ __forceinline__ uint32_t abs_bits_max(const float (&x)[8], uint32_t m) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
@@ -37,55 +41,145 @@ __device__ __forceinline__ uint32_t abs_bits_max(const float (&x)[8], uint32_t m
 
 // 8 codes as 8 bytes
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv) {
-  uint32_t m[8];
+  float m[8];
+  round_quotients8(x, s, inv, m);
+  uint32_t u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m[i] = __float_as_uint(round_quotient(x[i], s, inv));
-  const uint32_t a = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410);
-  const uint32_t b = __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410);
+  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(m[i]);
+  const uint32_t a = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+  const uint32_t b = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
   return make_uint2(a, b);
 }
 
+// 8 elements as they lie
 template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t amax(uint32_t m) const {
+    uint32_t p = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    return max(m, max(p & 0xFFFF0000u, p << 16));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float x_[8];
+  __device__ __forceinline__ void load(const float* p) { load8(p, x_); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x_[i] = 0.f;
+  }
+  __device__ __forceinline__ uint32_t amax(uint32_t m) const { return abs_bits_max(x_, m); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x_[i];
+  }
+};
+
+struct RowScale {
+  float s, inv;
+  bool live;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits, float* out) {
+  RowScale f;
+  const bool finite = amax_bits < 0x7F800000u;
+  f.s = __fdiv_rn(__uint_as_float(amax_bits), 127.f);
+  f.live = finite && f.s >= FLT_MIN;
+  f.inv = f.live ? 1.f / f.s : 0.f;
+  if (out) *out = f.live ? f.s : (finite ? 0.f : __uint_as_float(0x7FC00000u));
+  return f;
+}
+
+// R rows of a warp at once, up to 256 REGS elements of each in registers (LONG: the rest is read again)
+template <typename T, int R, int REGS, bool LONG>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, long long rows, int cols,
                                                          long long x_stride, int8_t* __restrict__ xq,
                                                          float* __restrict__ scale, WsHeader* hdr) {
   if (blockIdx.x == 0 && threadIdx.x < sizeof(WsHeader) / 4) reinterpret_cast<int32_t*>(hdr)[threadIdx.x] = 0;
   const int lane = threadIdx.x & 31;
-  for (long long r = blockIdx.x * 8ll + (threadIdx.x >> 5); r < rows; r += gridDim.x * 8ll) {
-    const T* row = x + r * x_stride;
-    float keep[kRowRegs][8];
-    uint32_t amax_bits = 0;
+  const long long step = gridDim.x * 8ll * R;
+  for (long long r0 = (blockIdx.x * 8ll + (threadIdx.x >> 5)) * R; r0 < rows; r0 += step) {
+    Raw8<T> keep[R][REGS];
+    uint32_t amax[R];
 #pragma unroll
-    for (int j = 0; j < kRowRegs; ++j) {
-      const int c = 256 * j + 8 * lane;
-      if (c < cols) {
-        load8(row + c, keep[j]);
-        amax_bits = abs_bits_max(keep[j], amax_bits);
+    for (int i = 0; i < R; ++i) {
+      const T* row = x + min(r0 + i, rows - 1) * x_stride;
+#pragma unroll
+      for (int j = 0; j < REGS; ++j) {
+        const int c = 256 * j + 8 * lane;
+        if (c < cols) keep[i][j].load(row + c);
+        else keep[i][j].zero();
       }
     }
-    for (int c = 256 * kRowRegs + 8 * lane; c < cols; c += 256) {
-      float v[8];
-      load8(row + c, v);
-      amax_bits = abs_bits_max(v, amax_bits);
-    }
-    amax_bits = __reduce_max_sync(~0u, amax_bits);
-    const bool finite = amax_bits < 0x7F800000u;
-    float s = __fdiv_rn(__uint_as_float(amax_bits), 127.f);
-    const bool live = finite && s >= FLT_MIN;
-    const float inv = live ? 1.f / s : 0.f;
-    if (lane == 0) scale[r] = live ? s : (finite ? 0.f : __uint_as_float(0x7FC00000u));
-    int8_t* out = xq + r * cols;
 #pragma unroll
-    for (int j = 0; j < kRowRegs; ++j) {
-      const int c = 256 * j + 8 * lane;
-      if (c < cols) *reinterpret_cast<uint2*>(out + c) = live ? codes8(keep[j], s, inv) : make_uint2(0, 0);
+    for (int i = 0; i < R; ++i) {
+      amax[i] = 0;
+#pragma unroll
+      for (int j = 0; j < REGS; ++j) amax[i] = keep[i][j].amax(amax[i]);
+      if constexpr (LONG) {
+        const T* row = x + min(r0 + i, rows - 1) * x_stride;
+#pragma unroll 4
+        for (int c = 256 * REGS + 8 * lane; c < cols; c += 256) {
+          Raw8<T> v;
+          v.load(row + c);
+          amax[i] = v.amax(amax[i]);
+        }
+      }
+      amax[i] = __reduce_max_sync(~0u, amax[i]);
     }
-    for (int c = 256 * kRowRegs + 8 * lane; c < cols; c += 256) {
-      float v[8];
-      load8(row + c, v);
-      *reinterpret_cast<uint2*>(out + c) = live ? codes8(v, s, inv) : make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (r0 + i >= rows) break;
+      const RowScale f = row_scale(amax[i], lane == 0 ? scale + r0 + i : nullptr);
+      int8_t* out = xq + (r0 + i) * cols;
+#pragma unroll
+      for (int j = 0; j < REGS; ++j) {
+        const int c = 256 * j + 8 * lane;
+        if (c < cols) {
+          float v[8];
+          keep[i][j].get(v);
+          *reinterpret_cast<uint2*>(out + c) = f.live ? codes8(v, f.s, f.inv) : make_uint2(0, 0);
+        }
+      }
+      if constexpr (LONG) {
+        const T* row = x + (r0 + i) * x_stride;
+#pragma unroll 4
+        for (int c = 256 * REGS + 8 * lane; c < cols; c += 256) {
+          float v[8];
+          load8(row + c, v);
+          *reinterpret_cast<uint2*>(out + c) = f.live ? codes8(v, f.s, f.inv) : make_uint2(0, 0);
+        }
+      }
     }
   }
+}
+
+template <typename T>
+cudaError_t launch_quant_rows(const void* x, long long rows, int cols, long long stride, int8_t* xq, float* scale,
+                              WsHeader* hdr, int sms, cudaStream_t s) {
+  const T* p = static_cast<const T*>(x);
+  if (cols <= 512) {
+    const unsigned blocks = (unsigned)std::min<long long>((rows + 15) / 16, (long long)sms * 16);
+    quant_rows_kernel<T, 2, 2, false><<<blocks, 256, 0, s>>>(p, rows, cols, stride, xq, scale, hdr);
+  } else {
+    const unsigned blocks = (unsigned)std::min<long long>((rows + 7) / 8, (long long)sms * 16);
+    if (cols <= 256 * kRowRegs)
+      quant_rows_kernel<T, 1, kRowRegs, false><<<blocks, 256, 0, s>>>(p, rows, cols, stride, xq, scale, hdr);
+    else
+      quant_rows_kernel<T, 1, kRowRegs, true><<<blocks, 256, 0, s>>>(p, rows, cols, stride, xq, scale, hdr);
+  }
+  return cudaGetLastError();
 }
 
 // ---- quantise a weight: w [K, N] -> wq [N, K], one scale a channel -------------
@@ -303,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // is done on the other pipes: the halves of the int32 go into the mantissa of 2^23
 // (exact), 65536 hi + lo is one rounded FMA, and the multiplications are packed in
 // pairs.  Each half of the epilogue (4 warps) has its own two staging boxes.
-constexpr int kPairStages = 5;
+constexpr int kPairStages = 4;
 constexpr int kPairStage = kBM * kBK;   // 16 KB: this CTA's 128 rows of x, or 128 channels of w
 constexpr int kPairEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
@@ -314,6 +408,7 @@ struct __align__(1024) SmemPair {
   uint8_t x[kPairStages][kPairStage];
   uint8_t w[kPairStages][kPairStage];
   uint8_t out[2][2][kBox];              // [half][in turn]
+  float wscale[2][kPairBN], bias[2][kPairBN];
   uint64_t full[kPairStages];           // even CTA: both CTAs' bytes of the stage landed
   uint64_t empty[kPairStages];          // both CTAs: the MMAs that read the stage completed
   uint64_t acc_full[2];
@@ -390,7 +485,7 @@ __device__ __forceinline__ uint64_t ints_to_float2(uint32_t a, uint32_t b) {
   return fma2(h, pack2(65536.f, 65536.f), add2(lo, pack2(-8388608.f, -8388608.f)));
 }
 
-template <typename TOut>
+template <typename TOut, bool SILU>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_i8_pair_kernel(const GemmI8Args a, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_out) {
@@ -481,7 +576,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     constexpr int kCols = 128 / (int)sizeof(TOut);   // columns of a box: 64 bf16 or 32 fp32
+    constexpr bool kBf16 = sizeof(TOut) == 2;
+    constexpr float kFactor = kBf16 && SILU ? 0.5f : 1.f;  // half of x where SiLU wants x / 2
     const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int te = threadIdx.x - 64 - 128 * half;    // thread of the half
     const bool issuer = (warp == 2 || warp == 6) && lane == 0;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -492,89 +590,91 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int b = tc & 1;
       const int row0 = (u / tiles_n) * 2 * kBM + rank * kBM;
       const int n0 = (u % tiles_n) * kPairBN;
-      // half the scale and bias where SiLU wants x / 2
-      const bool halved = sizeof(TOut) == 2 && a.silu;
-      float xs = row0 + r < a.T ? a.x_scale[row0 + r] : 0.f;
-      if (halved) xs *= 0.5f;
+      const float xs = kFactor * (row0 + r < a.T ? a.x_scale[row0 + r] : 0.f);
       const uint64_t xs2 = pack2(xs, xs);
-      const float bf = halved ? 0.5f : 1.f;
+      // the tile's scales and biases, a copy for each half (the barrier of the last tile's last box is behind its reads)
+      float(&ws)[kPairBN] = sm.wscale[half];
+      float(&bs)[kPairBN] = sm.bias[half];
+#pragma unroll
+      for (int c = te; c < kPairBN; c += 128) {
+        const int n = n0 + c;
+        ws[c] = n < a.N ? __ldg(a.w_scale + n) : 0.f;
+        bs[c] = n < a.N && a.bias ? kFactor * __ldg(a.bias + n) : 0.f;
+      }
       const bool ok = half_all(mbar_wait(&sm.acc_full[b], (tc >> 1) & 1, abort_flag, a.hdr, 34), half);
       if (!ok) break;
       tc_fence_after();
-      // this half's boxes: 2 i + half
-#pragma unroll 1
-      for (int i = 0; i < kPairBN / kCols / 2; ++i, ++boxes) {
-        const int c0 = (2 * i + half) * kCols;
+      constexpr int kChunks = kPairBN / 2 / 32;  // 32-column chunks of this half: box 2 i + half holds kCols / 32 of them
+      auto column = [&](int x) { return (2 * (x / (kCols / 32)) + half) * kCols + 32 * (x % (kCols / 32)); };
+      uint32_t acc[2][32];
+      tmem_ld32(tmem + lane_base + b * kPairBN + column(0), acc[0]);
+#pragma unroll
+      for (int x = 0; x < kChunks; ++x) {
+        const int c0 = column(x);
         uint8_t* box = sm.out[half][boxes & 1];
-        // the store issued two boxes ago has read this buffer
-        if (boxes >= 2) {
+        if (x % (kCols / 32) == 0 && boxes >= 2) {
+          // the store issued two boxes ago has read this buffer
           if (issuer) bulk_wait_read1();
           named_bar_sync(1 + half, 128);
         }
+        tmem_wait_ld(acc[x & 1]);
+        if (x + 1 < kChunks) {
+          tmem_ld32(tmem + lane_base + b * kPairBN + column(x + 1), acc[(x + 1) & 1]);
+        } else {
+          // this warp's part of accumulator b is read: tell the even CTA's issuer
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(b ? empty_addr1 : empty_addr0);
+        }
         const uint32_t dst = smem_u32(box) + r * 128;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t acc[32];
-          tmem_ld32(tmem + lane_base + b * kPairBN + c0 + c, acc);
-          tmem_wait_ld(acc);
-          if (i == kPairBN / kCols / 2 - 1 && c + 32 == kCols) {
-            // this warp's part of accumulator b is read: tell the even CTA's issuer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(b ? empty_addr1 : empty_addr0);
-          }
+        for (int e = 0; e < 32; e += 8) {
+          float y[8];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            const int n = n0 + c0 + c + e;
-            float4 w0 = make_float4(0.f, 0.f, 0.f, 0.f), w1 = w0, b0 = w0, b1 = w0;
-            if (n < a.N) {  // N is a multiple of 8
-              w0 = __ldg(reinterpret_cast<const float4*>(a.w_scale + n));
-              w1 = __ldg(reinterpret_cast<const float4*>(a.w_scale + n + 4));
-              if (a.bias) {
-                b0 = __ldg(reinterpret_cast<const float4*>(a.bias + n));
-                b1 = __ldg(reinterpret_cast<const float4*>(a.bias + n + 4));
-              }
-            }
-            const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-            const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-            float y[8];
+          for (int k = 0; k < 8; k += 4) {
+            const float4 wv = *reinterpret_cast<const float4*>(&ws[c0 + e + k]);
+            const float4 bv = *reinterpret_cast<const float4*>(&bs[c0 + e + k]);
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-              const uint64_t v2 = fma2(ints_to_float2(acc[e + k], acc[e + k + 1]),
-                                       mul2(xs2, pack2(wv[k], wv[k + 1])), pack2(bf * bv[k], bf * bv[k + 1]));
+            for (int q = 0; q < 4; q += 2) {
+              const uint32_t i0 = acc[x & 1][e + k + q], i1 = acc[x & 1][e + k + q + 1];
+              // without tanh the special-function unit is free for the conversion
+              const uint64_t f2 = SILU ? ints_to_float2(i0, i1) : pack2(__int2float_rn((int)i0), __int2float_rn((int)i1));
+              const uint64_t v2 = fma2(f2, mul2(xs2, q ? pack2(wv.z, wv.w) : pack2(wv.x, wv.y)),
+                                       q ? pack2(bv.z, bv.w) : pack2(bv.x, bv.y));
               float v0, v1;
               unpack2(v2, v0, v1);
-              if constexpr (sizeof(TOut) == 2) {
-                y[k] = a.silu ? fmaf(v0, tanh_approx(v0), v0) : v0;
-                y[k + 1] = a.silu ? fmaf(v1, tanh_approx(v1), v1) : v1;
+              if constexpr (SILU && kBf16) {
+                unpack2(fma2(v2, pack2(tanh_approx(v0), tanh_approx(v1)), v2), y[k + q], y[k + q + 1]);
               } else {
-                y[k] = act_i8<TOut>(v0, a.silu);
-                y[k + 1] = act_i8<TOut>(v1, a.silu);
-              }
-            }
-            // 16-byte chunk j of the box row at j ^ (r & 7) (the store's 128-byte swizzle)
-            if constexpr (sizeof(TOut) == 2) {
-              const int j = (c + e) / 8;
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((j ^ (r & 7)) << 4)),
-                           "r"(pack_bf16x2(y[0], y[1])), "r"(pack_bf16x2(y[2], y[3])), "r"(pack_bf16x2(y[4], y[5])),
-                           "r"(pack_bf16x2(y[6], y[7]))
-                           : "memory");
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; k += 4) {
-                const int j = (c + e + k) / 4;
-                asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((j ^ (r & 7)) << 4)), "f"(y[k]),
-                             "f"(y[k + 1]), "f"(y[k + 2]), "f"(y[k + 3])
-                             : "memory");
+                y[k + q] = SILU ? act_i8<TOut>(v0, 1) : v0;
+                y[k + q + 1] = SILU ? act_i8<TOut>(v1, 1) : v1;
               }
             }
           }
+          // 16-byte chunk j of the box row at j ^ (r & 7) (the store's 128-byte swizzle)
+          const int j0 = (x % (kCols / 32)) * 32 + e;
+          if constexpr (kBf16) {
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (((j0 / 8) ^ (r & 7)) << 4)),
+                         "r"(pack_bf16x2(y[0], y[1])), "r"(pack_bf16x2(y[2], y[3])), "r"(pack_bf16x2(y[4], y[5])),
+                         "r"(pack_bf16x2(y[6], y[7]))
+                         : "memory");
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4)
+              asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(dst + ((((j0 + k) / 4) ^ (r & 7)) << 4)),
+                           "f"(y[k]), "f"(y[k + 1]), "f"(y[k + 2]), "f"(y[k + 3])
+                           : "memory");
+          }
         }
-        fence_proxy_async_smem();
-        named_bar_sync(1 + half, 128);
-        if (issuer) {
-          if (n0 + c0 < a.N && row0 < a.T) tma_store_2d(&tm_out, box, n0 + c0, row0);  // rows and columns outside are dropped
-          bulk_commit();
+        if ((x + 1) % (kCols / 32) == 0) {
+          fence_proxy_async_smem();
+          named_bar_sync(1 + half, 128);
+          if (issuer) {
+            const int c = n0 + c0 + 32 - kCols;
+            if (c < a.N && row0 < a.T) tma_store_2d(&tm_out, box, c, row0);  // rows and columns outside are dropped
+            bulk_commit();
+          }
+          ++boxes;
         }
       }
     }
@@ -669,11 +769,11 @@ bool encode_out(CUtensorMap* m, void* base, long long rows, int N, long long str
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename TOut>
+template <typename TOut, bool SILU>
 cudaError_t launch_pair(const GemmI8Args& a, const void* xq, const void* wq, int dev, int sms, cudaStream_t s) {
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_i8_pair_kernel<TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(gemm_i8_pair_kernel<TOut, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemPair);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
@@ -696,7 +796,7 @@ cudaError_t launch_pair(const GemmI8Args& a, const void* xq, const void* wq, int
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<TOut>, a, tx, tw, to);
+  return cudaLaunchKernelEx(&cfg, gemm_i8_pair_kernel<TOut, SILU>, a, tx, tw, to);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -764,12 +864,10 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   float* xscale = reinterpret_cast<float*>(ws + kHeaderBytes + round256((size_t)p->rows * p->d_in));
   WsHeader* hdr = static_cast<WsHeader*>(workspace);
   const long long xs = p->x_stride ? p->x_stride : p->d_in;
-  const int blocks = (int)std::min<long long>((p->rows + 7) / 8, (long long)sms * 8);
-  if (p->dtype == HSTU_DT_BF16)
-    quant_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), p->rows, p->d_in, xs, xq, xscale, hdr);
-  else
-    quant_rows_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(x), p->rows, p->d_in, xs, xq, xscale, hdr);
-  if (cudaGetLastError() != cudaSuccess) return HSTU_ERR_CUDA;
+  if ((p->dtype == HSTU_DT_BF16 ? launch_quant_rows<__nv_bfloat16>(x, p->rows, p->d_in, xs, xq, xscale, hdr, sms, s)
+                                : launch_quant_rows<float>(x, p->rows, p->d_in, xs, xq, xscale, hdr, sms, s)) !=
+      cudaSuccess)
+    return HSTU_ERR_CUDA;
   GemmI8Args a;
   a.T = p->rows;
   a.K = p->d_in;
@@ -785,8 +883,10 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   // single SMs below (four times as many)
   cudaError_t e;
   if (pair_units(p->rows, p->d_out) * 2 >= sms)
-    e = p->out_dtype == HSTU_DT_BF16 ? launch_pair<__nv_bfloat16>(a, xq, w_q, dev, sms, s)
-                                     : launch_pair<float>(a, xq, w_q, dev, sms, s);
+    e = p->out_dtype == HSTU_DT_BF16
+            ? (a.silu ? launch_pair<__nv_bfloat16, true>(a, xq, w_q, dev, sms, s)
+                      : launch_pair<__nv_bfloat16, false>(a, xq, w_q, dev, sms, s))
+            : (a.silu ? launch_pair<float, true>(a, xq, w_q, dev, sms, s) : launch_pair<float, false>(a, xq, w_q, dev, sms, s));
   else
     e = p->out_dtype == HSTU_DT_BF16 ? launch_single<128, __nv_bfloat16>(a, xq, w_q, dev, s)
                                      : launch_single<128, float>(a, xq, w_q, dev, s);

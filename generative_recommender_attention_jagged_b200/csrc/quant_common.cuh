@@ -31,18 +31,53 @@ constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an
 
 // x / s rounded to the nearest integer, ties to even, for |x / s| < 2^21, as
 // kRoundMagic + integer (its low bits are the integer in two's complement).
-// inv ~ 1 / s puts the first guess within one of the answer; the remainder
-// x - q s is exact in one FMA (a multiple of the smaller ulp, no larger than
-// about s), so the comparison with s / 2 decides exactly, whatever the error
-// of inv.  Six operations against the ~10 of an IEEE division, and exact at
-// ties, where a rounded quotient is not.
-__device__ __forceinline__ float round_quotient(float x, float s, float inv) {
-  float m = fmaf(x, inv, kRoundMagic);
-  const float t = 2.f * fmaf(-(m - kRoundMagic), s, x);
+// The first guess m = rint(x inv) with inv ~ 1 / s is within one of the answer,
+// and the remainder x - q s is exact in one FMA (a multiple of the smaller ulp,
+// no larger than about s): while it is below s / 2 the guess stands, whatever
+// the error of inv, and otherwise (a tie, or a quotient so near one that inv's
+// error decided) fix_quotient compares exactly.  A rounded quotient is not exact
+// at ties; an IEEE division costs more than guess and test together (three FMA
+// pipe operations and one comparison).
+__device__ __forceinline__ float guess_quotient(float x, float inv) { return fmaf(x, inv, kRoundMagic); }
+// twice the remainder of the guess m
+__device__ __forceinline__ float twice_rest(float x, float s, float m) {
+  return 2.f * fmaf(kRoundMagic - m, s, x);
+}
+__device__ __forceinline__ float fix_quotient(float x, float s, float m) {
+  const float t = twice_rest(x, s, m);
   const bool odd = __float_as_int(m) & 1;
   if (t > s || (odd && t == s)) m += 1.f;
   if (t < -s || (odd && t == -s)) m -= 1.f;
   return m;
+}
+__device__ __forceinline__ float round_quotient(float x, float s, float inv) {
+  return fix_quotient(x, s, guess_quotient(x, inv));
+}
+
+// rounded quotients of 8 elements, as round_quotient
+__device__ __forceinline__ void round_quotients8(const float (&x)[8], float s, float inv, float (&m)[8]) {
+  bool stands = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] = guess_quotient(x[i], inv);
+    stands = stands && fabsf(fmaf(kRoundMagic - m[i], s, x[i])) < 0.5f * s;
+  }
+  if (!stands) {  // about one element in a thousand
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fix_quotient(x[i], s, m[i]);
+  }
+}
+
+// smallest and largest, NaN if either is NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 struct Quant4 {
@@ -50,26 +85,42 @@ struct Quant4 {
   float z;        // zero point 0..15
   uint32_t meta;  // the stored word: scale | zero << 16 (bf16 bits)
   bool live;      // codes are not all zero
+  bool clamp;     // an end of the row rounds to a code outside 0..15
 };
 
-// Format of a row with extremes lo <= 0 <= hi; `finite`: no infinity or NaN in it.
-__device__ __forceinline__ Quant4 quant4_of(float lo, float hi, bool finite) {
+// Format of a row with extremes lo <= 0 <= hi (NaN if an element is).
+__device__ __forceinline__ Quant4 quant4_of(float lo, float hi) {
   Quant4 f;
   const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
   f.s = __bfloat162float(sb);
-  const bool nan = !finite || f.s > FLT_MAX;
+  const bool nan = !(f.s <= FLT_MAX);  // an infinity, a NaN or a range beyond fp32
   f.live = !nan && f.s >= FLT_MIN;
   f.inv = f.live ? 1.f / f.s : 0.f;
   f.z = f.live ? fminf(round_quotient(-lo, f.s, f.inv) - kRoundMagic, 15.f) : 0.f;
+  f.clamp = f.live && (round_quotient(lo, f.s, f.inv) - kRoundMagic + f.z < 0.f ||
+                       round_quotient(hi, f.s, f.inv) - kRoundMagic + f.z > 15.f);
   const uint32_t sbits = f.live ? (uint32_t)__bfloat16_as_ushort(sb) : (nan ? 0x7FC0u : 0u);
   f.meta = sbits | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.z)) << 16);
   return f;
 }
 
-// code 0..15 of x
-__device__ __forceinline__ uint32_t quant4_code(const Quant4& f, float x) {
-  const float q = round_quotient(x, f.s, f.inv) - kRoundMagic + f.z;
-  return (uint32_t)__float2int_rn(fminf(fmaxf(q, 0.f), 15.f));
+// The word of 8 elements.  The codes are put together as fp32 sums of
+// code * 16^i (at most 65535, exact), four to a half of the word.
+__device__ __forceinline__ uint32_t quant4_word(const Quant4& f, const float (&x)[8]) {
+  if (!f.live) return 0;
+  float m[8];
+  round_quotients8(x, f.s, f.inv, m);
+  if (f.clamp) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fminf(fmaxf(m[i], kRoundMagic - f.z), kRoundMagic + 15.f - f.z);
+  }
+  float even = f.z * 4369.f, odd = even;  // 0x1111
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    even = fmaf(m[2 * i] - kRoundMagic, (float)(1 << (4 * i)), even);
+    odd = fmaf(m[2 * i + 1] - kRoundMagic, (float)(1 << (4 * i)), odd);
+  }
+  return __byte_perm(__float_as_uint(even + 8388608.f), __float_as_uint(odd + 8388608.f), 0x5410);
 }
 
 // scale and zero point of a stored word
