@@ -130,49 +130,53 @@ __device__ __forceinline__ void quantise_token(const KvArgs& a, const Q4Pool& po
   constexpr int kHeads = 32 / G;
   const size_t src0 = (size_t)row * a.kv_stride;
   for (int h0 = lane / G; h0 - lane / G < a.H; h0 += 2 * kHeads) {
-    float x[2][2][W][8];  // [heads][K, V]
+    Elems8<T> x[4][W];  // rows: K, V of the first heads, K, V of the second
+    float lo = 0.f, hi = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int v = 0; v < 2; ++v)
+      for (int w = 0; w < W; ++w) {
+        const int h = h0 + (i >> 1) * kHeads, wi = g + G * w;
+        if (h < a.H && wi < words)
+          x[i][w].load(reinterpret_cast<const T*>(i & 1 ? a.v_new : a.k_new) + src0 + (size_t)h * a.d + 8 * wi);
+        else
+          x[i][w].zero();
+      }
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const int h = h0 + i * kHeads, wi = g + G * w;
-          if (h < a.H && wi < words) {
-            load8(reinterpret_cast<const T*>(v ? a.v_new : a.k_new) + src0 + (size_t)h * a.d + 8 * wi, x[i][v][w]);
-          } else {
+    for (int i = 0; i < 4; ++i) {
+      auto ex = x[i][0].extremes();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[i][v][w][e] = 0.f;
-          }
-        }
+      for (int w = 1; w < W; ++w) ex = Elems8<T>::join(ex, x[i][w].extremes());
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int o = G / 2; o >= 1; o >>= 1) ex = Elems8<T>::join(ex, Elems8<T>::other(ex, o));
+      if ((lane & 3) == i) {  // lane i of a group of four works row i's format out for all
+        lo = Elems8<T>::lowest(ex);
+        hi = Elems8<T>::highest(ex);
+      }
+    }
+    bool clamp;
+    const Quant4 f = quant4_of(lo, hi, clamp);
+    const unsigned clamps = __ballot_sync(~0u, clamp);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        float lo = 0.f, hi = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int from = (lane & ~3) + i;
+      const float s = __shfl_sync(~0u, f.s, from), inv = __shfl_sync(~0u, f.inv, from), z = __shfl_sync(~0u, f.z, from);
+      const uint32_t meta = __shfl_sync(~0u, f.meta, from);
+      const bool cl = (clamps >> from) & 1;
+      const int h = h0 + (i >> 1) * kHeads;
+      if (h < a.H) {
+        const size_t at = (page_row + h) * a.P + slot;
+        uint32_t* dst = reinterpret_cast<uint32_t*>((i & 1 ? pool.v : pool.k) + at * (a.d / 2));
 #pragma unroll
         for (int w = 0; w < W; ++w)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            lo = min_nan(lo, x[i][v][w][e]);
-            hi = max_nan(hi, x[i][v][w][e]);
+          if (g + G * w < words) {
+            float e[8];
+            x[i][w].get(e);
+            dst[g + G * w] = quant4_word<sizeof(T) == 2>(s, inv, z, cl, e);
           }
-#pragma unroll
-        for (int o = G / 2; o >= 1; o >>= 1) {
-          lo = min_nan(lo, __shfl_xor_sync(~0u, lo, o));
-          hi = max_nan(hi, __shfl_xor_sync(~0u, hi, o));
-        }
-        const int h = h0 + i * kHeads;
-        if (h < a.H) {
-          const Quant4 f = quant4_of(lo, hi);
-          const size_t at = (page_row + h) * a.P + slot;
-          uint32_t* dst = reinterpret_cast<uint32_t*>((v ? pool.v : pool.k) + at * (a.d / 2));
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-            if (g + G * w < words) dst[g + G * w] = quant4_word(f, x[i][v][w]);
-          if (g == 0) (v ? pool.v_meta : pool.k_meta)[at] = f.meta;
-        }
+        if (g == 0) (i & 1 ? pool.v_meta : pool.k_meta)[at] = meta;
       }
+    }
   }
 }
 
@@ -286,11 +290,26 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_q4_kernel(const ReadArgs 
 #pragma unroll
           for (int w = 0; w < W; ++w) {
             if (h >= a.H || g + G * w >= words) continue;
-            float y[8];
+            T* out = static_cast<T*>(v ? a.v_out : a.k_out) + ((size_t)row * a.H + h) * a.d + 8 * (g + G * w);
+            const uint32_t c = code[i][v][w];
+            if constexpr (sizeof(T) == 2) {
+              // code - zero is exact in bf16 and the product is rounded once, two elements at a time
+              const __nv_bfloat162 s2 = __float2bfloat162_rn(s), z2 = __float2bfloat162_rn(128.f + z);
+              uint32_t y[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)  // 2^23 + code, exact
-              y[e] = s * (__uint_as_float(((code[i][v][w] >> nibble_shift(e)) & 15u) | 0x4B000000u) - (8388608.f + z));
-            store8(static_cast<T*>(v ? a.v_out : a.k_out) + ((size_t)row * a.H + h) * a.d + 8 * (g + G * w), y);
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t q = ((c >> (4 * e)) & 0x000F000Fu) | 0x43004300u;
+                const __nv_bfloat162 p = __hmul2(s2, __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q), z2));
+                y[e] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+              *reinterpret_cast<uint4*>(out) = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+              float y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)  // 2^23 + code, exact
+                y[e] = s * (__uint_as_float(((c >> nibble_shift(e)) & 15u) | 0x4B000000u) - (8388608.f + z));
+              store8(out, y);
+            }
           }
         }
     }
@@ -329,8 +348,8 @@ struct Read {
   }
 };
 
-// a warp a token, up to 16 blocks of 8 warps an SM
-int row_blocks(int rows) { return std::max(1, std::min((rows + kRowWarps - 1) / kRowWarps, 148 * 16)); }
+// a warp a token, up to so many blocks of 8 warps an SM
+int row_blocks(int rows, int per_sm) { return std::max(1, std::min((rows + kRowWarps - 1) / kRowWarps, 148 * per_sm)); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -401,7 +420,7 @@ int hstu_kv_append_q4(const hstu_kv_params* p, const void* k_new, const void* v_
     if (launch_kv_append_plan(a, s) != cudaSuccess) return HSTU_ERR_CUDA;
     if (p->total_new == 0) return HSTU_OK;
   }
-  return by_head_dim<Append>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, fused, row_blocks(p->total_new), s) ==
+  return by_head_dim<Append>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, fused, row_blocks(p->total_new, 3), s) ==
                  cudaSuccess
              ? HSTU_OK
              : HSTU_ERR_CUDA;
@@ -440,7 +459,7 @@ int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_p
   const Q4Pool pool{static_cast<uint8_t*>(const_cast<void*>(k_pool)), static_cast<uint8_t*>(const_cast<void*>(v_pool)),
                     static_cast<uint32_t*>(const_cast<void*>(k_scales)),
                     static_cast<uint32_t*>(const_cast<void*>(v_scales))};
-  return by_head_dim<Read>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, row_blocks(p->total_new), s) == cudaSuccess
+  return by_head_dim<Read>(p->head_dim, a, pool, p->dtype == HSTU_DT_BF16, row_blocks(p->total_new, 8), s) == cudaSuccess
              ? HSTU_OK
              : HSTU_ERR_CUDA;
 }

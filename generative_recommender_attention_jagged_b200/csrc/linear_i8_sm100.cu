@@ -396,10 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // unit gives one of tanh and int-to-float conversion in that time, so the conversion
 // is done on the other pipes: the halves of the int32 go into the mantissa of 2^23
 // (exact), 65536 hi + lo is one rounded FMA, and the multiplications are packed in
-// pairs.  Each half of the epilogue (4 warps) has its own two staging boxes.
+// pairs.  Sixteen epilogue warps (four to a scheduler, to cover their latencies) work
+// in four groups of 64 columns, each with a staging box and barriers of its own.
 constexpr int kPairStages = 4;
 constexpr int kPairStage = kBM * kBK;   // 16 KB: this CTA's 128 rows of x, or 128 channels of w
-constexpr int kPairEpiWarps = 8;
+constexpr int kPairEpiWarps = 16;      // four groups of 64 columns, a warp per 32 rows
 constexpr int kPairThreads = 32 * (2 + kPairEpiWarps);
 constexpr int kPairBN = 256;
 constexpr int kBox = kBM * 128;         // 128 rows x 128 bytes of output
@@ -407,8 +408,8 @@ constexpr int kBox = kBM * 128;         // 128 rows x 128 bytes of output
 struct __align__(1024) SmemPair {
   uint8_t x[kPairStages][kPairStage];
   uint8_t w[kPairStages][kPairStage];
-  uint8_t out[2][2][kBox];              // [half][in turn]
-  float wscale[2][kPairBN], bias[2][kPairBN];
+  uint8_t out[4][kBox];                 // a staging box for each group of 64 columns
+  float wscale[4][64], bias[4][64];
   uint64_t full[kPairStages];           // even CTA: both CTAs' bytes of the stage landed
   uint64_t empty[kPairStages];          // both CTAs: the MMAs that read the stage completed
   uint64_t acc_full[2];
@@ -436,17 +437,17 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* s
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// the 128 threads of an epilogue half agree on a flag
-__device__ __forceinline__ bool half_all(bool ok, int half) {
+// the 128 threads of an epilogue group agree on a flag
+__device__ __forceinline__ bool group_all(bool ok, int group) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "bar.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok), "r"(3 + half)
+      : "r"((uint32_t)ok), "r"(5 + group)
       : "memory");
   return r != 0;
 }
@@ -575,68 +576,64 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
-    constexpr int kCols = 128 / (int)sizeof(TOut);   // columns of a box: 64 bf16 or 32 fp32
-    constexpr bool kBf16 = sizeof(TOut) == 2;
+    constexpr bool kBf16 = sizeof(TOut) == 2;        // a box (128 bytes a row) holds 64 bf16 or 32 fp32 columns
     constexpr float kFactor = kBf16 && SILU ? 0.5f : 1.f;  // half of x where SiLU wants x / 2
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const int te = threadIdx.x - 64 - 128 * half;    // thread of the half
-    const bool issuer = (warp == 2 || warp == 6) && lane == 0;
+    const int quarter = warp & 3, grp = (warp - 2) >> 2;
+    const int te = threadIdx.x - 64 - 128 * grp;     // thread of the group
+    const bool issuer = te == 0;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t empty_addr0 = map_shared(smem_u32(&sm.acc_empty[0]), 0);
     const uint32_t empty_addr1 = map_shared(smem_u32(&sm.acc_empty[1]), 0);
-    int tc = 0, boxes = 0;
+    float(&ws)[64] = sm.wscale[grp];
+    float(&bs)[64] = sm.bias[grp];
+    uint8_t* box = sm.out[grp];
+    const uint32_t dst = smem_u32(box) + r * 128;
+    int tc = 0;
     for (int u = pair; u < n_units; u += n_pairs, ++tc) {
       const int b = tc & 1;
       const int row0 = (u / tiles_n) * 2 * kBM + rank * kBM;
-      const int n0 = (u % tiles_n) * kPairBN;
+      const int n0 = (u % tiles_n) * kPairBN + 64 * grp;
       const float xs = kFactor * (row0 + r < a.T ? a.x_scale[row0 + r] : 0.f);
       const uint64_t xs2 = pack2(xs, xs);
-      // the tile's scales and biases, a copy for each half (the barrier of the last tile's last box is behind its reads)
-      float(&ws)[kPairBN] = sm.wscale[half];
-      float(&bs)[kPairBN] = sm.bias[half];
-#pragma unroll
-      for (int c = te; c < kPairBN; c += 128) {
-        const int n = n0 + c;
-        ws[c] = n < a.N ? __ldg(a.w_scale + n) : 0.f;
-        bs[c] = n < a.N && a.bias ? kFactor * __ldg(a.bias + n) : 0.f;
+      // the scales and biases of the group's columns (the barrier of the last tile's box is behind its reads)
+      if (te < 64) {
+        const int n = n0 + te;
+        ws[te] = n < a.N ? __ldg(a.w_scale + n) : 0.f;
+        bs[te] = n < a.N && a.bias ? kFactor * __ldg(a.bias + n) : 0.f;
       }
-      const bool ok = half_all(mbar_wait(&sm.acc_full[b], (tc >> 1) & 1, abort_flag, a.hdr, 34), half);
+      const bool ok = group_all(mbar_wait(&sm.acc_full[b], (tc >> 1) & 1, abort_flag, a.hdr, 34), grp);
       if (!ok) break;
       tc_fence_after();
-      constexpr int kChunks = kPairBN / 2 / 32;  // 32-column chunks of this half: box 2 i + half holds kCols / 32 of them
-      auto column = [&](int x) { return (2 * (x / (kCols / 32)) + half) * kCols + 32 * (x % (kCols / 32)); };
+      const uint32_t acc_tmem = tmem + lane_base + b * kPairBN + 64 * grp;
       uint32_t acc[2][32];
-      tmem_ld32(tmem + lane_base + b * kPairBN + column(0), acc[0]);
+      tmem_ld32(acc_tmem, acc[0]);
 #pragma unroll
-      for (int x = 0; x < kChunks; ++x) {
-        const int c0 = column(x);
-        uint8_t* box = sm.out[half][boxes & 1];
-        if (x % (kCols / 32) == 0 && boxes >= 2) {
-          // the store issued two boxes ago has read this buffer
-          if (issuer) bulk_wait_read1();
-          named_bar_sync(1 + half, 128);
+      for (int x = 0; x < 2; ++x) {  // chunks of 32 columns
+        if (x == 0 || !kBf16) {
+          // the last store from the box has read it
+          if (issuer) bulk_wait_read();
+          named_bar_sync(1 + grp, 128);
         }
-        tmem_wait_ld(acc[x & 1]);
-        if (x + 1 < kChunks) {
-          tmem_ld32(tmem + lane_base + b * kPairBN + column(x + 1), acc[(x + 1) & 1]);
+        tmem_wait_ld(acc[x]);
+        if (x == 0) {
+          tmem_ld32(acc_tmem + 32, acc[1]);
         } else {
           // this warp's part of accumulator b is read: tell the even CTA's issuer
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(b ? empty_addr1 : empty_addr0);
         }
-        const uint32_t dst = smem_u32(box) + r * 128;
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
           float y[8];
 #pragma unroll
           for (int k = 0; k < 8; k += 4) {
-            const float4 wv = *reinterpret_cast<const float4*>(&ws[c0 + e + k]);
-            const float4 bv = *reinterpret_cast<const float4*>(&bs[c0 + e + k]);
+            const float4 wv = *reinterpret_cast<const float4*>(&ws[32 * x + e + k]);
+            const float4 bv = *reinterpret_cast<const float4*>(&bs[32 * x + e + k]);
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
-              const uint32_t i0 = acc[x & 1][e + k + q], i1 = acc[x & 1][e + k + q + 1];
+              const uint32_t i0 = acc[x][e + k + q], i1 = acc[x][e + k + q + 1];
               // without tanh the special-function unit is free for the conversion
               const uint64_t f2 = SILU ? ints_to_float2(i0, i1) : pack2(__int2float_rn((int)i0), __int2float_rn((int)i1));
               const uint64_t v2 = fma2(f2, mul2(xs2, q ? pack2(wv.z, wv.w) : pack2(wv.x, wv.y)),
@@ -652,7 +649,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
           }
           // 16-byte chunk j of the box row at j ^ (r & 7) (the store's 128-byte swizzle)
-          const int j0 = (x % (kCols / 32)) * 32 + e;
+          const int j0 = (kBf16 ? 32 * x : 0) + e;
           if constexpr (kBf16) {
             asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (((j0 / 8) ^ (r & 7)) << 4)),
                          "r"(pack_bf16x2(y[0], y[1])), "r"(pack_bf16x2(y[2], y[3])), "r"(pack_bf16x2(y[4], y[5])),
@@ -666,15 +663,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                            : "memory");
           }
         }
-        if ((x + 1) % (kCols / 32) == 0) {
+        if (x == 1 || !kBf16) {
           fence_proxy_async_smem();
-          named_bar_sync(1 + half, 128);
+          named_bar_sync(1 + grp, 128);
           if (issuer) {
-            const int c = n0 + c0 + 32 - kCols;
+            const int c = n0 + (kBf16 ? 0 : 32 * x);
             if (c < a.N && row0 < a.T) tma_store_2d(&tm_out, box, c, row0);  // rows and columns outside are dropped
             bulk_commit();
           }
-          ++boxes;
         }
       }
     }

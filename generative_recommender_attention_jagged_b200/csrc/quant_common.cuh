@@ -80,41 +80,64 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// x / s for |x / s| < 2^20, s and inv ~ 1 / s normal: the remainder of a first
+// product is exact, and adding its share again gives the quotient to half an ulp and
+// exactly where it has a short binary fraction (the correction is then off by far less
+// than the last bit).  Three operations of the FMA pipe.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = x * inv;
+  return fmaf(fmaf(-q, s, x), inv, q);
+}
+
 struct Quant4 {
-  float s, inv;   // bf16-exact scale and about its reciprocal
+  float s, inv;   // bf16-exact scale (0: all codes 0) and about its reciprocal
   float z;        // zero point 0..15
   uint32_t meta;  // the stored word: scale | zero << 16 (bf16 bits)
-  bool live;      // codes are not all zero
-  bool clamp;     // an end of the row rounds to a code outside 0..15
 };
 
-// Format of a row with extremes lo <= 0 <= hi (NaN if an element is).
-__device__ __forceinline__ Quant4 quant4_of(float lo, float hi) {
+// Format of a row with extremes lo <= 0 <= hi (NaN if an element is).  `clamp`: an end
+// of the row rounds to a code outside 0..15.
+__device__ __forceinline__ Quant4 quant4_of(float lo, float hi, bool& clamp) {
   Quant4 f;
   const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
-  f.s = __bfloat162float(sb);
-  const bool nan = !(f.s <= FLT_MAX);  // an infinity, a NaN or a range beyond fp32
-  f.live = !nan && f.s >= FLT_MIN;
-  f.inv = f.live ? 1.f / f.s : 0.f;
-  f.z = f.live ? fminf(round_quotient(-lo, f.s, f.inv) - kRoundMagic, 15.f) : 0.f;
-  f.clamp = f.live && (round_quotient(lo, f.s, f.inv) - kRoundMagic + f.z < 0.f ||
-                       round_quotient(hi, f.s, f.inv) - kRoundMagic + f.z > 15.f);
-  const uint32_t sbits = f.live ? (uint32_t)__bfloat16_as_ushort(sb) : (nan ? 0x7FC0u : 0u);
+  const float s = __bfloat162float(sb);
+  const bool nan = !(s <= FLT_MAX);  // an infinity, a NaN or a range beyond fp32
+  const bool live = !nan && s >= FLT_MIN;
+  f.s = live ? s : 0.f;
+  f.inv = live ? __frcp_rn(s) : 0.f;
+  f.z = live ? fminf(round_quotient(-lo, s, f.inv) - kRoundMagic, 15.f) : 0.f;
+  clamp = live && (round_quotient(lo, s, f.inv) - kRoundMagic + f.z < 0.f ||
+                   round_quotient(hi, s, f.inv) - kRoundMagic + f.z > 15.f);
+  const uint32_t sbits = live ? (uint32_t)__bfloat16_as_ushort(sb) : (nan ? 0x7FC0u : 0u);
   f.meta = sbits | ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(f.z)) << 16);
   return f;
 }
 
-// The word of 8 elements.  The codes are put together as fp32 sums of
-// code * 16^i (at most 65535, exact), four to a half of the word.
-__device__ __forceinline__ uint32_t quant4_word(const Quant4& f, const float (&x)[8]) {
-  if (!f.live) return 0;
+// The word of 8 elements.  A quotient of two bf16 numbers is a half-integer or at
+// least 2^-16 away from one (relative), so the rounded quotient decides a bf16 row's
+// codes; for fp32 rows one that comes out as a half-integer is compared exactly.  The
+// codes are put together as fp32 sums of code * 16^i (at most 65535, exact), four to a
+// half of the word.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quant4_word(float s, float inv, float z, bool clamp, const float (&x)[8]) {
+  if (s == 0.f) return 0;
   float m[8];
-  round_quotients8(x, f.s, f.inv, m);
-  if (f.clamp) {
+  bool half = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fminf(fmaxf(m[i], kRoundMagic - f.z), kRoundMagic + 15.f - f.z);
+  for (int i = 0; i < 8; ++i) {
+    const float q = quotient(x[i], s, inv);
+    m[i] = q + kRoundMagic;
+    if constexpr (!BF16) half = half || fabsf(q - (m[i] - kRoundMagic)) == 0.5f;
   }
-  float even = f.z * 4369.f, odd = even;  // 0x1111
+  if (!BF16 && half) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fix_quotient(x[i], s, m[i]);
+  }
+  if (clamp) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fminf(fmaxf(m[i], kRoundMagic - z), kRoundMagic + 15.f - z);
+  }
+  float even = z * 4369.f, odd = even;  // 0x1111
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     even = fmaf(m[2 * i] - kRoundMagic, (float)(1 << (4 * i)), even);
@@ -129,6 +152,86 @@ __device__ __forceinline__ float meta_zero(uint32_t meta) { return __uint_as_flo
 
 // bit position of element e (0..7) inside its 32-bit word
 __host__ __device__ __forceinline__ int nibble_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
+
+// packed bf16: smaller / larger of each half, NaN if either is NaN
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// 8 consecutive elements of a row as they lie, and the row's extremes packed so
+// that one shuffle carries both
+template <typename T>
+struct Elems8;
+template <>
+struct Elems8<__nv_bfloat16> {
+  using Extremes = uint32_t;  // bf16 pair (-smallest, largest)
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0u; }
+  __device__ __forceinline__ Extremes extremes() const {
+    uint32_t lo = min2_nan(min2_nan(w[0], w[1]), min2_nan(w[2], w[3]));
+    uint32_t hi = max2_nan(max2_nan(w[0], w[1]), max2_nan(w[2], w[3]));
+    lo = min2_nan(lo, __byte_perm(lo, lo, 0x1032));
+    hi = max2_nan(hi, __byte_perm(hi, hi, 0x1032));
+    return __byte_perm(lo ^ 0x80008000u, hi, 0x5410);
+  }
+  __device__ static __forceinline__ Extremes join(Extremes a, Extremes b) { return max2_nan(a, b); }
+  __device__ static __forceinline__ Extremes other(Extremes a, int mask) { return __shfl_xor_sync(~0u, a, mask); }
+  // with 0 among them
+  __device__ static __forceinline__ float lowest(Extremes a) { return -__uint_as_float(max2_nan(a, 0u) << 16); }
+  __device__ static __forceinline__ float highest(Extremes a) { return __uint_as_float(max2_nan(a, 0u) & 0xFFFF0000u); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Elems8<float> {
+  using Extremes = float2;
+  float e[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    e[0] = a.x, e[1] = a.y, e[2] = a.z, e[3] = a.w, e[4] = b.x, e[5] = b.y, e[6] = b.z, e[7] = b.w;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = 0.f;
+  }
+  __device__ __forceinline__ Extremes extremes() const {
+    float lo = e[0], hi = e[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      lo = min_nan(lo, e[i]);
+      hi = max_nan(hi, e[i]);
+    }
+    return make_float2(lo, hi);
+  }
+  __device__ static __forceinline__ Extremes join(Extremes a, Extremes b) {
+    return make_float2(min_nan(a.x, b.x), max_nan(a.y, b.y));
+  }
+  __device__ static __forceinline__ Extremes other(Extremes a, int mask) {
+    return make_float2(__shfl_xor_sync(~0u, a.x, mask), __shfl_xor_sync(~0u, a.y, mask));
+  }
+  __device__ static __forceinline__ float lowest(Extremes a) { return min_nan(a.x, 0.f); }
+  __device__ static __forceinline__ float highest(Extremes a) { return max_nan(a.y, 0.f); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = e[i];
+  }
+};
 
 // 8 consecutive elements as fp32
 __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
