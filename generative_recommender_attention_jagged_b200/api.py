@@ -330,91 +330,108 @@ def hstu_kv_evict(evict_mask, k_pool, page_table, cached_lens, free_pages, free_
 
 
 # ---- 8-bit linear layer, 4-bit cache ----------------------------------------
+#
+# These calls are short enough for the host to count (a small one takes about
+# 10 us on the GPU), so their checks use the cheapest accessor of each property
+# and pointers go to ctypes as plain integers.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _call_on:
-    """One entry-point call on the device of its tensors: refuses tensors of
-    several devices, makes theirs current for the call, and picks the stream
-    (the given one, else that device's current one)."""
-
-    def __init__(self, stream, *tensors):
-        self.dev = next(t.device for t in tensors if t is not None)
-        for t in tensors:
-            if t is not None and t.device != self.dev:
-                raise ValueError(f"all tensors must be on one device, got {self.dev} and {t.device}")
-        if stream is not None and stream.device != self.dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.dev}")
-        self.given = stream
-        self.ctx = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.ctx = torch.cuda.device(self.dev)
-            self.ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        """An output or scratch buffer of this call, kept until its stream has used it."""
-        t = torch.empty(shape, dtype=dtype, device=self.dev)
-        if self.given is not None:
-            t.record_stream(self.given)
-        return t
-
-    @property
-    def stream(self):
-        s = self.given if self.given is not None else torch.cuda.current_stream(self.dev)
-        return ctypes.c_void_p(s.cuda_stream)
+def _one_device(named) -> int:
+    """Index of the GPU that holds every tensor of `named` ((name, tensor or None) pairs)."""
+    dev = -1
+    for name, t in named:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on cuda:{d}, the tensors before it on cuda:{dev}")
+    return dev
 
 
-def _need_out(name: str, t: torch.Tensor, shape, dtype, rows_only: bool = False):
-    """An output given by the caller: on a GPU, of this shape and type, contiguous
-    (rows_only: contiguous rows with any stride)."""
-    _need_cuda(name, t, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if rows_only:
-        if t.numel() and t.stride(-1) != 1:
-            raise ValueError(f"{name} must have contiguous rows")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _on_device(dev: int, stream):
+    """(context that makes `dev` current, or None if it is; raw stream of the call)."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    guard = None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+    return guard, (_raw_stream(dev) if stream is None else stream.cuda_stream)
 
 
-def _need_workspace(t: torch.Tensor):
-    _need_cuda("workspace", t)
-    if not t.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+def _empty(shape, dtype, dev: int, stream):
+    """An output or scratch buffer of this call, kept until its stream has used it."""
+    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+class _Devices(dict):
+    def __missing__(self, index):
+        self[index] = torch.device("cuda", index)
+        return self[index]
+
+
+_DEVICES = _Devices()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, where: str, guard, *args):
+    if guard is None:
+        rc = fn(*args)
+    else:
+        with guard:
+            rc = fn(*args)
+    if rc:
+        _lib.check(rc, where)
+
+
+def _need(name: str, t, dtype, shape):
+    """A contiguous tensor of this type and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}"
+                         f" with strides {t.stride()}")
+
+
+def _ints(name: str, t, n: int):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _token_rows(name: str, t, H: int, d: int) -> int:
+    """Token stride of a [T, H, d] view with packed heads."""
+    s = t.stride()
+    if t.numel() and (s[2] != 1 or s[1] != d):
+        raise ValueError(f"{name}: heads and features must be packed (stride 1 / d)")
+    return s[0] if t.shape[0] > 1 else H * d
 
 
 def hstu_quant_i8_weight(w, *, w_q=None, w_scale=None, stream=None):
     """w [d_in, d_out] (bf16 or fp32) -> (w_q [d_out, d_in] int8, w_scale [d_out]
     fp32): one scale a channel, the layout hstu_linear_i8 reads."""
-    _need_cuda("w", w)
+    dev = _one_device((("w", w), ("w_q", w_q), ("w_scale", w_scale)))
     if w.dim() != 2 or w.dtype not in _DT or not w.is_contiguous():
         raise ValueError("w must be a contiguous bf16 or fp32 [d_in, d_out] matrix")
     K, N = w.shape
-    with _call_on(stream, w, w_q, w_scale) as c:
-        if w_q is None:
-            w_q = c.empty((N, K), torch.int8)
-        if w_scale is None:
-            w_scale = c.empty((N,), torch.float32)
-        _need_out("w_q", w_q, (N, K), torch.int8)
-        _need_out("w_scale", w_scale, (N,), torch.float32)
-        rc = _lib.load().hstu_quant_i8_weight(_p(w), K, N, _DT[w.dtype], _p(w_q), _p(w_scale), c.stream)
-    _lib.check(rc, "hstu_quant_i8_weight")
+    guard, raw = _on_device(dev, stream)
+    w_q = _empty((N, K), torch.int8, dev, stream) if w_q is None else w_q
+    w_scale = _empty((N,), torch.float32, dev, stream) if w_scale is None else w_scale
+    _need("w_q", w_q, torch.int8, (N, K))
+    _need("w_scale", w_scale, torch.float32, (N,))
+    _call(_lib.load().hstu_quant_i8_weight, "hstu_quant_i8_weight", guard, w.data_ptr(), K, N, _DT[w.dtype],
+          w_q.data_ptr(), w_scale.data_ptr(), raw)
     return w_q, w_scale
 
 
 def hstu_linear_i8_workspace_size(rows: int, d_in: int, d_out: int) -> int:
-    p = _lib.LinearI8Params(rows=rows, d_in=d_in, d_out=d_out, x_stride=0, out_stride=0, dtype=_lib.DT_BF16,
-                            out_dtype=_lib.DT_BF16, flags=0)
+    p = _lib.LinearI8Params(rows, d_in, d_out, 0, 0, _lib.DT_BF16, _lib.DT_BF16, 0)
     return int(_lib.load().hstu_linear_i8_workspace_size(ctypes.byref(p)))
 
 
@@ -423,72 +440,61 @@ def hstu_linear_i8(x, w_q, w_scale, bias=None, *, silu: bool = False, out=None, 
     """out = act(x W + bias) with x quantised to 8 bits token by token and W held
     in 8 bits channel by channel (hstu_quant_i8_weight); out_dtype defaults to
     x's type."""
-    _need_cuda("x", x)
-    _need_cuda("w_q", w_q, torch.int8)
-    _need_cuda("w_scale", w_scale, torch.float32)
-    _need_cuda("bias", bias, torch.float32)
-    if x.dim() != 2 or x.dtype not in _DT or (x.numel() and x.stride(1) != 1):
+    dev = _one_device((("x", x), ("w_q", w_q), ("w_scale", w_scale), ("bias", bias), ("out", out),
+                       ("workspace", workspace)))
+    if x.dim() != 2 or x.dtype not in _DT or (x.stride(1) != 1 and x.numel()):
         raise ValueError("x must be a bf16 or fp32 [T, d_in] matrix with contiguous rows")
-    if w_q.dim() != 2 or w_q.shape[1] != x.shape[1] or not w_q.is_contiguous():
-        raise ValueError("w_q must be a contiguous [d_out, d_in] matrix")
-    N, K = w_q.shape
-    for name, t in (("w_scale", w_scale), ("bias", bias)):
-        if t is not None and (tuple(t.shape) != (N,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous [d_out] vector")
+    T, K = x.shape
+    if w_q.dim() != 2 or w_q.dtype != torch.int8 or w_q.shape[1] != K or not w_q.is_contiguous():
+        raise ValueError(f"w_q must be a contiguous int8 [d_out, {K}] matrix")
+    N = w_q.shape[0]
+    _need("w_scale", w_scale, torch.float32, (N,))
+    if bias is not None:
+        _need("bias", bias, torch.float32, (N,))
     dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else x.dtype)
     if dt not in _DT:
         raise ValueError(f"out must be bf16 or fp32, got {dt}")
-    T = x.shape[0]
-    with _call_on(stream, x, w_q, w_scale, bias, out, workspace) as c:
-        if out is None:
-            out = c.empty((T, N), dt)
-        else:
-            _need_out("out", out, (T, N), dt, rows_only=True)
-        p = _lib.LinearI8Params(rows=T, d_in=K, d_out=N, x_stride=_row_stride(x), out_stride=_row_stride(out),
-                                dtype=_DT[x.dtype], out_dtype=_DT[dt], flags=_lib.LIN_SILU if silu else 0)
-        lib = _lib.load()
-        if workspace is None:
-            workspace = c.empty((int(lib.hstu_linear_i8_workspace_size(ctypes.byref(p))),), torch.uint8)
-        else:
-            _need_workspace(workspace)
-        rc = lib.hstu_linear_i8(ctypes.byref(p), _p(x), _p(w_q), _p(w_scale), _p(bias), _p(out), _p(workspace),
-                                workspace.nbytes, c.stream)
-    _lib.check(rc, "hstu_linear_i8")
+    guard, raw = _on_device(dev, stream)
+    if out is None:
+        out = _empty((T, N), dt, dev, stream)
+    elif out.dtype != dt or tuple(out.shape) != (T, N) or (out.stride(1) != 1 and out.numel()):
+        raise ValueError(f"out must be a {dt} [{T}, {N}] matrix with contiguous rows, got {out.dtype} {tuple(out.shape)}")
+    p = ctypes.byref(_lib.LinearI8Params(T, K, N, x.stride(0) if T > 1 else K, out.stride(0) if T > 1 else N,
+                                         _DT[x.dtype], _DT[dt], _lib.LIN_SILU if silu else 0))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _empty((int(lib.hstu_linear_i8_workspace_size(p)),), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(lib.hstu_linear_i8, "hstu_linear_i8", guard, p, x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+          out.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
     return out
 
 
 def _q4_kv_params(k_pool, page_table, dtype, stride: int, total: int) -> _lib.KvParams:
     num_pages, H, P, half = k_pool.shape
-    return _lib.KvParams(batch=page_table.shape[0], num_heads=H, head_dim=2 * half, page_size=P, num_pages=num_pages,
-                         max_pages_per_user=page_table.shape[1], kv_stride=stride, total_new=total, dtype=_DT[dtype])
+    B, max_pages = page_table.shape
+    return _lib.KvParams(B, H, 2 * half, P, num_pages, max_pages, stride, total, _DT[dtype])
 
 
 def _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H: int, d: int):
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _need_cuda(name, t, torch.uint8)
-        if t.dim() != 4 or t.shape[1] != H or 2 * t.shape[3] != d or t.shape != k_pool.shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [num_pages, {H}, page_size, {d // 2}] byte tensor")
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        _need_cuda(name, t, torch.bfloat16)
-        if tuple(t.shape) != (*k_pool.shape[:3], 2) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 [num_pages, H, page_size, 2] tensor")
-
-
-def _int_vector(name: str, t, n: int):
-    _need_cuda(name, t, torch.int32)
-    if t is not None and (t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous int32 vector of {n}")
+    shape = tuple(k_pool.shape)
+    if len(shape) != 4 or shape[1] != H or 2 * shape[3] != d:
+        raise ValueError(f"k_pool must be [num_pages, {H}, page_size, {d // 2}], got {shape}")
+    _need("k_pool", k_pool, torch.uint8, shape)
+    _need("v_pool", v_pool, torch.uint8, shape)
+    meta = (shape[0], shape[1], shape[2], 2)
+    _need("k_scales", k_scales, torch.bfloat16, meta)
+    _need("v_scales", v_scales, torch.bfloat16, meta)
 
 
 def _page_table(name: str, t):
-    _need_cuda(name, t, torch.int32)
-    if t.dim() != 2 or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [batch, max_pages_per_user] int32 matrix")
 
 
 def hstu_kv_q4_workspace_size(batch: int) -> int:
-    p = _lib.KvParams(batch=batch, num_heads=1, head_dim=32, page_size=1, num_pages=1, max_pages_per_user=1,
-                      kv_stride=0, total_new=0, dtype=_lib.DT_BF16)
+    p = _lib.KvParams(batch, 1, 32, 1, 1, 1, 0, 0, _lib.DT_BF16)
     return int(_lib.load().hstu_kv_q4_workspace_size(ctypes.byref(p)))
 
 
@@ -496,34 +502,36 @@ def hstu_kv_append_q4(k_new, v_new, new_offsets, k_pool, v_pool, k_scales, v_sca
                       free_pages, free_count, *, num_append=None, workspace=None, stream=None):
     """hstu_kv_append into a 4-bit pool (k_pool, v_pool [num_pages, H, page_size,
     d / 2] bytes, k_scales, v_scales [num_pages, H, page_size, 2] bf16); in place."""
-    if k_new.dim() != 3 or k_new.dtype not in _DT or v_new.shape != k_new.shape:
+    dev = _one_device((("k_new", k_new), ("v_new", v_new), ("new_offsets", new_offsets), ("k_pool", k_pool),
+                       ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales), ("page_table", page_table),
+                       ("cached_lens", cached_lens), ("free_pages", free_pages), ("free_count", free_count),
+                       ("num_append", num_append), ("workspace", workspace)))
+    if k_new.dim() != 3 or k_new.dtype not in _DT or v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be bf16 or fp32 [T, H, d] tensors")
     T, H, d = k_new.shape
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _need_cuda(name, t, k_new.dtype)
-    stride = _rows_view("k_new", k_new, H, d)
-    if _rows_view("v_new", v_new, H, d) != stride:
+    token = _token_rows("k_new", k_new, H, d)
+    if _token_rows("v_new", v_new, H, d) != token:
         raise ValueError("k_new and v_new must share one token stride")
     _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
     _page_table("page_table", page_table)
     B = page_table.shape[0]
-    _int_vector("new_offsets", new_offsets, B + 1)
-    _int_vector("num_append", num_append, B)
-    _int_vector("cached_lens", cached_lens, B)
-    _int_vector("free_pages", free_pages, k_pool.shape[0])
-    _int_vector("free_count", free_count, 1)
-    with _call_on(stream, k_new, v_new, new_offsets, num_append, k_pool, v_pool, k_scales, v_scales, page_table,
-                  cached_lens, free_pages, free_count, workspace) as c:
-        p = _q4_kv_params(k_pool, page_table, k_new.dtype, stride, T)
-        lib = _lib.load()
-        if workspace is None:
-            workspace = c.empty((int(lib.hstu_kv_q4_workspace_size(ctypes.byref(p))),), torch.uint8)
-        else:
-            _need_workspace(workspace)
-        rc = lib.hstu_kv_append_q4(ctypes.byref(p), _p(k_new), _p(v_new), _p(new_offsets), _p(num_append), _p(k_pool),
-                                   _p(v_pool), _p(k_scales), _p(v_scales), _p(page_table), _p(cached_lens),
-                                   _p(free_pages), _p(free_count), _p(workspace), workspace.nbytes, c.stream)
-    _lib.check(rc, "hstu_kv_append_q4")
+    _ints("new_offsets", new_offsets, B + 1)
+    _ints("cached_lens", cached_lens, B)
+    _ints("free_pages", free_pages, k_pool.shape[0])
+    _ints("free_count", free_count, 1)
+    if num_append is not None:
+        _ints("num_append", num_append, B)
+    guard, raw = _on_device(dev, stream)
+    p = ctypes.byref(_q4_kv_params(k_pool, page_table, k_new.dtype, token, T))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _empty((int(lib.hstu_kv_q4_workspace_size(p)),), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(lib.hstu_kv_append_q4, "hstu_kv_append_q4", guard, p, k_new.data_ptr(), v_new.data_ptr(),
+          new_offsets.data_ptr(), _ptr(num_append), k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
+          v_scales.data_ptr(), page_table.data_ptr(), cached_lens.data_ptr(), free_pages.data_ptr(),
+          free_count.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
     return workspace
 
 
@@ -531,34 +539,39 @@ def hstu_kv_read_q4(k_pool, v_pool, k_scales, v_scales, page_table, cached_lens,
                     total_tokens: int, dtype=torch.bfloat16, k_out=None, v_out=None, workspace=None, stream=None):
     """Dense (k, v) [total_tokens, H, d] of cached tokens: row offsets[u] + i is
     token starts[u] + i of user u."""
+    dev = _one_device((("k_pool", k_pool), ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales),
+                       ("page_table", page_table), ("cached_lens", cached_lens), ("starts", starts),
+                       ("offsets", offsets), ("k_out", k_out), ("v_out", v_out), ("workspace", workspace)))
     if k_pool.dim() != 4:
         raise ValueError("k_pool must be [num_pages, H, page_size, d / 2]")
     H, d = k_pool.shape[1], 2 * k_pool.shape[3]
     _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
     _page_table("page_table", page_table)
     B = page_table.shape[0]
-    _int_vector("cached_lens", cached_lens, B)
-    _int_vector("starts", starts, B)
-    _int_vector("offsets", offsets, B + 1)
+    _ints("cached_lens", cached_lens, B)
+    _ints("starts", starts, B)
+    _ints("offsets", offsets, B + 1)
     if dtype not in _DT:
         raise ValueError(f"dtype must be bf16 or fp32, got {dtype}")
-    with _call_on(stream, k_pool, v_pool, k_scales, v_scales, page_table, cached_lens, starts, offsets, k_out, v_out,
-                  workspace) as c:
-        shape = (total_tokens, H, d)
-        k_out = c.empty(shape, dtype) if k_out is None else k_out
-        v_out = c.empty(shape, dtype) if v_out is None else v_out
-        _need_out("k_out", k_out, shape, dtype)
-        _need_out("v_out", v_out, shape, dtype)
-        p = _q4_kv_params(k_pool, page_table, dtype, 0, total_tokens)
-        lib = _lib.load()
-        if workspace is None:
-            workspace = c.empty((int(lib.hstu_kv_q4_workspace_size(ctypes.byref(p))),), torch.uint8)
-        else:
-            _need_workspace(workspace)
-        rc = lib.hstu_kv_read_q4(ctypes.byref(p), _p(k_pool), _p(v_pool), _p(k_scales), _p(v_scales), _p(page_table),
-                                 _p(cached_lens), _p(starts), _p(offsets), _p(k_out), _p(v_out), _p(workspace),
-                                 workspace.nbytes, c.stream)
-    _lib.check(rc, "hstu_kv_read_q4")
+    guard, raw = _on_device(dev, stream)
+    shape = (total_tokens, H, d)
+    if k_out is None:
+        k_out = _empty(shape, dtype, dev, stream)
+    else:
+        _need("k_out", k_out, dtype, shape)
+    if v_out is None:
+        v_out = _empty(shape, dtype, dev, stream)
+    else:
+        _need("v_out", v_out, dtype, shape)
+    p = ctypes.byref(_q4_kv_params(k_pool, page_table, dtype, 0, total_tokens))
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _empty((int(lib.hstu_kv_q4_workspace_size(p)),), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(lib.hstu_kv_read_q4, "hstu_kv_read_q4", guard, p, k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
+          v_scales.data_ptr(), page_table.data_ptr(), cached_lens.data_ptr(), starts.data_ptr(), offsets.data_ptr(),
+          k_out.data_ptr(), v_out.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
     return k_out, v_out
 
 
@@ -583,60 +596,61 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
                            max_cached_len: Optional[int] = None, out=None, workspace=None, raw_av: bool = False,
                            force_simt: bool = False, precise_silu: bool = False, stream=None):
     """hstu_attn_fwd_paged over a prefix held in 4 bits (see hstu_kv_append_q4)."""
-    if q.dim() != 3 or q.dtype not in _DT or k.shape != q.shape or v.shape != q.shape:
-        raise ValueError("q, k and v must be bf16 or fp32 [T, H, d] tensors of one shape")
-    T, H, d = q.shape
+    dev = _one_device((("q", q), ("k", k), ("v", v), ("u", u), ("new_offsets", new_offsets), ("timestamps", timestamps),
+                       ("ts_offsets", ts_offsets), ("rab_pos", rab_pos), ("rab_ts", rab_ts), ("k_pool", k_pool),
+                       ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales),
+                       ("kv_page_table", kv_page_table), ("cached_lens", cached_lens),
+                       ("num_candidates", num_candidates), ("ln_gamma", ln_gamma), ("ln_beta", ln_beta), ("out", out),
+                       ("workspace", workspace)))
     dt = q.dtype
-    for name, t in (("q", q), ("k", k), ("v", v), ("u", u)):
-        _need_cuda(name, t, dt)
-    if tuple(u.shape) != (T, H * d):
-        raise ValueError(f"u must be [T, H*d] = {(T, H * d)}, got {tuple(u.shape)}")
+    if q.dim() != 3 or dt not in _DT or k.shape != q.shape or v.shape != q.shape or k.dtype != dt or v.dtype != dt:
+        raise ValueError("q, k and v must be bf16 or fp32 [T, H, d] tensors of one shape and type")
+    T, H, d = q.shape
+    D = H * d
+    if tuple(u.shape) != (T, D) or u.dtype != dt or (u.stride(1) != 1 and u.numel()):
+        raise ValueError(f"u must be a {dt} [{T}, {D}] matrix with contiguous rows, got {u.dtype} {tuple(u.shape)}")
     _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
     _page_table("kv_page_table", kv_page_table)
-    B = kv_page_table.shape[0]
-    _int_vector("new_offsets", new_offsets, B + 1)
-    _int_vector("ts_offsets", ts_offsets, B + 1)
-    _int_vector("cached_lens", cached_lens, B)
-    _int_vector("num_candidates", num_candidates, B)
-    _need_cuda("timestamps", timestamps, torch.int64)
-    for name, t, n in (("rab_pos", rab_pos, 2 * n_max - 1), ("rab_ts", rab_ts, None), ("ln_gamma", ln_gamma, H * d),
-                       ("ln_beta", ln_beta, H * d)):
-        _need_cuda(name, t, torch.float32)
-        if t is not None and (not t.is_contiguous() or (n is not None and t.numel() != n)):
-            raise ValueError(f"{name} must be contiguous" + (f" with {n} entries" if n is not None else ""))
-    if not timestamps.is_contiguous():
-        raise ValueError("timestamps must be contiguous")
-    qs = _rows_view("q", q, H, d)
-    if _rows_view("k", k, H, d) != qs or _rows_view("v", v, H, d) != qs:
+    B, max_pages = kv_page_table.shape
+    _ints("new_offsets", new_offsets, B + 1)
+    _ints("ts_offsets", ts_offsets, B + 1)
+    _ints("cached_lens", cached_lens, B)
+    if num_candidates is not None:
+        _ints("num_candidates", num_candidates, B)
+    if timestamps.dtype != torch.int64 or timestamps.dim() != 1 or not timestamps.is_contiguous():
+        raise ValueError("timestamps must be a contiguous int64 vector")
+    _need("rab_pos", rab_pos, torch.float32, (2 * n_max - 1,))
+    _need("rab_ts", rab_ts, torch.float32, (rab_ts.numel(),))
+    for name, t in (("ln_gamma", ln_gamma), ("ln_beta", ln_beta)):
+        if t is not None:
+            _need(name, t, torch.float32, (D,))
+    qs = _token_rows("q", q, H, d)
+    if _token_rows("k", k, H, d) != qs or _token_rows("v", v, H, d) != qs:
         raise ValueError("q, k and v must share one token stride")
     flags = ((_lib.F_OUTPUT_RAW_AV if raw_av else 0) | (_lib.F_FORCE_SIMT if force_simt else 0) |
              (_lib.F_PRECISE_SILU if precise_silu else 0))
-    with _call_on(stream, q, k, v, u, new_offsets, timestamps, ts_offsets, rab_pos, rab_ts, k_pool, v_pool, k_scales,
-                  v_scales, kv_page_table, cached_lens, num_candidates, ln_gamma, ln_beta, out, workspace) as c:
-        params = attn_params(batch=B, num_heads=H, head_dim=d, n_max=n_max, total_tokens=T,
-                             max_seq_len=n_max if max_seq_len is None else max_seq_len, dtype=dt, alpha=alpha,
-                             num_ts_buckets=rab_ts.numel(), qkv_stride=qs, u_stride=_rows_view("u", u, H, d),
-                             ln_eps=ln_eps, flags=flags)
-        lib = _lib.load()
-        if num_splits is None:
-            num_splits = lib.hstu_attn_paged_q4_default_splits(ctypes.byref(params),
-                                                               n_max if max_cached_len is None else max_cached_len)
-        shape, odt = ((T, H, d), torch.float32) if raw_av else ((T, H * d), dt)
-        if out is None:
-            out = c.empty(shape, odt)
-        else:
-            _need_out("out", out, shape, odt)
-        if workspace is None:
-            workspace = c.empty((int(lib.hstu_attn_paged_q4_workspace_size(ctypes.byref(params), num_splits)),),
-                                torch.uint8)
-        else:
-            _need_workspace(workspace)
-        rc = lib.hstu_attn_fwd_paged_q4(
-            ctypes.byref(params), _p(q), _p(k), _p(v), _p(u), _p(new_offsets), _p(timestamps), _p(ts_offsets),
-            _p(num_candidates), _p(rab_pos), _p(rab_ts), _p(ln_gamma), _p(ln_beta), _p(k_pool), _p(v_pool),
-            _p(k_scales), _p(v_scales), k_pool.shape[0], _p(kv_page_table), kv_page_table.shape[1], k_pool.shape[2],
-            _p(cached_lens), num_splits, _p(out), _p(workspace), workspace.nbytes, c.stream)
-    _lib.check(rc, "hstu_attn_fwd_paged_q4")
+    guard, raw = _on_device(dev, stream)
+    p = ctypes.byref(_lib.AttnParams(B, H, d, n_max, rab_ts.numel(), T, n_max if max_seq_len is None else max_seq_len,
+                                     qs, u.stride(0) if T > 1 else D, d ** -0.5 if alpha is None else alpha, ln_eps,
+                                     _DT[dt], flags))
+    lib = _lib.load()
+    if num_splits is None:
+        num_splits = lib.hstu_attn_paged_q4_default_splits(p, n_max if max_cached_len is None else max_cached_len)
+    shape, odt = ((T, H, d), torch.float32) if raw_av else ((T, D), dt)
+    if out is None:
+        out = _empty(shape, odt, dev, stream)
+    else:
+        _need("out", out, odt, shape)
+    if workspace is None:
+        workspace = _empty((int(lib.hstu_attn_paged_q4_workspace_size(p, num_splits)),), torch.uint8, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _call(lib.hstu_attn_fwd_paged_q4, "hstu_attn_fwd_paged_q4", guard, p, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          u.data_ptr(), new_offsets.data_ptr(), timestamps.data_ptr(), ts_offsets.data_ptr(), _ptr(num_candidates),
+          rab_pos.data_ptr(), rab_ts.data_ptr(), _ptr(ln_gamma), _ptr(ln_beta), k_pool.data_ptr(), v_pool.data_ptr(),
+          k_scales.data_ptr(), v_scales.data_ptr(), k_pool.shape[0], kv_page_table.data_ptr(), max_pages,
+          k_pool.shape[2], cached_lens.data_ptr(), num_splits, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+          raw)
     return out
 
 
