@@ -91,12 +91,6 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // Row state of the exact time-bucket walk.
 struct Walk {
   long long t_i;   // the row's timestamp
@@ -123,15 +117,11 @@ enum BiasMode { kBiasConst = 0, kBiasEdge = 1, kBiasOct = 2, kBiasWalk = 3 };
 //   kBiasOct:   every column's bucket from the octave table (|dt| + 1 < 2^32)
 //   kBiasWalk:  per-column walk over the bucket edges (wider gaps)
 // MASK zeroes the columns past climit.
-// SCALED (keys in 4 bits): ks[c] replaces alpha / 2 as the factor of column c
-// and the weight is multiplied by vs[c] (bf16 pairs), both at the chunk's first
-// column; the mask is then applied last, so that a masked key's scale may be NaN.
-template <int MODE, bool MASK, bool PRECISE, bool SCALED = false>
+template <int MODE, bool MASK, bool PRECISE>
 __device__ __forceinline__ void silu_chunk(const uint32_t* sr, const uint32_t (&pw)[16], uint32_t (&pk)[16],
                                            const long long* ts, int col0, int climit, int pos, float tsb_lo,
                                            float alpha_half, Walk& w, const long long* thr, const float* rts,
-                                           const uint4* oct, const float* ks = nullptr,
-                                           const uint32_t* vs = nullptr) {
+                                           const uint4* oct) {
   const uint64_t ah2 = pk2(alpha_half, alpha_half);
   const uint64_t tsb2 = pk2(w.tsb, w.tsb);
   const unsigned int ti1 = (unsigned int)(w.t_i + 1);  // octave mode: differences fit in 32 bits
@@ -149,21 +139,11 @@ __device__ __forceinline__ void silu_chunk(const uint32_t* sr, const uint32_t (&
       return w.tsb;
     }
   };
-  float4 ks4 = {};
-  uint4 vs4 = {};
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
     uint64_t tb2 = tsb2;
     if constexpr (MODE != kBiasConst) tb2 = pk2(ts_bias(col0 + c), ts_bias(col0 + c + 1));
-    uint64_t f2 = ah2;
-    uint32_t v2 = 0;
-    if constexpr (SCALED) {  // the columns' factors, the same for every lane
-      if (c % 4 == 0) ks4 = *reinterpret_cast<const float4*>(ks + c);
-      if (c % 8 == 0) vs4 = *reinterpret_cast<const uint4*>(vs + c / 2);
-      f2 = c % 4 == 0 ? pk2(ks4.x, ks4.y) : pk2(ks4.z, ks4.w);
-      v2 = c % 8 == 0 ? vs4.x : c % 8 == 2 ? vs4.y : c % 8 == 4 ? vs4.z : vs4.w;
-    }
-    const uint64_t h2 = fma2(pk2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2, tb2);
+    const uint64_t h2 = fma2(pk2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), ah2, tb2);
     float h0, h1;
     upk2(h2, h0, h1);
     const uint32_t pb = pw[c >> 1];
@@ -171,28 +151,21 @@ __device__ __forceinline__ void silu_chunk(const uint32_t* sr, const uint32_t (&
       // fp32: P = hb (1 + tanh hb), one MUFU tanh per score, rounded once to bf16
       h0 += __uint_as_float(pb << 16);
       h1 += __uint_as_float(pb & 0xFFFF0000u);
-      if constexpr (MASK && !SCALED) {  // SiLU(0) = 0 exactly: masking hb masks P
+      if constexpr (MASK) {  // SiLU(0) = 0 exactly: masking hb masks P
         h0 = (col0 + c <= climit) ? h0 : 0.f;
         h1 = (col0 + c + 1 <= climit) ? h1 : 0.f;
       }
       const uint64_t p2 = fma2(pk2(h0, h1), pk2(tanh_approx(h0), tanh_approx(h1)), pk2(h0, h1));
       float p0, p1;
       upk2(p2, p0, p1);
-      if constexpr (SCALED) {
-        p0 *= __uint_as_float(v2 << 16);
-        p1 *= __uint_as_float(v2 & 0xFFFF0000u);
-      }
       pk[c >> 1] = pack_bf16x2(p0, p1);
     } else {
       // packed bf16: one MUFU tanh per two scores; P = hb (1 + tanh hb) as one bf16x2 FMA
       uint32_t hb = add_bf16x2(pack_bf16x2(h0, h1), pb);
-      if constexpr (MASK && !SCALED)
+      if constexpr (MASK)
         hb &= (col0 + c <= climit ? 0x0000FFFFu : 0u) | (col0 + c + 1 <= climit ? 0xFFFF0000u : 0u);
       pk[c >> 1] = fma_bf16x2(hb, tanh_bf16x2(hb), hb);
-      if constexpr (SCALED) pk[c >> 1] = mul_bf16x2(pk[c >> 1], v2);
     }
-    if constexpr (MASK && SCALED)
-      pk[c >> 1] &= (col0 + c <= climit ? 0x0000FFFFu : 0u) | (col0 + c + 1 <= climit ? 0xFFFF0000u : 0u);
   }
   if constexpr (MODE == kBiasOct) {  // the walk state continues from the chunk's last column
     w.b = b_last;
@@ -201,24 +174,19 @@ __device__ __forceinline__ void silu_chunk(const uint32_t* sr, const uint32_t (&
   }
 }
 
-template <bool MASK, bool PRECISE, bool SCALED = false>
+template <bool MASK, bool PRECISE>
 __device__ __forceinline__ void silu_chunk_mode(int mode, const uint32_t* sr, const uint32_t (&pw)[16],
                                                 uint32_t (&pk)[16], const long long* ts, int col0, int climit,
                                                 int pos, float tsb_lo, float alpha_half, Walk& w,
-                                                const long long* thr, const float* rts, const uint4* oct,
-                                                const float* ks = nullptr, const uint32_t* vs = nullptr) {
+                                                const long long* thr, const float* rts, const uint4* oct) {
   if (mode == kBiasConst)
-    silu_chunk<kBiasConst, MASK, PRECISE, SCALED>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct,
-                                               ks, vs);
+    silu_chunk<kBiasConst, MASK, PRECISE>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct);
   else if (mode == kBiasEdge)
-    silu_chunk<kBiasEdge, MASK, PRECISE, SCALED>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct,
-                                               ks, vs);
+    silu_chunk<kBiasEdge, MASK, PRECISE>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct);
   else if (mode == kBiasOct)
-    silu_chunk<kBiasOct, MASK, PRECISE, SCALED>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct,
-                                               ks, vs);
+    silu_chunk<kBiasOct, MASK, PRECISE>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct);
   else
-    silu_chunk<kBiasWalk, MASK, PRECISE, SCALED>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct,
-                                               ks, vs);
+    silu_chunk<kBiasWalk, MASK, PRECISE>(sr, pw, pk, ts, col0, climit, pos, tsb_lo, alpha_half, w, thr, rts, oct);
 }
 
 // Time-bias mode of the chunk starting at col0 for this row, decided by the

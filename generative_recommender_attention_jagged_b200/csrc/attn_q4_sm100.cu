@@ -11,20 +11,18 @@
 // scale of a key is the factor of its column of S (where alpha stood), the scale
 // of a value a factor of its column of P.
 //
-// With 128 rows against a key tile the step is bound by instruction issue (the
-// SiLU and the widening of the codes) and by tanh, not by the cache's bytes
-// (16 KB a tile), so nothing waits on anything for long and the widening is
-// spread over the same 16 elementwise warps:
+// With 128 rows against a key tile the step is bound by instruction issue and by the
+// latencies of its chain (S, SiLU, P), not by the cache's bytes (16 KB a tile):
 //
-//   - each thread copies its own 16 bytes of a K and of a V row (cp.async) into
-//     a place of its own in shared memory two tiles ahead and later widens them
-//     into the 128B-swizzled tile the tensor core reads: no hand-over, no
-//     producer of its own, four lanes a row (64 contiguous bytes).
-//   - the order of one warp at key tile t: bias + SiLU of S(t) -> P(t); widen
-//     K(t + 2) and V(t + 1); request the codes of K(t + 4), V(t + 3).  S is
-//     double-buffered in tensor memory, so while the warps work on S(t) and widen,
-//     the tensor core does O += P(t - 1) V(t - 1) and S(t + 1).
-//   - one warp looks pages, scales and timestamps up for the tiles ahead (KeyInfo,
+//   - eight elementwise warps (two 32-key chunks of each tile each) turn S(t) into P(t).
+//     S is double-buffered in tensor memory, so the tensor core does O += P(t - 1) V(t - 1)
+//     and S(t + 1) meanwhile.
+//   - eight widening warps turn the codes of K(t + 2), V(t + 2) into the 128B-swizzled
+//     bf16 tiles the tensor core reads.  Each thread copies its own 16 bytes of two K and
+//     two V rows (cp.async) into places of its own two tiles ahead, so nothing is handed
+//     over; four lanes a row (64 contiguous bytes).  One set of sixteen warps doing both in
+//     turn took 2.9 us a tile: every warp waits for the same barriers at the same time.
+//   - two warps look pages, scales and timestamps up for the tiles ahead (KeyInfo,
 //     5 stages), one builds the position window (2 stages), one issues the MMAs.
 //
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
@@ -41,13 +39,15 @@
 namespace hstu {
 namespace {
 
-constexpr int kEwWarps = 16;              // 4 warpgroups: one 32-key chunk of every key tile each
-constexpr int kEwThreads = 32 * kEwWarps;
-constexpr int kMmaWarp = kEwWarps;        // MMA issuer, TMEM owner, Q
-constexpr int kKeyWarp = kEwWarps + 1;
-constexpr int kWinWarp = kEwWarps + 2;
-constexpr int kThreads = 32 * (kEwWarps + 3);
+constexpr int kEwWarps = 8;               // 2 warpgroups: two 32-key chunks of every key tile each
+constexpr int kWideWarps = 8;             // 16 key rows of every tile each
+constexpr int kWideThreads = 32 * kWideWarps;
+constexpr int kMmaWarp = kEwWarps + kWideWarps;  // MMA issuer, TMEM owner, Q
+constexpr int kWinWarp = kMmaWarp + 1;
+constexpr int kKeyWarp = kMmaWarp + 2;    // two of them, taking tiles in turn
+constexpr int kThreads = 32 * (kMmaWarp + 4);
 constexpr int kKeyStages = 5;
+constexpr int kFirst = 4;                 // tiles looked up by elementwise warps before the loop
 constexpr int kWinStages = 2;
 constexpr uint32_t kTmemCols = 512;       // S0 [0,128) S1 [128,256) O [256,384)
 
@@ -67,7 +67,7 @@ struct __align__(1024) SmemQ4 {
   uint8_t q[kTileBytes];
   uint8_t k[2][kTileBytes];
   uint8_t v[2][kTileBytes];
-  uint4 codes[2][2][kEwThreads];  // [stage][K, V]: each thread's 16 bytes
+  uint4 codes[2][2][2][kWideThreads];  // [stage][K, V][row of the thread]: each thread's 16 bytes
   KeyInfo key[kKeyStages];
   Window win[kWinStages];
   long long thr[kMaxBuckets];
@@ -75,19 +75,20 @@ struct __align__(1024) SmemQ4 {
   uint4 oct[32];
   uint32_t win_rs[kWinLoads * 16];
   uint64_t bar_q;
-  uint64_t bar_key_full[kKeyStages];   // 32 lanes of the key warp
-  uint64_t bar_key_empty[kKeyStages];  // 16 elementwise warps
-  uint64_t bar_win_full[kWinStages];
-  uint64_t bar_win_empty[kWinStages];
-  uint64_t bar_s_full[2];  // S buffer b written
-  uint64_t bar_p_full[2];  // P in buffer b written (512 threads)
-  uint64_t bar_kv_full;    // 512 threads: phase 0 = K(0), K(1), V(0); phase t + 1 = K(t + 2), V(t + 1)
-  uint64_t bar_pv;         // O += P(t) V(t) completed
+  uint64_t bar_key_full[kKeyStages];   // the warp that looked the tile up
+  uint64_t bar_key_empty[kKeyStages];  // elementwise and widening warps
+  uint64_t bar_win_full[kWinStages];   // the window warp (which has seen the tile's KeyInfo)
+  uint64_t bar_win_empty[kWinStages];  // elementwise warps
+  uint64_t bar_s_full[2];  // S buffer b written: the K stage that it read is free
+  uint64_t bar_p_full[2];  // P in buffer b written (elementwise warps)
+  uint64_t bar_k_full[2];  // widening warps
+  uint64_t bar_v_full[2];
+  uint64_t bar_v_empty[2]; // the A.V GEMM that read the stage completed
   uint64_t bar_o_full;
   uint32_t tmem_base;
   int abort;
   int item_user, item_tile;
-  int scan[20];
+  int scan[kThreads / 32];
 };
 constexpr size_t kSmemBytes = sizeof(SmemQ4) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -99,6 +100,11 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -114,6 +120,197 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t zz) {
 // whether a bf16 pair holds an infinity or NaN
 __device__ __forceinline__ bool not_finite(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
+// One warp's look-up of a tile's keys: lane l has keys l, l + 32, ..
+struct Lookup {
+  const AttnArgs& a;
+  const TileGeom& g;
+  const int32_t* table;
+  int user, head, tb, cnt, step;  // tiles between one look-up and the warp's next
+  bool checks;  // whether this CTA checks the user's timestamps
+  bool sorted = true;
+  int pid[4];
+  long long ts[4], row[4];
+  float ks[4];
+  uint32_t vs[4], zz[4];
+
+  __device__ static __forceinline__ bool in_range(long long x) { return x <= kTsLimit && x >= -kTsLimit; }
+
+  // page ids of a tile's keys, loaded a tile before the scales that they lead to; no branch
+  // stands between the loads of the four keys, so that their latencies overlap
+  __device__ __forceinline__ void load_pages(int t) {
+    const int lane = threadIdx.x & 31;
+    int k0, width;
+    key_tile(g, tb + t, k0, width);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      pid[k] = k0 < g.L ? table[page_index(a, k0 + min(lane + 32 * k, width - 1))] : 0;
+  }
+  // times, scales and zero points of tile t, then the page ids of the warp's next tile
+  __device__ __forceinline__ void scales(int t) {
+    const int lane = threadIdx.x & 31;
+    int k0, width;
+    key_tile(g, tb + t, k0, width);
+    const bool cached = k0 < g.L;
+    uint32_t km[4], vm[4];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = lane + 32 * k, j = k0 + min(c, width - 1), page = page_index(a, j);
+      ts[k] = a.ts[g.tso + j];
+      const bool in = pid[k] >= 0 && pid[k] < a.num_pages;
+      bad |= !in;
+      row[k] = ((long long)(in ? pid[k] : 0) * a.H + head) * a.page_size + (cached ? j - page * a.page_size : 0);
+      km[k] = a.k_scales[row[k]];
+      vm[k] = a.v_scales[row[k]];
+      if (!in || !cached || c >= width) row[k] = -1;
+    }
+    const long long first = checks && lane == 0 && k0 > 0 ? a.ts[g.tso + k0 - 1] : LLONG_MIN;
+    if (bad) report_error(a.hdr, kErrPage, user);
+    if (t + step < cnt) load_pages(t + step);
+    long long last = first;  // timestamp of the key before this lane's first
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool fresh = !cached && lane + 32 * k < width;  // a new token
+      const bool held = row[k] >= 0;
+      ks[k] = held ? 0.5f * a.alpha * meta_scale(km[k]) : fresh ? 0.5f * a.alpha : 0.f;
+      vs[k] = held ? vm[k] & 0xFFFFu : fresh ? 0x3F80u : 0u;
+      // 128 + zero in bf16, exact
+      zz[k] = held ? pack_bf16x2(128.f + meta_zero(km[k]), 128.f + meta_zero(vm[k])) : 0x43004300u;
+      if (checks) {
+        long long before = __shfl_up_sync(~0u, ts[k], 1);
+        if (lane == 0) before = last;
+        last = __shfl_sync(~0u, ts[k], 31);
+        sorted &= ts[k] >= before && in_range(ts[k]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(KeyInfo& key) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = lane + 32 * k;
+      key.ts[c] = ts[k];
+      key.row[c] = row[k];
+      key.ks[c] = ks[k];
+      reinterpret_cast<uint16_t*>(key.vs)[c] = (uint16_t)vs[k];
+      key.zz[c] = zz[k];
+    }
+  }
+};
+
+// Columns at a time.  The size of the loops counts here: a CTA runs six of them at once, and
+// with the weights' code repeated for every mode of the time bias (146 KB) the warps waited for
+// instructions more than for anything else (4.3 of 12 stall cycles an issue); so the bias is
+// added first, in bf16 like the position bias, and one copy of the rest serves all modes.
+constexpr int kCols = 32;
+
+__device__ __noinline__ int bucket_slow(const long long* thr, long long x) { return bucket_search(thr, x); }
+
+// Adds the time bias of kCols columns (0.5 * rab_ts of their buckets, see BiasMode; the chunk's
+// mode is kBiasConst, kBiasEdge or else one bucket a column) to their position bias pw[k] =
+// columns 2 k, 2 k + 1; returns what is left to add to every column.
+__device__ __forceinline__ float add_time_bias(int mode, uint32_t (&pw)[kCols / 2], Walk& w, const long long* ts,
+                                               int left, float tsb_lo, const long long* thr, const float* rts,
+                                               const uint4* oct) {
+  if (mode == kBiasConst) return w.tsb;
+  if (mode == kBiasEdge) {  // `left` columns are before the edge
+    const uint32_t lo = pack_bf16x2(tsb_lo, tsb_lo), hi = pack_bf16x2(w.tsb, w.tsb), mix = pack_bf16x2(tsb_lo, w.tsb);
+#pragma unroll
+    for (int k = 0; k < kCols / 2; ++k)
+      pw[k] = add_bf16x2(pw[k], left >= 2 * k + 2 ? lo : left <= 2 * k ? hi : mix);
+    return 0.f;
+  }
+  int b = 0;
+#pragma unroll
+  for (int k = 0; k < kCols / 2; ++k) {
+    float v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long x = max(w.t_i + 1 - ts[2 * k + e], 1ll);  // later keys only in masked columns
+      b = (x >> 32) == 0 ? bucket_oct(oct, (unsigned int)x) : bucket_slow(thr, x);
+      v[e] = rts[b];
+    }
+    pw[k] = add_bf16x2(pw[k], pack_bf16x2(v[0], v[1]));
+  }
+  // the walk goes on from the last column
+  w.b = b;
+  w.tlim = w.t_i + 1 - thr[b];
+  w.tsb = rts[b];
+  return 0.f;
+}
+
+// kCols scores of one row -> weights times the values' scales (bf16 pairs, over the biases in
+// pw).  ks, vs: the columns' factors (the same for every lane); columns past `limit` get 0,
+// last, so that a masked key's scales may be NaN.
+template <bool MASK, bool PRECISE>
+__device__ __forceinline__ void weights_of(const uint32_t (&sr)[kCols], uint32_t (&pw)[kCols / 2], float tsb,
+                                           const float* ks, const uint32_t* vs, int limit) {
+  const uint64_t tsb2 = pk2(tsb, tsb);
+  float4 ks4 = {};
+  uint4 vs4 = {};
+#pragma unroll
+  for (int c = 0; c < kCols; c += 2) {
+    if (c % 4 == 0) ks4 = *reinterpret_cast<const float4*>(ks + c);
+    if (c % 8 == 0) vs4 = *reinterpret_cast<const uint4*>(vs + c / 2);
+    const uint64_t f2 = c % 4 == 0 ? pk2(ks4.x, ks4.y) : pk2(ks4.z, ks4.w);
+    const uint32_t v2 = c % 8 == 0 ? vs4.x : c % 8 == 2 ? vs4.y : c % 8 == 4 ? vs4.z : vs4.w;
+    float h0, h1;  // half the score, without the position bias
+    upk2(fma2(pk2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2, tsb2), h0, h1);
+    uint32_t p;
+    if constexpr (PRECISE) {
+      h0 += __uint_as_float(pw[c >> 1] << 16);
+      h1 += __uint_as_float(pw[c >> 1] & 0xFFFF0000u);
+      float p0, p1;
+      upk2(fma2(pk2(h0, h1), pk2(tanh_approx(h0), tanh_approx(h1)), pk2(h0, h1)), p0, p1);
+      p = pack_bf16x2(p0 * __uint_as_float(v2 << 16), p1 * __uint_as_float(v2 & 0xFFFF0000u));
+    } else {
+      const uint32_t hb = add_bf16x2(pack_bf16x2(h0, h1), pw[c >> 1]);
+      p = mul_bf16x2(fma_bf16x2(hb, tanh_bf16x2(hb), hb), v2);
+    }
+    if constexpr (MASK) p &= (c <= limit ? 0x0000FFFFu : 0u) | (c + 1 <= limit ? 0xFFFF0000u : 0u);
+    pw[c >> 1] = p;
+  }
+}
+
+// The bounded wait (as mbar_wait: about 2 s, or until another warp gave up), out of line and
+// with a hint to sleep up to 20 us a try: a waiting warp that polls takes issue slots from the
+// working ones, and inlined at every wait the code came to 9 KB.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abort, WsHeader* hdr, int where) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (abort != nullptr && *(volatile int*)abort) return false;
+    if (global_timer_ns() - t0 > 2000000000ull) {
+      if (abort != nullptr) *(volatile int*)abort = 1;
+      report_error(hdr, kErrTimeout, where);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, int* abort, WsHeader* hdr, int where) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, hdr, where);
+}
+// A warp waits for a phase: one lane polls (32 lanes of 16 waiting warps polling keep the
+// shared-memory pipe from the warps that work), the others follow.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, WsHeader* hdr, int where) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = lane_wait(bar, parity, abort, hdr, where);
+  return __shfl_sync(~0u, ok, 0);
+}
+// A warp arrives once, when all its lanes are there.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // The user and 128-row tile of the qt-th query tile of the batch (all threads;
@@ -179,23 +376,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cnt = max(0, te - tb);
   const int prmin = min(g.qs, g.h);
   const int32_t* table = a.page_table + (size_t)user * a.max_pages;
+  // head 0 of the user's last tile (it sees every key but the candidates) checks the timestamps on the way
+  const bool checks = head == 0 && (sm.item_tile + 1) * kTile >= g.n - g.L;
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int s = 0; s < kKeyStages; ++s) {
-      mbar_init(&sm.bar_key_full[s], 32);
-      mbar_init(&sm.bar_key_empty[s], kEwWarps);
+      mbar_init(&sm.bar_key_full[s], 1);
+      mbar_init(&sm.bar_key_empty[s], kEwWarps + kWideWarps);
     }
     for (int s = 0; s < kWinStages; ++s) {
-      mbar_init(&sm.bar_win_full[s], 32);
+      mbar_init(&sm.bar_win_full[s], 1);
       mbar_init(&sm.bar_win_empty[s], kEwWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.bar_s_full[b], 1);
-      mbar_init(&sm.bar_p_full[b], kEwThreads);
+      mbar_init(&sm.bar_p_full[b], kEwWarps);
+      mbar_init(&sm.bar_k_full[b], kWideWarps);
+      mbar_init(&sm.bar_v_full[b], kWideWarps);
+      mbar_init(&sm.bar_v_empty[b], 1);
     }
-    mbar_init(&sm.bar_kv_full, kEwThreads);
-    mbar_init(&sm.bar_pv, 1);
     mbar_init(&sm.bar_o_full, 1);
     sm.abort = 0;
     fence_barrier_init();
@@ -208,98 +408,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  volatile int* abort_flag = &sm.abort;
+  int* abort_flag = &sm.abort;
   const int row_base = a.q_offsets[user] - g.L;  // row of key position p is row_base + p (p >= L)
 
-  if (warp == kKeyWarp) {
-    // ------------------------------------------------------------------ key warp
-    // lane l holds keys l, l + 32, ..: looked up one tile ahead of the free stage
-    long long kts[4], krow[4];
-    float kks[4];
-    uint32_t kvs[4], kzz[4];
-    // head 0 of the user's last tile (it sees every key but the candidates) checks the timestamps on the way
-    const bool checks = head == 0 && (sm.item_tile + 1) * kTile >= g.n - g.L;
-    bool sorted = true;
-    auto in_range = [](long long x) { return x <= kTsLimit && x >= -kTsLimit; };
-    long long last_ts = LLONG_MIN;  // timestamp of the key before the tile
-    // page ids of a tile's keys, loaded a tile before the scales that they lead to; no branch
-    // stands between the loads of the four keys, so that their latencies overlap
-    int pid[4];
-    auto load_pages = [&](int t) {
-      int k0, width;
-      key_tile(g, tb + t, k0, width);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        pid[k] = k0 < g.L ? table[page_index(a, k0 + min(lane + 32 * k, width - 1))] : 0;
-    };
-    auto look_up = [&](int t) {
-      int k0, width;
-      key_tile(g, tb + t, k0, width);
-      const bool cached = k0 < g.L;
-      uint32_t km[4], vm[4];
-      bool bad = false;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k, j = k0 + min(c, width - 1), page = page_index(a, j);
-        kts[k] = a.ts[g.tso + j];
-        const bool in = pid[k] >= 0 && pid[k] < a.num_pages;
-        bad |= !in;
-        krow[k] = ((long long)(in ? pid[k] : 0) * a.H + head) * a.page_size + (cached ? j - page * a.page_size : 0);
-        km[k] = a.k_scales[krow[k]];
-        vm[k] = a.v_scales[krow[k]];
-        if (!in || !cached || c >= width) krow[k] = -1;
-      }
-      if (bad) report_error(a.hdr, kErrPage, user);
-      if (t + 1 < cnt) load_pages(t + 1);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool fresh = !cached && lane + 32 * k < width;  // a new token
-        const bool held = krow[k] >= 0;
-        kks[k] = held ? 0.5f * a.alpha * meta_scale(km[k]) : fresh ? 0.5f * a.alpha : 0.f;
-        kvs[k] = held ? vm[k] & 0xFFFFu : fresh ? 0x3F80u : 0u;
-        // 128 + zero in bf16, exact
-        kzz[k] = held ? pack_bf16x2(128.f + meta_zero(km[k]), 128.f + meta_zero(vm[k])) : 0x43004300u;
-        if (checks) {
-          long long before = __shfl_up_sync(~0u, kts[k], 1);
-          if (lane == 0) before = last_ts;
-          last_ts = __shfl_sync(~0u, kts[k], 31);
-          sorted &= kts[k] >= before && in_range(kts[k]);
-        }
-      }
-    };
-    if (checks && cnt > 0) {
-      int k0, width;
-      key_tile(g, tb, k0, width);
-      if (k0 > 0) last_ts = a.ts[g.tso + k0 - 1];
-    }
-    if (cnt > 0) {
-      load_pages(0);
-      look_up(0);
-    }
-    for (int t = 0; t < cnt; ++t) {
+  // ------------------------------------------------------------------ look-ups
+  // The key warps take tiles kFirst, .. in turn, looked up before their stage is free; the first
+  // tiles fall to elementwise warps, one each, so that their latencies overlap.
+  if (warp >= kKeyWarp || warp < kFirst) {
+    Lookup look{a, g, table, user, head, tb, cnt, 2, checks};
+    const int t0 = warp < kFirst ? warp : kFirst + warp - kKeyWarp, end = warp < kFirst ? min(cnt, warp + 1) : cnt;
+    if (t0 < end) look.load_pages(t0);
+#pragma unroll 1
+    for (int t = t0; t < end; t += 2) {
       const int s = t % kKeyStages;
-      bool ok = true;
-      if (lane == 0 && t >= kKeyStages)
-        ok = mbar_wait(&sm.bar_key_empty[s], ((t / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51);
-      ok = __shfl_sync(~0u, ok, 0);
-      if (!ok) break;
-      KeyInfo& key = sm.key[s];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = lane + 32 * k;
-        key.ts[c] = kts[k];
-        key.row[c] = krow[k];
-        key.ks[c] = kks[k];
-        reinterpret_cast<uint16_t*>(key.vs)[c] = (uint16_t)kvs[k];
-        key.zz[c] = kzz[k];
-      }
-      mbar_arrive(&sm.bar_key_full[s]);
-      if (t + 1 < cnt) look_up(t + 1);
+      look.scales(t);
+      if (t >= kKeyStages && !warp_wait(&sm.bar_key_empty[s], ((t / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51)) break;
+      look.store(sm.key[s]);
+      warp_arrive(&sm.bar_key_full[s]);
     }
-    if (checks && split == a.num_splits - 1)  // the candidates, which are no tile's keys
+    if (checks && split == a.num_splits - 1 && warp == kKeyWarp)  // the candidates, which are no tile's keys
       for (int j = g.h + lane; j < g.n; j += 32)
-        sorted &= in_range(a.ts[g.tso + j]) && (j == 0 || a.ts[g.tso + j] >= a.ts[g.tso + j - 1]);
-    if (!sorted) report_error(a.hdr, kErrUnsorted, user);
+        look.sorted &= Lookup::in_range(a.ts[g.tso + j]) && (j == 0 || a.ts[g.tso + j] >= a.ts[g.tso + j - 1]);
+    if (!look.sorted) report_error(a.hdr, kErrUnsorted, user);
+  }
+  if (warp >= kKeyWarp) {
   } else if (warp == kWinWarp) {
     // ------------------------------------------------------------------ position window (see Meta in attn_common.cuh)
     const int n_rab = 2 * a.n_max - 1;
@@ -317,11 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (cnt > 0) load_win(0);
     for (int t = 0; t < cnt; ++t) {
       const int s = t % kWinStages;
-      bool ok = true;
-      if (lane == 0 && t >= kWinStages)
-        ok = mbar_wait(&sm.bar_win_empty[s], ((t / kWinStages) & 1) ^ 1, abort_flag, a.hdr, 52);
-      ok = __shfl_sync(~0u, ok, 0);
-      if (!ok) break;
+      if (t >= kWinStages && !warp_wait(&sm.bar_win_empty[s], ((t / kWinStages) & 1) ^ 1, abort_flag, a.hdr, 52)) break;
       Window& m = sm.win[s];
       __syncwarp();
       uint16_t* rs16 = reinterpret_cast<uint16_t*>(sm.win_rs);
@@ -337,7 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m.win[f][p] = make_uint4(__funnelshift_r(x0, x1, sh), __funnelshift_r(x1, x2, sh), __funnelshift_r(x2, x3, sh),
                                  __funnelshift_r(x3, x4, sh));
       }
-      mbar_arrive(&sm.bar_win_full[s]);
+      // whoever sees this barrier has seen the tile's KeyInfo too
+      if (!warp_wait(&sm.bar_key_full[t % kKeyStages], (t / kKeyStages) & 1, abort_flag, a.hdr, 52)) break;
+      warp_arrive(&sm.bar_win_full[s]);
       if (t + 1 < cnt) load_win(t + 1);
     }
   } else if (warp == kMmaWarp) {
@@ -364,248 +494,242 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + 256, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8,
                  sw128_desc(v_base + kk * 2048, kHalfBytes, 1024), idesc_pv, (t > 0 || kk > 0));
+        mma_commit(&sm.bar_v_empty[t & 1]);
       };
       // Q has landed before anything else uses it (and before the CTA may exit)
-      bool ok = mbar_wait(&sm.bar_q, 0, abort_flag, a.hdr, 53);
-      if (ok && cnt > 0) ok = mbar_wait(&sm.bar_kv_full, 0, abort_flag, a.hdr, 54);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < min(cnt, 2); ++t) issue_s(t);
-      }
-      for (int t = 0; ok && t < cnt; ++t) {
-        ok = mbar_wait(&sm.bar_p_full[t & 1], (t >> 1) & 1, abort_flag, a.hdr, 55);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(t);  // V(t): phase t of kv_full, waited for below (t - 1) or above (0)
-        if (t + 1 < cnt) {
-          // the commit comes after this wait: with it the elementwise warps could be
-          // through the next phase of kv_full before this thread looked at this one
-          ok = mbar_wait(&sm.bar_kv_full, (t + 1) & 1, abort_flag, a.hdr, 54);
+      bool ok = lane_wait(&sm.bar_q, 0, abort_flag, a.hdr, 53);
+#pragma unroll 1
+      for (int t = -2; ok && t < cnt; ++t) {
+        if (t >= 0) {
+          ok = lane_wait(&sm.bar_p_full[t & 1], (t >> 1) & 1, abort_flag, a.hdr, 55) &&
+               lane_wait(&sm.bar_v_full[t & 1], (t >> 1) & 1, abort_flag, a.hdr, 55);
           if (!ok) break;
-          mma_commit(&sm.bar_pv);
           tc_fence_after();
-          if (t + 2 < cnt) issue_s(t + 2);
+          issue_pv(t);
+        }
+        if (t + 2 < cnt) {  // into the buffer whose P the GEMM above has read
+          ok = lane_wait(&sm.bar_k_full[t & 1], ((t + 2) >> 1) & 1, abort_flag, a.hdr, 54);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(t + 2);
         }
       }
       mma_commit(&sm.bar_o_full);
-      mbar_wait(&sm.bar_o_full, 0, nullptr, a.hdr, 58);
-      mbar_wait(&sm.bar_q, 0, nullptr, a.hdr, 58);
+      lane_wait(&sm.bar_o_full, 0, nullptr, a.hdr, 58);
+      lane_wait(&sm.bar_q, 0, nullptr, a.hdr, 58);
     }
     __syncwarp();
+  } else if (warp >= kEwWarps) {
+    // ------------------------------------------------------------------ widening warps
+    const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool);
+    const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool);
+    const int wt = threadIdx.x - 32 * kEwWarps;
+    // rows wr and wr + 8 and a quarter (32 dimensions) of each: four lanes a row.  The 16-byte chunk of
+    // dimensions 32 wq + 8 c sits at chunk (4 (wq & 1) + c) ^ (row & 7) of half wq >> 1; threads of the
+    // second half take their words in the order c ^ 2, so that the eight lanes of a quarter-warp store to
+    // eight different places
+    const int wr = 16 * (warp - kEwWarps) + (lane >> 2), wq = lane & 3;
+    const int flip = wq & 2;
+    const uint32_t wbase = (wq >> 1) * kHalfBytes + wr * 128;
+    const int wchunk = 4 * (wq & 1);
+    // the thread's codes of tile t into its own places
+    auto request = [&](int t) {
+      if (t < cnt) {
+        const KeyInfo& key = sm.key[t % kKeyStages];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const long long row = key.row[wr + 8 * x];
+          if (row >= 0) {
+            cp16_ca(&sm.codes[t & 1][0][x][wt], kp + row * 64 + 16 * wq);
+            cp16_ca(&sm.codes[t & 1][1][x][wt], vp + row * 64 + 16 * wq);
+          }
+        }
+      }
+      cp_commit();
+    };
+    auto store_rows = [&](uint8_t* tile, int t, int which) {  // which: 0 K, 1 V
+      KeyInfo& key = sm.key[t % kKeyStages];
+      int k0, width;
+      key_tile(g, tb + t, k0, width);
+      if (k0 < g.L) {  // cached keys
+        uint4 w[2];
+        uint32_t zz[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          w[x] = sm.codes[t & 1][which][x][wt];
+          const uint32_t z = key.zz[wr + 8 * x];
+          zz[x] = __byte_perm(z, z, which ? 0x3232 : 0x1010);
+          // (rows past the width: what an earlier tile left, finite numbers under scales of 0)
+          if (flip) w[x] = make_uint4(w[x].z, w[x].w, w[x].x, w[x].y);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t base = smem_u32(tile) + wbase + x * 8 * 128;
+          const uint32_t ww[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sts_v4(base + (((wchunk + (c ^ flip)) ^ (wr & 7)) << 4), widen8(ww[c], zz[x]));
+        }
+      } else {  // new tokens: bf16 rows as they are (zeros past the width)
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int r = wr + 8 * x;
+          const bool on = r < width;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(which ? a.v : a.k) +
+                                                            (size_t)(row_base + k0 + (on ? r : 0)) * a.qkv_stride +
+                                                            head * kHeadDim + 32 * wq);
+          uint4 w[4];
+          bool bad = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            w[c] = on ? src[c] : make_uint4(0, 0, 0, 0);
+            bad |= not_finite(w[c].x) | not_finite(w[c].y) | not_finite(w[c].z) | not_finite(w[c].w);
+          }
+          if (which) {  // a value row that is not finite: zeros, and a weight of NaN for the rows that see it
+            bad = __any_sync(0xFu << (lane & ~3), bad);
+            if (bad && wq == 0) reinterpret_cast<uint16_t*>(key.vs)[r] = 0x7FC0u;
+          }
+          const uint32_t base = smem_u32(tile) + wbase + x * 8 * 128;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sts_v4(base + (((wchunk + c) ^ (wr & 7)) << 4), which && bad ? make_uint4(0, 0, 0, 0) : w[c]);
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    auto key_ready = [&](int t) -> bool {
+      return t >= cnt || warp_wait(&sm.bar_key_full[t % kKeyStages], (t / kKeyStages) & 1, abort_flag, a.hdr, 56);
+    };
+    bool ok = cnt > 0;
+#pragma unroll 1
+    for (int t = -2; ok && t < cnt; ++t) {
+      const int b = t & 1;
+      if (t >= 0) {
+      cp_wait<1>();
+      // K(t) over K(t - 2), which S(t - 2) has read; then V(t) over V(t - 2)
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
+        if (t >= 2) ok = warp_wait(which ? &sm.bar_v_empty[b] : &sm.bar_s_full[b], ((t - 2) >> 1) & 1, abort_flag, a.hdr, 57);
+        if (!ok) break;
+        store_rows(which ? sm.v[b] : sm.k[b], t, which);
+        warp_arrive(which ? &sm.bar_v_full[b] : &sm.bar_k_full[b]);
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(&sm.bar_key_empty[t % kKeyStages]);
+      }
+      ok = key_ready(t + 2);
+      if (ok) request(t + 2);
+    }
+    cp_wait<0>();
   } else {
     // ------------------------------------------------------------------ elementwise warps
-    for (int x = threadIdx.x; x < kMaxBuckets; x += kEwThreads) {
+    for (int x = threadIdx.x; x < kMaxBuckets; x += 32 * kEwWarps) {
       sm.thr[x] = tab.thr[x];
       sm.rab_ts_half[x] = x < a.nb ? 0.5f * a.rab_ts[x] : 0.f;
     }
     if (threadIdx.x < 32)
       sm.oct[threadIdx.x] = make_uint4(tab.oct[threadIdx.x][0], tab.oct[threadIdx.x][1], tab.oct[threadIdx.x][2],
                                        tab.oct[threadIdx.x][3]);
-    named_bar_sync(5, kEwThreads);
-    const int grp = warp >> 2;                // warpgroup = 32-key chunk of every key tile
+    named_bar_sync(5, 32 * kEwWarps);
+    const int grp = warp >> 2;                // warpgroup = 64-key half of every key tile
     const int r = threadIdx.x & (kTile - 1);  // query row of the tile == TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const int i = min(g.qs + r, g.n - 1);
     const int jmax = i < g.h ? i : g.h - 1;
     const int pr = min(i, g.h);
     const int zb = prmin + 255 - pr;
-    const int col0 = 32 * grp;
-    const uint8_t* kp = static_cast<const uint8_t*>(a.k_pool);
-    const uint8_t* vp = static_cast<const uint8_t*>(a.v_pool);
-
-    // ---- widening: this thread's key row and quarter (32 dimensions) of every tile
-    const int wr = 8 * warp + (lane >> 2), wq = lane & 3;
-    // the 16-byte chunk of dimensions 32 wq + 8 c sits at chunk (4 (wq & 1) + c) ^ (wr & 7) of half wq >> 1;
-    // threads of the second half take their words in the order c ^ 2, so that the eight lanes of a
-    // quarter-warp store to eight different places
-    const int flip = wq & 2;
-    const uint32_t wbase = (wq >> 1) * kHalfBytes + wr * 128;
-    const int wchunk = 4 * (wq & 1);
-    auto request = [&](int t, int which) {  // codes of K (0) or V (1) of tile t into this thread's place
-      if (t >= cnt) return;
-      const long long row = sm.key[t % kKeyStages].row[wr];
-      if (row >= 0) cp16_ca(&sm.codes[t & 1][which][threadIdx.x], (which ? vp : kp) + row * 64 + 16 * wq);
-    };
-    auto store_row = [&](uint8_t* tile, int t, int which) {
-      KeyInfo& key = sm.key[t % kKeyStages];
-      const uint32_t base = smem_u32(tile) + wbase;
-      int k0, width;
-      key_tile(g, tb + t, k0, width);
-      if (k0 < g.L) {  // cached keys: codes (zeros for rows past the width)
-        uint4 w = make_uint4(0, 0, 0, 0);
-        uint32_t zz = 0x43004300u;
-        if (key.row[wr] >= 0) {
-          w = sm.codes[t & 1][which][threadIdx.x];
-          const uint32_t z = key.zz[wr];
-          zz = __byte_perm(z, z, which ? 0x3232 : 0x1010);
-        }
-        if (flip) w = make_uint4(w.z, w.w, w.x, w.y);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sts_v4(base + (((wchunk + (c ^ flip)) ^ (wr & 7)) << 4), widen8(ww[c], zz));
-      } else {  // new tokens: bf16 rows as they are (zeros past the width)
-        const bool on = wr < width;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(which ? a.v : a.k) +
-                                                          (size_t)(row_base + k0 + (on ? wr : 0)) * a.qkv_stride +
-                                                          head * kHeadDim + 32 * wq);
-        uint4 w[4];
-        bool bad = false;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          w[c] = on ? src[c] : make_uint4(0, 0, 0, 0);
-          bad |= not_finite(w[c].x) | not_finite(w[c].y) | not_finite(w[c].z) | not_finite(w[c].w);
-        }
-        if (which) {  // a value row that is not finite: zeros, and a weight of NaN for the rows that see it
-          bad = __any_sync(0xFu << (lane & ~3), bad);
-          if (bad && wq == 0) reinterpret_cast<uint16_t*>(key.vs)[wr] = 0x7FC0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          sts_v4(base + (((wchunk + c) ^ (wr & 7)) << 4), which && bad ? make_uint4(0, 0, 0, 0) : w[c]);
-      }
-    };
-    auto key_ready = [&](int t) -> bool {
-      return t >= cnt || mbar_wait(&sm.bar_key_full[t % kKeyStages], (t / kKeyStages) & 1, abort_flag, a.hdr, 56);
-    };
-
-    bool ok = true;
-    // first tiles: K(0), K(1), V(0) now; the codes of K(2), V(1) and K(3), V(2) on their way
-    if (cnt > 0) {
-      ok = key_ready(0) && key_ready(1) && key_ready(2) && key_ready(3);
-      ok = ew_all(ok, grp);
-      if (ok) {
-        request(0, 0);
-        request(1, 0);
-        request(0, 1);
-        cp_commit();
-        cp_wait<0>();
-        store_row(sm.k[0], 0, 0);
-        if (cnt > 1) store_row(sm.k[1], 1, 0);
-        store_row(sm.v[0], 0, 1);
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.bar_kv_full);
-        request(2, 0);
-        request(1, 1);
-        cp_commit();
-        request(3, 0);
-        request(2, 1);
-        cp_commit();
-      }
-    }
     Walk w;
     w.t_i = a.ts[g.tso + i];
     w.b = 0;
     w.tlim = 0;
     w.tsb = 0.f;
-    // (leaving the loop is agreed on by the warpgroup: ew_all)
-    const int steps = ok ? cnt : 0;
-    for (int t = 0; t < steps; ++t) {
+    bool ok = true;
+    for (int t = 0; t < cnt; ++t) {
       const int b = t & 1;
       int k0, width;
       key_tile(g, tb + t, k0, width);
-      ok = ok && mbar_wait(&sm.bar_win_full[t % kWinStages], (t / kWinStages) & 1, abort_flag, a.hdr, 56);
-      ok = ok && mbar_wait(&sm.bar_s_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
-      // a tile of new tokens: every thread has seen its value rows (the NaN scales)
-      if (k0 >= g.L) ok = ok && mbar_wait(&sm.bar_kv_full, t & 1, abort_flag, a.hdr, 56);
-      ok = ew_all(ok, grp);
+      ok = warp_wait(&sm.bar_win_full[t % kWinStages], (t / kWinStages) & 1, abort_flag, a.hdr, 56);
+      ok = ok && warp_wait(&sm.bar_s_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
+      // a tile of new tokens: the NaN scales of its value rows are set
+      if (k0 >= g.L) ok = ok && warp_wait(&sm.bar_v_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
       if (!ok) break;
       tc_fence_after();
       const KeyInfo& key = sm.key[t % kKeyStages];
       const Window& m = sm.win[t % kWinStages];
       const int climit = min(jmax - k0, width - 1);  // columns c <= climit are allowed
       const uint32_t s_tmem = tmem + lane_base + b * 128;
-      uint32_t sr[32];
-      tmem_ld32(s_tmem + col0, sr);
       if (t == 0) {
-        w.b = bucket_of_dt(sm.thr, w.t_i - key.ts[min(col0, width - 1)]);
+        w.b = bucket_of_dt(sm.thr, w.t_i - key.ts[min(64 * grp, width - 1)]);
         w.tlim = w.t_i + 1 - sm.thr[w.b];
         w.tsb = sm.rab_ts_half[w.b];
       }
-      const bool need_mask = !__all_sync(~0u, climit >= col0 + 31);
-      int pos;
-      float tsb_lo;
-      const int mode = chunk_mode(w, key.ts, col0, climit, sm.thr, sm.rab_ts_half, pos, tsb_lo);
-      const int z0 = zb + col0;
-      const uint32_t winb = smem_u32(&m.win[z0 >> 3][z0 & 7]);
-      uint32_t pw[16];
+#pragma unroll 1
+      for (int col0 = 64 * grp; col0 < 64 * grp + 64; col0 += kCols) {
+        uint32_t sr[kCols];
+        tmem_ld32(s_tmem + col0, sr);
+        int pos;
+        float tsb_lo;
+        const int mode = chunk_mode(w, key.ts, col0, climit, sm.thr, sm.rab_ts_half, pos, tsb_lo);
+        const int z0 = zb + col0;
+        const uint32_t winb = smem_u32(&m.win[z0 >> 3][z0 & 7]);
+        uint32_t pw[kCols / 2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint4 v4 = lds_v4(winb + k * 8 * 16);
-        pw[4 * k] = v4.x;
-        pw[4 * k + 1] = v4.y;
-        pw[4 * k + 2] = v4.z;
-        pw[4 * k + 3] = v4.w;
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v4 = lds_v4(winb + k * 8 * 16);
+          pw[4 * k] = v4.x;
+          pw[4 * k + 1] = v4.y;
+          pw[4 * k + 2] = v4.z;
+          pw[4 * k + 3] = v4.w;
+        }
+        const float tsb = add_time_bias(mode, pw, w, key.ts + col0, pos - col0, tsb_lo, sm.thr, sm.rab_ts_half, sm.oct);
+        tmem_wait_ld(sr);
+        if (!__all_sync(~0u, climit >= col0 + kCols - 1))
+          weights_of<true, PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2, climit - col0);
+        else
+          weights_of<false, PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2, 0);
+        // the chunk's P goes over the first 16 of its own (read) columns
+        tmem_st16(s_tmem + col0, pw);
       }
-      tmem_wait_ld(sr);
-      uint32_t pk[16];
-      const float* ks = key.ks + col0;
-      const uint32_t* vs = key.vs + col0 / 2;
-      if (need_mask)
-        silu_chunk_mode<true, PRECISE, true>(mode, sr, pw, pk, key.ts, col0, climit, pos, tsb_lo, 0.f, w, sm.thr,
-                                             sm.rab_ts_half, sm.oct, ks, vs);
-      else
-        silu_chunk_mode<false, PRECISE, true>(mode, sr, pw, pk, key.ts, col0, climit, pos, tsb_lo, 0.f, w, sm.thr,
-                                              sm.rab_ts_half, sm.oct, ks, vs);
-      tmem_st16(s_tmem + col0, pk);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sm.bar_p_full[b]);
-      // ---- K(t + 2) over K(t) (S(t) has read it), V(t + 1) over V(t - 1)
-      if (t + 1 < cnt) {
-        cp_wait<1>();
-        if (t + 2 < cnt) store_row(sm.k[b], t + 2, 0);
-        if (t > 0) ok = mbar_wait(&sm.bar_pv, (t - 1) & 1, abort_flag, a.hdr, 57);
-        ok = ew_all(ok, grp);
-        if (!ok) break;
-        store_row(sm.v[b ^ 1], t + 1, 1);
-        fence_proxy_async_smem();
-        mbar_arrive(&sm.bar_kv_full);
-      }
-      // the stages of tile t are free; the codes two tiles further are asked for
-      __syncwarp();
+      warp_arrive(&sm.bar_p_full[b]);
       if (lane == 0) {
         mbar_arrive(&sm.bar_key_empty[t % kKeyStages]);
         mbar_arrive(&sm.bar_win_empty[t % kWinStages]);
       }
-      ok = key_ready(t + 4);
-      ok = __all_sync(~0u, ok);
-      if (ok) {
-        request(t + 4, 0);
-        request(t + 3, 1);
-      }
-      cp_commit();
     }
-    cp_wait<0>();
-    if (ok && cnt > 0) {
-      ok = ew_all(mbar_wait(&sm.bar_o_full, 0, abort_flag, a.hdr, 57), grp);
-      tc_fence_after();
-    } else if (ok) {
-      ok = ew_all(mbar_wait(&sm.bar_q, 0, abort_flag, a.hdr, 57), grp);  // the staging below is over Q
-    }
+    // with no key tile nothing waited for Q, which the staging below is over
+    ok = ok && warp_wait(cnt > 0 ? &sm.bar_o_full : &sm.bar_q, 0, abort_flag, a.hdr, 57);
+    ok = ew_all(ok, grp);  // the warps left the loop by themselves
+    tc_fence_after();
     if (ok) {
-      // O out through shared memory in whole row segments (as attn_sm100_single.cu)
-      const uint32_t stage = (grp < 2 ? smem_u32(sm.q) : smem_u32(sm.k[0])) + (grp & 1) * (kTileBytes / 2);
+      // O out through shared memory in whole row segments (as attn_sm100_single.cu), 32 columns at a time
+      const uint32_t stage = grp == 0 ? smem_u32(sm.q) : smem_u32(sm.k[0]);
       const int wrank = warp & 3;
-      uint32_t orr[32];
-      if (cnt > 0) {
-        tmem_ld32(tmem + lane_base + 256 + col0, orr);
-        tmem_wait_ld(orr);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) orr[e] = 0u;
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        sts_v4(stage + r * 128 + ((c ^ (r & 7)) << 4),
-               make_uint4(orr[4 * c], orr[4 * c + 1], orr[4 * c + 2], orr[4 * c + 3]));
-      named_bar_sync(1 + grp, kTile);
 #pragma unroll 1
-      for (int rr = 4 * wrank + (lane >> 3); rr < kTile; rr += 16) {
-        const int c = lane & 7;
-        if (rr < g.nq_rows) {
-          const uint4 val = lds_v4(stage + rr * 128 + ((c ^ (rr & 7)) << 4));
-          float* orow = a.o_ws + (((size_t)split * a.T_q + (g.qrow0 + rr)) * a.H + head) * kHeadDim;
-          *reinterpret_cast<uint4*>(orow + col0 + 4 * c) = val;
+      for (int x = 0; x < 2; ++x) {
+        const int col0 = 64 * grp + 32 * x;
+        const uint32_t slab = stage + x * (kTileBytes / 2);
+        uint32_t orr[32];
+        if (cnt > 0) {
+          tmem_ld32(tmem + lane_base + 256 + col0, orr);
+          tmem_wait_ld(orr);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) orr[e] = 0u;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          sts_v4(slab + r * 128 + ((c ^ (r & 7)) << 4),
+                 make_uint4(orr[4 * c], orr[4 * c + 1], orr[4 * c + 2], orr[4 * c + 3]));
+        named_bar_sync(1 + grp, kTile);
+#pragma unroll 1
+        for (int rr = 4 * wrank + (lane >> 3); rr < kTile; rr += 16) {
+          const int c = lane & 7;
+          if (rr < g.nq_rows) {
+            const uint4 val = lds_v4(slab + rr * 128 + ((c ^ (rr & 7)) << 4));
+            float* orow = a.o_ws + (((size_t)split * a.T_q + (g.qrow0 + rr)) * a.H + head) * kHeadDim;
+            *reinterpret_cast<uint4*>(orow + col0 + 4 * c) = val;
+          }
         }
       }
     }

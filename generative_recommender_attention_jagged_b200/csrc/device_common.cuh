@@ -86,9 +86,11 @@ __device__ __forceinline__ TileGeom tile_geom(const AttnArgs& a, int user, int q
   return g;
 }
 
-// page of position j and j's slot in it (a division is ~20 instructions)
+// Page of position j: with s = ceil(log2(page_size)) and mul = ceil(2^(31+s) / page_size),
+// mul * page_size exceeds 2^(31+s) by less than 2^s, which j < 2^31 does not carry into the
+// quotient.  (A division is ~20 instructions.)
 __device__ __forceinline__ int page_index(const AttnArgs& a, int j) {
-  return a.page_shift >= 0 ? j >> a.page_shift : j / a.page_size;
+  return (int)(((unsigned long long)(unsigned)j * a.page_mul) >> a.page_shift);
 }
 
 // key tile t of a query tile: first key position and number of keys

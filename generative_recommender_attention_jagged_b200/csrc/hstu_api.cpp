@@ -223,9 +223,12 @@ int run(const hstu_attn_params* p, const Common& c) {
   a.paged = c.paged ? 1 : 0;
   a.num_splits = tc ? c.splits : 1;
   a.page_size = c.page_size;
-  a.page_shift = -1;
-  for (int b = 0; b < 31; ++b)
-    if (c.page_size == 1 << b) a.page_shift = b;
+  if (c.page_size > 0) {  // see page_index
+    int bits = 0;
+    while (bits < 31 && (1 << bits) < c.page_size) ++bits;
+    a.page_shift = 31 + bits;
+    a.page_mul = (uint32_t)(((1ull << a.page_shift) + (uint32_t)c.page_size - 1) / (uint32_t)c.page_size);
+  }
   a.num_pages = c.num_pages;
   a.max_pages = c.max_pages;
   a.max_items = l.max_items;

@@ -65,7 +65,8 @@ struct AttnArgs {
   int32_t paged;        // 0 = jagged full sequence, 1 = paged prefix + new tokens
   int32_t num_splits;
   int32_t page_size, num_pages, max_pages;
-  int32_t page_shift;   // log2(page_size), or -1 where it is no power of two (4-bit kernels)
+  uint32_t page_mul;    // j / page_size = (j * page_mul) >> page_shift for 0 <= j < 2^31 (4-bit kernels)
+  int32_t page_shift;
   int32_t max_items;
   int32_t item_tiles;   // query tiles per work item: 2 (two-tile kernel) or 1 (one-tile kernel)
   int32_t out_raw;      // write o (fp32 [T,H,d]) instead of y
