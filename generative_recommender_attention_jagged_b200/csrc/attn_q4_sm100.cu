@@ -22,8 +22,9 @@
 //     two V rows (cp.async) into places of its own two tiles ahead, so nothing is handed
 //     over; four lanes a row (64 contiguous bytes).  One set of sixteen warps doing both in
 //     turn took 2.9 us a tile: every warp waits for the same barriers at the same time.
-//   - two warps look pages, scales and timestamps up for the tiles ahead (KeyInfo,
-//     5 stages), one builds the position window (2 stages), one issues the MMAs.
+//   - they also look the tiles' pages, scales and timestamps up (KeyInfo, 4 stages: page id,
+//     scales and codes each a tile ahead of the next); one more warp builds the position
+//     window (2 stages), one issues the MMAs.
 //
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
 // row that is not finite is stored as zeros and its scale set to NaN: the mask is
@@ -44,20 +45,17 @@ constexpr int kWideWarps = 8;             // 16 key rows of every tile each
 constexpr int kWideThreads = 32 * kWideWarps;
 constexpr int kMmaWarp = kEwWarps + kWideWarps;  // MMA issuer, TMEM owner, Q
 constexpr int kWinWarp = kMmaWarp + 1;
-constexpr int kKeyWarp = kMmaWarp + 2;    // two of them, taking tiles in turn
-constexpr int kThreads = 32 * (kMmaWarp + 4);
-constexpr int kKeyStages = 5;
-constexpr int kFirst = 4;                 // tiles looked up by elementwise warps before the loop
+constexpr int kThreads = 32 * (kMmaWarp + 2);
+constexpr int kKeyStages = 4;
 constexpr int kWinStages = 2;
+constexpr int kTailTiles = 4;             // what a user's last tiles cost beyond the others, in tiles
 constexpr uint32_t kTmemCols = 512;       // S0 [0,128) S1 [128,256) O [256,384)
 
-// What the key warp finds out about a tile's keys.
+// What the elementwise warps need of a tile's keys.
 struct KeyInfo {
   long long ts[kTile];    // timestamps (the last one repeated past the tile's width)
-  long long row[kTile];   // pool row (page, head, slot) of a cached key, or -1
   float ks[kTile];        // alpha / 2 times the scale of the key (new tokens: alpha / 2); 0 past the width
   uint32_t vs[kTile / 2]; // bf16 pairs: scale of the value (new tokens: 1); 0 past the width
-  uint32_t zz[kTile];     // bf16 128 + zero of the key | of the value
 };
 struct Window {
   uint4 win[kWinChunks][8];
@@ -75,8 +73,8 @@ struct __align__(1024) SmemQ4 {
   uint4 oct[32];
   uint32_t win_rs[kWinLoads * 16];
   uint64_t bar_q;
-  uint64_t bar_key_full[kKeyStages];   // the warp that looked the tile up
-  uint64_t bar_key_empty[kKeyStages];  // elementwise and widening warps
+  uint64_t bar_key_full[kKeyStages];   // widening warps
+  uint64_t bar_key_empty[kKeyStages];  // elementwise warps
   uint64_t bar_win_full[kWinStages];   // the window warp (which has seen the tile's KeyInfo)
   uint64_t bar_win_empty[kWinStages];  // elementwise warps
   uint64_t bar_s_full[2];  // S buffer b written: the K stage that it read is free
@@ -122,84 +120,6 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
 
-// One warp's look-up of a tile's keys: lane l has keys l, l + 32, ..
-struct Lookup {
-  const AttnArgs& a;
-  const TileGeom& g;
-  const int32_t* table;
-  int user, head, tb, cnt, step;  // tiles between one look-up and the warp's next
-  bool checks;  // whether this CTA checks the user's timestamps
-  bool sorted = true;
-  int pid[4];
-  long long ts[4], row[4];
-  float ks[4];
-  uint32_t vs[4], zz[4];
-
-  __device__ static __forceinline__ bool in_range(long long x) { return x <= kTsLimit && x >= -kTsLimit; }
-
-  // page ids of a tile's keys, loaded a tile before the scales that they lead to; no branch
-  // stands between the loads of the four keys, so that their latencies overlap
-  __device__ __forceinline__ void load_pages(int t) {
-    const int lane = threadIdx.x & 31;
-    int k0, width;
-    key_tile(g, tb + t, k0, width);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      pid[k] = k0 < g.L ? table[page_index(a, k0 + min(lane + 32 * k, width - 1))] : 0;
-  }
-  // times, scales and zero points of tile t, then the page ids of the warp's next tile
-  __device__ __forceinline__ void scales(int t) {
-    const int lane = threadIdx.x & 31;
-    int k0, width;
-    key_tile(g, tb + t, k0, width);
-    const bool cached = k0 < g.L;
-    uint32_t km[4], vm[4];
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = lane + 32 * k, j = k0 + min(c, width - 1), page = page_index(a, j);
-      ts[k] = a.ts[g.tso + j];
-      const bool in = pid[k] >= 0 && pid[k] < a.num_pages;
-      bad |= !in;
-      row[k] = ((long long)(in ? pid[k] : 0) * a.H + head) * a.page_size + (cached ? j - page * a.page_size : 0);
-      km[k] = a.k_scales[row[k]];
-      vm[k] = a.v_scales[row[k]];
-      if (!in || !cached || c >= width) row[k] = -1;
-    }
-    const long long first = checks && lane == 0 && k0 > 0 ? a.ts[g.tso + k0 - 1] : LLONG_MIN;
-    if (bad) report_error(a.hdr, kErrPage, user);
-    if (t + step < cnt) load_pages(t + step);
-    long long last = first;  // timestamp of the key before this lane's first
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool fresh = !cached && lane + 32 * k < width;  // a new token
-      const bool held = row[k] >= 0;
-      ks[k] = held ? 0.5f * a.alpha * meta_scale(km[k]) : fresh ? 0.5f * a.alpha : 0.f;
-      vs[k] = held ? vm[k] & 0xFFFFu : fresh ? 0x3F80u : 0u;
-      // 128 + zero in bf16, exact
-      zz[k] = held ? pack_bf16x2(128.f + meta_zero(km[k]), 128.f + meta_zero(vm[k])) : 0x43004300u;
-      if (checks) {
-        long long before = __shfl_up_sync(~0u, ts[k], 1);
-        if (lane == 0) before = last;
-        last = __shfl_sync(~0u, ts[k], 31);
-        sorted &= ts[k] >= before && in_range(ts[k]);
-      }
-    }
-  }
-  __device__ __forceinline__ void store(KeyInfo& key) const {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = lane + 32 * k;
-      key.ts[c] = ts[k];
-      key.row[c] = row[k];
-      key.ks[c] = ks[k];
-      reinterpret_cast<uint16_t*>(key.vs)[c] = (uint16_t)vs[k];
-      key.zz[c] = zz[k];
-    }
-  }
-};
-
 // Columns at a time.  The size of the loops counts here: a CTA runs six of them at once, and
 // with the weights' code repeated for every mode of the time bias (146 KB) the warps waited for
 // instructions more than for anything else (4.3 of 12 stall cycles an issue); so the bias is
@@ -242,11 +162,10 @@ __device__ __forceinline__ float add_time_bias(int mode, uint32_t (&pw)[kCols / 
 }
 
 // kCols scores of one row -> weights times the values' scales (bf16 pairs, over the biases in
-// pw).  ks, vs: the columns' factors (the same for every lane); columns past `limit` get 0,
-// last, so that a masked key's scales may be NaN.
-template <bool MASK, bool PRECISE>
+// pw).  ks, vs: the columns' factors (the same for every lane).
+template <bool PRECISE>
 __device__ __forceinline__ void weights_of(const uint32_t (&sr)[kCols], uint32_t (&pw)[kCols / 2], float tsb,
-                                           const float* ks, const uint32_t* vs, int limit) {
+                                           const float* ks, const uint32_t* vs) {
   const uint64_t tsb2 = pk2(tsb, tsb);
   float4 ks4 = {};
   uint4 vs4 = {};
@@ -269,7 +188,6 @@ __device__ __forceinline__ void weights_of(const uint32_t (&sr)[kCols], uint32_t
       const uint32_t hb = add_bf16x2(pack_bf16x2(h0, h1), pw[c >> 1]);
       p = mul_bf16x2(fma_bf16x2(hb, tanh_bf16x2(hb), hb), v2);
     }
-    if constexpr (MASK) p &= (c <= limit ? 0x0000FFFFu : 0u) | (c + 1 <= limit ? 0xFFFF0000u : 0u);
     pw[c >> 1] = p;
   }
 }
@@ -313,14 +231,34 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The user and 128-row tile of the qt-th query tile of the batch (all threads;
-// thread x sums the tiles of its share of users, the warps' sums meet in sm.scan).
+// The user and 128-row tile of the qt-th query tile of the batch, into sm.item_user (-1: none) and
+// sm.item_tile; all threads.  Up to kThreads users are taken in the order of their lengths, longest
+// first, so that the last CTAs to start are short ones; larger batches, which have many CTAs an SM
+// anyway, in their own order.
 __device__ __forceinline__ void find_item(const AttnArgs& a, SmemQ4& sm, int qt) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int* len = reinterpret_cast<int*>(sm.q);  // the tiles of shared memory are free so far
+  int* user = len + kThreads;
+  const bool sorted = a.B <= kThreads;
+  auto tiles_of = [&](int u) {
+    return max(0, (int)(((long long)a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile));
+  };
+  if (tid == 0) sm.item_user = -1;
+  if (sorted) {
+    const int mine = tid < a.B ? a.cached_lens[tid] : 0;
+    len[tid] = mine;
+    __syncthreads();
+    if (tid < a.B) {
+      int rank = 0;
+      for (int u = 0; u < a.B; ++u) rank += len[u] > mine || (len[u] == mine && u < tid);
+      user[rank] = tid;
+    }
+    __syncthreads();
+  }
   const int per = (a.B + kThreads - 1) / kThreads;
-  const int lo = min(a.B, (int)threadIdx.x * per), hi = min(a.B, lo + per);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
   int mine = 0;
-  for (int u = lo; u < hi; ++u) mine += max(0, (int)(((long long)a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile));
+  for (int x = lo; x < hi; ++x) mine += tiles_of(sorted ? user[x] : x);
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -328,14 +266,13 @@ __device__ __forceinline__ void find_item(const AttnArgs& a, SmemQ4& sm, int qt)
     if (lane >= o) incl += y;
   }
   if (lane == 31) sm.scan[warp] = incl;
-  if (threadIdx.x == 0) sm.item_user = -1;
   __syncthreads();
   int before = incl - mine;
   for (int w = 0; w < warp; ++w) before += sm.scan[w];
   if (qt >= before && qt < before + mine) {
     int at = before;
-    for (int u = lo; u < hi; ++u) {
-      const int tiles = max(0, (int)(((long long)a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile));
+    for (int x = lo; x < hi; ++x) {
+      const int u = sorted ? user[x] : x, tiles = tiles_of(u);
       if (qt < at + tiles) {
         sm.item_user = u;
         sm.item_tile = qt - at;
@@ -371,8 +308,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const TileGeom g = tile_geom(a, user, sm.item_tile);
+  // The last tiles (recent keys: a bucket edge every few columns; masked and new ones) take two to
+  // three times the others' time: they count for more when the keys are split.
   int tb, te;
-  split_range(g.n_tiles, split, a.num_splits, tb, te);
+  const int tail = g.n_tiles >= 4 * a.num_splits ? kTailTiles : 0;
+  split_range(g.n_tiles + tail, split, a.num_splits, tb, te);
+  tb = min(tb, g.n_tiles);
+  te = min(te, g.n_tiles);
   const int cnt = max(0, te - tb);
   const int prmin = min(g.qs, g.h);
   const int32_t* table = a.page_table + (size_t)user * a.max_pages;
@@ -382,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
     for (int s = 0; s < kKeyStages; ++s) {
-      mbar_init(&sm.bar_key_full[s], 1);
-      mbar_init(&sm.bar_key_empty[s], kEwWarps + kWideWarps);
+      mbar_init(&sm.bar_key_full[s], kWideWarps);
+      mbar_init(&sm.bar_key_empty[s], kEwWarps);
     }
     for (int s = 0; s < kWinStages; ++s) {
       mbar_init(&sm.bar_win_full[s], 1);
@@ -411,28 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* abort_flag = &sm.abort;
   const int row_base = a.q_offsets[user] - g.L;  // row of key position p is row_base + p (p >= L)
 
-  // ------------------------------------------------------------------ look-ups
-  // The key warps take tiles kFirst, .. in turn, looked up before their stage is free; the first
-  // tiles fall to elementwise warps, one each, so that their latencies overlap.
-  if (warp >= kKeyWarp || warp < kFirst) {
-    Lookup look{a, g, table, user, head, tb, cnt, 2, checks};
-    const int t0 = warp < kFirst ? warp : kFirst + warp - kKeyWarp, end = warp < kFirst ? min(cnt, warp + 1) : cnt;
-    if (t0 < end) look.load_pages(t0);
-#pragma unroll 1
-    for (int t = t0; t < end; t += 2) {
-      const int s = t % kKeyStages;
-      look.scales(t);
-      if (t >= kKeyStages && !warp_wait(&sm.bar_key_empty[s], ((t / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51)) break;
-      look.store(sm.key[s]);
-      warp_arrive(&sm.bar_key_full[s]);
-    }
-    if (checks && split == a.num_splits - 1 && warp == kKeyWarp)  // the candidates, which are no tile's keys
-      for (int j = g.h + lane; j < g.n; j += 32)
-        look.sorted &= Lookup::in_range(a.ts[g.tso + j]) && (j == 0 || a.ts[g.tso + j] >= a.ts[g.tso + j - 1]);
-    if (!look.sorted) report_error(a.hdr, kErrUnsorted, user);
-  }
-  if (warp >= kKeyWarp) {
-  } else if (warp == kWinWarp) {
+  if (warp == kWinWarp) {
     // ------------------------------------------------------------------ position window (see Meta in attn_common.cuh)
     const int n_rab = 2 * a.n_max - 1;
     float mwin[kWinLoads];
@@ -532,20 +453,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int flip = wq & 2;
     const uint32_t wbase = (wq >> 1) * kHalfBytes + wr * 128;
     const int wchunk = 4 * (wq & 1);
-    // the thread's codes of tile t into its own places
-    auto request = [&](int t) {
-      if (t < cnt) {
-        const KeyInfo& key = sm.key[t % kKeyStages];
+    // The warp looks its 16 keys up itself, one a lane (lanes 16 .. 31 as lanes 0 .. 15): page id,
+    // then scales and time, then the codes, each a tile ahead of the next.
+    const int kc = 16 * (warp - kEwWarps) + (lane & 15);
+    int pid = 0;
+    long long row = -1, ts = 0, ts_before = 0;
+    uint32_t km = 0, vm = 0;
+    uint32_t zz0 = 0, zz1 = 0, zz2 = 0;  // 128 + zero of key | value as bf16: of the tile being widened and the next two
+    bool sorted = true;
+    auto in_range = [](long long x) { return x <= kTsLimit && x >= -kTsLimit; };
+    auto load_page = [&](int t) {
+      int k0, width;
+      key_tile(g, tb + t, k0, width);
+      pid = k0 < g.L ? table[page_index(a, k0 + min(kc, width - 1))] : 0;
+    };
+    auto load_scales = [&](int t) {
+      int k0, width;
+      key_tile(g, tb + t, k0, width);
+      const int j = k0 + min(kc, width - 1);
+      const bool in = pid >= 0 && pid < a.num_pages;
+      if (!in) report_error(a.hdr, kErrPage, user);
+      row = ((long long)(in ? pid : 0) * a.H + head) * a.page_size + (k0 < g.L ? j - page_index(a, j) * a.page_size : 0);
+      km = a.k_scales[row];
+      vm = a.v_scales[row];
+      ts = a.ts[g.tso + j];
+      ts_before = checks && j > 0 ? a.ts[g.tso + j - 1] : LLONG_MIN;
+      if (!in || k0 >= g.L || kc >= width) row = -1;
+    };
+    // tile t's KeyInfo, and its codes into this thread's own places
+    auto announce = [&](int t) {
+      int k0, width;
+      key_tile(g, tb + t, k0, width);
+      KeyInfo& key = sm.key[t % kKeyStages];
+      const bool held = row >= 0, fresh = k0 >= g.L && kc < width;  // cached; a new token
+      sorted &= !checks || (ts >= ts_before && in_range(ts));
+      if (lane < 16) {
+        key.ts[kc] = ts;
+        key.ks[kc] = held ? 0.5f * a.alpha * meta_scale(km) : fresh ? 0.5f * a.alpha : 0.f;
+        reinterpret_cast<uint16_t*>(key.vs)[kc] = (uint16_t)(held ? vm : fresh ? 0x3F80u : 0u);
+      }
+      zz2 = held ? pack_bf16x2(128.f + meta_zero(km), 128.f + meta_zero(vm)) : 0x43004300u;  // exact
+      warp_arrive(&sm.bar_key_full[t % kKeyStages]);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const long long row = key.row[wr + 8 * x];
-          if (row >= 0) {
-            cp16_ca(&sm.codes[t & 1][0][x][wt], kp + row * 64 + 16 * wq);
-            cp16_ca(&sm.codes[t & 1][1][x][wt], vp + row * 64 + 16 * wq);
-          }
+      for (int x = 0; x < 2; ++x) {
+        const long long r = __shfl_sync(~0u, row, (lane >> 2) + 8 * x);
+        if (r >= 0) {
+          cp16_ca(&sm.codes[t & 1][0][x][wt], kp + r * 64 + 16 * wq);
+          cp16_ca(&sm.codes[t & 1][1][x][wt], vp + r * 64 + 16 * wq);
         }
       }
-      cp_commit();
     };
     auto store_rows = [&](uint8_t* tile, int t, int which) {  // which: 0 K, 1 V
       KeyInfo& key = sm.key[t % kKeyStages];
@@ -557,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           w[x] = sm.codes[t & 1][which][x][wt];
-          const uint32_t z = key.zz[wr + 8 * x];
+          const uint32_t z = __shfl_sync(~0u, zz0, (lane >> 2) + 8 * x);
           zz[x] = __byte_perm(z, z, which ? 0x3232 : 0x1010);
           // (rows past the width: what an earlier tile left, finite numbers under scales of 0)
           if (flip) w[x] = make_uint4(w[x].z, w[x].w, w[x].x, w[x].y);
@@ -596,29 +552,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
     };
-    auto key_ready = [&](int t) -> bool {
-      return t >= cnt || warp_wait(&sm.bar_key_full[t % kKeyStages], (t / kKeyStages) & 1, abort_flag, a.hdr, 56);
-    };
-    bool ok = cnt > 0;
+    bool ok = true;
 #pragma unroll 1
-    for (int t = -2; ok && t < cnt; ++t) {
+    for (int t = -4; ok && t < cnt; ++t) {
       const int b = t & 1;
+      zz0 = zz1;
+      zz1 = zz2;
       if (t >= 0) {
-      cp_wait<1>();
-      // K(t) over K(t - 2), which S(t - 2) has read; then V(t) over V(t - 2)
+        cp_wait<1>();
+        // K(t) over K(t - 2), which S(t - 2) has read; then V(t) over V(t - 2)
 #pragma unroll 1
-      for (int which = 0; which < 2; ++which) {
-        if (t >= 2) ok = warp_wait(which ? &sm.bar_v_empty[b] : &sm.bar_s_full[b], ((t - 2) >> 1) & 1, abort_flag, a.hdr, 57);
+        for (int which = 0; which < 2; ++which) {
+          if (t >= 2)
+            ok = warp_wait(which ? &sm.bar_v_empty[b] : &sm.bar_s_full[b], ((t - 2) >> 1) & 1, abort_flag, a.hdr, 57);
+          if (!ok) break;
+          store_rows(which ? sm.v[b] : sm.k[b], t, which);
+          warp_arrive(which ? &sm.bar_v_full[b] : &sm.bar_k_full[b]);
+        }
         if (!ok) break;
-        store_rows(which ? sm.v[b] : sm.k[b], t, which);
-        warp_arrive(which ? &sm.bar_v_full[b] : &sm.bar_k_full[b]);
       }
-      if (!ok) break;
-      if (lane == 0) mbar_arrive(&sm.bar_key_empty[t % kKeyStages]);
+      if (t + 2 >= 0 && t + 2 < cnt) {
+        const int s = (t + 2) % kKeyStages;
+        if (t + 2 >= kKeyStages)
+          ok = warp_wait(&sm.bar_key_empty[s], (((t + 2) / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51);
+        if (!ok) break;
+        announce(t + 2);
       }
-      ok = key_ready(t + 2);
-      if (ok) request(t + 2);
+      if (t >= -2) cp_commit();
+      if (t + 3 >= 0 && t + 3 < cnt) load_scales(t + 3);
+      if (t + 4 < cnt) load_page(t + 4);
     }
+    if (checks && split == a.num_splits - 1 && warp == kEwWarps)  // the candidates, which are no tile's keys
+      for (int j = g.h + lane; j < g.n; j += 32)
+        sorted &= in_range(a.ts[g.tso + j]) && (j == 0 || a.ts[g.tso + j] >= a.ts[g.tso + j - 1]);
+    if (!sorted) report_error(a.hdr, kErrUnsorted, user);
     cp_wait<0>();
   } else {
     // ------------------------------------------------------------------ elementwise warps
@@ -682,10 +649,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float tsb = add_time_bias(mode, pw, w, key.ts + col0, pos - col0, tsb_lo, sm.thr, sm.rab_ts_half, sm.oct);
         tmem_wait_ld(sr);
-        if (!__all_sync(~0u, climit >= col0 + kCols - 1))
-          weights_of<true, PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2, climit - col0);
-        else
-          weights_of<false, PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2, 0);
+        weights_of<PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2);
+        if (!__all_sync(~0u, climit >= col0 + kCols - 1)) {
+          // the mask comes last: a masked key's scales, and so its weight, may be NaN
+#pragma unroll
+          for (int k = 0; k < kCols / 2; ++k) {
+            const int left = climit - col0 - 2 * k;  // columns allowed after the pair's first
+            pw[k] &= left >= 1 ? ~0u : left == 0 ? 0x0000FFFFu : 0u;
+          }
+        }
         // the chunk's P goes over the first 16 of its own (read) columns
         tmem_st16(s_tmem + col0, pw);
       }

@@ -417,12 +417,12 @@ int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max
   const Q4Kernel kernel = q4_kernel_for(p);
   if (kernel == kQ4Simt) return 1;
   if (kernel == kQ4Tc) {
-    // one wave of CTAs while there are few tiles; otherwise two halves of every
-    // tile, so that the last wave is short
+    // one wave of CTAs while there are few tiles, whole key ranges otherwise (a
+    // CTA's start and end cost about three key tiles)
     const long long tiles = std::max<long long>(p->batch, (p->total_tokens + kTile - 1) / kTile);
     const long long units = tiles * p->num_heads;
     const long long key_tiles = std::max(1, (max_cached_len + kTile - 1) / kTile);
-    const long long s = std::max<long long>(units >= num_sms() ? 2 : 1, num_sms() / units);
+    const long long s = std::max<long long>(1, num_sms() / units);
     return (int32_t)std::max<long long>(1, std::min<long long>({s, (key_tiles + 1) / 2, kMaxSplits}));
   }
   // about eight CTAs an SM: two waves of them even out users of different length
