@@ -158,9 +158,13 @@ __device__ __forceinline__ void split3(float x, float (&y)[3]) {
   }
 }
 
+__device__ __noinline__ int bucket_slow(const long long* thr, long long dt) { return bucket_of_dt(thr, dt); }
+
+// rab_ts of the bucket of t_i - t_j: the octave table for differences of 0 .. 2^32 - 2 (the search
+// stays out of line, it would be unrolled at every score)
 __device__ __forceinline__ float time_bias(const long long* thr, const float* rts, const uint4* oct, long long dt) {
-  const unsigned long long x = abs_dt_plus1(dt);
-  return rts[x < (1ull << 32) ? bucket_oct(oct, (unsigned int)x) : bucket_of_dt(thr, dt)];
+  const unsigned long long x = (unsigned long long)dt + 1;
+  return rts[(x >> 32) == 0 && x != 0 ? bucket_oct(oct, (unsigned int)x) : bucket_slow(thr, dt)];
 }
 
 __device__ __forceinline__ float warp_add(float x) {
@@ -203,22 +207,23 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
   const int32_t* table = a.page_table + (size_t)u * a.max_pages;
   const int64_t* ts = a.ts + tso;
 
-  if (head == 0 && rg == 0) {
-    // this part's page ids and timestamps (the first part also has the new tokens')
+  // this part's page ids and timestamps (the first part also has the new tokens')
+  auto check_keys = [&] {
     for (int x = k_lo / a.page_size + threadIdx.x; x < (k_hi + a.page_size - 1) / a.page_size; x += kThreads) {
       const int pid = table[x];
       if (pid < 0 || pid >= a.num_pages) report_error(a.hdr, kErrPage, u);
     }
-    auto check_ts = [&](int lo, int hi) {
-      for (int j = lo + threadIdx.x; j < hi; j += kThreads) {
-        const long long x = ts[j];
-        if (x > kTsLimit || x < -kTsLimit || (j > 0 && x < ts[j - 1])) report_error(a.hdr, kErrUnsorted, u);
-      }
-    };
-    check_ts(k_lo, k_hi);
-    if (split == 0) check_ts(L, n);
+    for (int x = threadIdx.x; x < k_hi - k_lo + (split == 0 ? n - L : 0); x += kThreads) {
+      const int j = x < k_hi - k_lo ? k_lo + x : L + x - (k_hi - k_lo);
+      const long long t = ts[j];
+      if (t > kTsLimit || t < -kTsLimit || (j > 0 && t < ts[j - 1])) report_error(a.hdr, kErrUnsorted, u);
+    }
+  };
+  const bool checks = head == 0 && rg == 0;
+  if (rows == 0) {
+    if (checks) check_keys();
+    return;
   }
-  if (rows == 0) return;
 
   for (int x = threadIdx.x; x < kMaxBuckets; x += kThreads) {
     sm.thr[x] = tab.thr[x];
@@ -302,15 +307,17 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
         // a page id out of range is reported above; its rows are not touched
         const bool on = j < k_hi && pid >= 0 && pid < a.num_pages;
         Stage<D>& st = ring[m % kRing];
-        const long long slot =
-            on ? ((long long)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : -1;
+        // (the pool has fewer than 2^32 rows: attn_q4_small_supported)
+        const uint32_t slot =
+            on ? ((uint32_t)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : ~0u;
         constexpr int kPieces = D / 32;  // 16-byte pieces of a row
 #pragma unroll
         for (int x = 0; x < kPieces; ++x) {
           const int c = 32 * x + lane, row = c / kPieces, piece = c % kPieces;
-          const long long s = __shfl_sync(~0u, slot, row);
-          cp16(st.k + row * (D / 2) + piece * 16, kp + (s < 0 ? 0 : s) * (D / 2) + piece * 16, s >= 0);
-          cp16(st.v + row * Stage<D>::kVRow + piece * 16, vp + (s < 0 ? 0 : s) * (D / 2) + piece * 16, s >= 0);
+          const uint32_t s = __shfl_sync(~0u, slot, row);
+          const size_t from = s == ~0u ? 0 : (size_t)s * (D / 2) + piece * 16;
+          cp16(st.k + row * (D / 2) + piece * 16, kp + from, s != ~0u);
+          cp16(st.v + row * Stage<D>::kVRow + piece * 16, vp + from, s != ~0u);
         }
         cp4(&st.km[lane], a.k_scales + (on ? slot : 0), on);
         cp4(&st.vm[lane], a.v_scales + (on ? slot : 0), on);
@@ -514,21 +521,35 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       const bool cand = i >= hist;
       const int j_end = cand ? hist : i + 1;
       const long long ti = ts[i];
-      for (int jj = L; jj <= j_end; ++jj) {
-        int j = jj;
-        if (jj == j_end) {
-          if (!cand) break;
-          j = i;
+      // its keys L .. j_end - 1, and a candidate's own; four at a time, so that their loads overlap
+      const int count = j_end - L + (cand ? 1 : 0);
+#pragma unroll 1
+      for (int c0 = 0; c0 < count; c0 += 4) {
+        float dot[4];
+        int j[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int x = min(c0 + c, count - 1);
+          j[c] = L + x < j_end ? L + x : i;
+          const T* kr = kn + (size_t)(q0 + j[c] - L) * a.qkv_stride + head * D + kPer * lane;
+          dot[c] = 0.f;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) dot[c] = fmaf(qv[e], as_f(kr[e]), dot[c]);
         }
-        const size_t kr = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
-        float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) dot = fmaf(qv[e], as_f(kn[kr + e]), dot);
-        const float sc = a.alpha * warp_add(dot) + a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1] +
-                         time_bias(sm.thr, sm.rts, sm.oct, ti - ts[j]);
-        const float wt = silu_of<T>(sc);
+        for (int o = 16; o >= 1; o >>= 1)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, as_f(vn[kr + e]), acc[e]);
+          for (int c = 0; c < 4; ++c) dot[c] += __shfl_xor_sync(~0u, dot[c], o);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c0 + c < count) {  // (nothing of a key past the last is used)
+            const T* vr = vn + (size_t)(q0 + j[c] - L) * a.qkv_stride + head * D + kPer * lane;
+            const float sc = a.alpha * dot[c] + a.rab_pos[min(i, hist) - min(j[c], hist) + a.n_max - 1] +
+                             time_bias(sm.thr, sm.rts, sm.oct, ti - ts[j[c]]);
+            const float wt = silu_of<T>(sc);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, as_f(vr[e]), acc[e]);
+          }
       }
 #pragma unroll
       for (int e = 0; e < kPer; ++e) sm.self[r][kPer * lane + e] = acc[e];
@@ -557,6 +578,8 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
     __syncthreads();
   }
 
+  if (checks) check_keys();  // (the keys' own loads have them in the caches by now)
+
   // ---- the last CTA of the user adds the parts, normalises and gates
   __threadfence();
   __syncthreads();
@@ -566,24 +589,31 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
   __threadfence();
   const int HD = a.H * D;  // a multiple of 32, at most 1024
   const float inv_n = 1.f / (float)a.n_max;
+#pragma unroll 1
   for (int r = warp; r < rows; r += kWarps) {
     const size_t row = q0 + r;
     float2 x[16];
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      x[k] = make_float2(0.f, 0.f);
-      if (64 * k + 2 * lane < HD) {
-        const float* src = a.o_ws + row * HD + 64 * k + 2 * lane;
-        for (int s = 0; s < parts; ++s) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(src + (size_t)s * a.T_q * HD));
-          x[k].x += y.x;
-          x[k].y += y.y;
-        }
-        x[k].x *= inv_n;
-        x[k].y *= inv_n;
-        sum += x[k].x + x[k].y;
+    for (int k = 0; k < 16; ++k) x[k] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int s = 0; s < parts; ++s) {  // the features' loads are independent
+      const float* src = a.o_ws + ((size_t)s * a.T_q + row) * HD + 2 * lane;
+      float2 y[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        y[k] = 64 * k + 2 * lane < HD ? __ldcg(reinterpret_cast<const float2*>(src + 64 * k)) : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        x[k].x += y[k].x;
+        x[k].y += y[k].y;
       }
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      x[k].x *= inv_n;
+      x[k].y *= inv_n;
+      sum += x[k].x + x[k].y;
     }
     if (a.out_raw) {
       float* out = static_cast<float*>(a.out) + row * HD + 2 * lane;
@@ -646,7 +676,9 @@ cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counter
 
 }  // namespace
 
-bool attn_q4_small_supported(int head_dim, int batch) { return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535; }
+bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
+  return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535 && pool_rows < 0xFFFFFFFFll;
+}
 
 // Rows of one pass over the cached bytes: 16 where users have more than 8 on
 // average (fp32 calls with d > 64: 8, their three-term fragments fill the registers).

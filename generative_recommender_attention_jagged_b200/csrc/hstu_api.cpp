@@ -144,8 +144,10 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
 // kQ4Simt: d > 128, or on request.
 enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 
-Q4Kernel q4_kernel_for(const hstu_attn_params* p) {
-  if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, p->batch)) return kQ4Simt;
+// pool_rows: num_pages * H * page_size, 0 where it is not known yet (workspace sizes: the CUDA-core kernel,
+// which pools of 2^32 rows fall back to, needs the least)
+Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
+  if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, p->batch, pool_rows)) return kQ4Simt;
   return use_tensor_cores(p) && (long long)p->total_tokens > 16ll * p->batch ? kQ4Tc : kQ4Small;
 }
 
@@ -201,7 +203,8 @@ int run(const hstu_attn_params* p, const Common& c) {
   // tensor-core path: whole pages land as 1024-byte-aligned swizzled boxes
   if (tc && c.paged && (c.page_size < 8 || c.page_size > kTile || kTile % c.page_size)) return HSTU_ERR_UNSUPPORTED;
   const int item_tiles = item_tiles_for(p, c.paged);
-  const Q4Kernel q4_kernel = q4 ? q4_kernel_for(p) : kQ4Simt;
+  const Q4Kernel q4_kernel =
+      q4 ? q4_kernel_for(p, (long long)c.num_pages * p->num_heads * c.page_size) : kQ4Simt;
   const Layout l = q4 ? q4_layout_for(p, c.splits, q4_kernel) : layout_for(p, tc ? c.splits : 1, tc, item_tiles);
   if (c.ws_bytes < l.total) return HSTU_ERR_WORKSPACE;
 
