@@ -47,7 +47,7 @@
 //
 // The new rows' own keys are a few: each warp takes rows and does the allowed
 // pairs in fp32 FMAs, so that what a mask hides is never touched.  The CTA that
-// finishes a user last (a counter in the workspace) adds the parts in order,
+// finishes a group of rows last (a counter in the workspace) adds the parts in order,
 // normalises and gates: one launch besides the clearing of the counters.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -179,8 +179,9 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
   return max(kMinPart, ((L + splits - 1) / splits + kKeys - 1) / kKeys * kKeys);
 }
 
+// (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
 template <typename T, int D, int NQ>
-__global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
                                                                  int32_t* counters, int row_groups) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kTerms = kF32 ? 3 : 1;
@@ -541,16 +542,20 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       const int count = j_end - L + (cand ? 1 : 0);
 #pragma unroll 1
       for (int c0 = 0; c0 < count; c0 += 4) {
-        float dot[4];
-        int j[4];
+        float dot[4], bias[4], vv[4][kPer];
+        long long tj[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int x = min(c0 + c, count - 1);
-          j[c] = L + x < j_end ? L + x : i;
-          const T* kr = kn + (size_t)(q0 + j[c] - L) * a.qkv_stride + head * D + kPer * lane;
+          const int x = min(c0 + c, count - 1), j = L + x < j_end ? L + x : i;
+          const size_t at = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
           dot[c] = 0.f;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) dot[c] = fmaf(qv[e], as_f(kr[e]), dot[c]);
+          for (int e = 0; e < kPer; ++e) {
+            dot[c] = fmaf(qv[e], as_f(kn[at + e]), dot[c]);
+            vv[c][e] = as_f(vn[at + e]);
+          }
+          bias[c] = a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1];
+          tj[c] = ts[j];
         }
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1)
@@ -559,12 +564,10 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (c0 + c < count) {  // (nothing of a key past the last is used)
-            const T* vr = vn + (size_t)(q0 + j[c] - L) * a.qkv_stride + head * D + kPer * lane;
-            const float sc = a.alpha * dot[c] + a.rab_pos[min(i, hist) - min(j[c], hist) + a.n_max - 1] +
-                             time_bias(sm.thr, sm.rts, sm.oct, ti - ts[j[c]]);
-            const float wt = silu_of<T>(sc);
+            const float wt =
+                silu_of<T>(a.alpha * dot[c] + bias[c] + time_bias(sm.thr, sm.rts, sm.oct, ti - tj[c]));
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, as_f(vr[e]), acc[e]);
+            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, vv[c][e], acc[e]);
           }
       }
 #pragma unroll
@@ -596,22 +599,32 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
 
   if (checks) check_keys();  // (the keys' own loads have them in the caches by now)
 
-  // ---- the last CTA of the user adds the parts, normalises and gates
+  // ---- the last CTA of these rows adds the parts, normalises and gates
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u], 1) == a.H * parts * row_groups - 1;
+  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u * row_groups + rg], 1) == a.H * parts - 1;
   __syncthreads();
   if (!sm.last) return;
   __threadfence();
   const int HD = a.H * D;  // a multiple of 32, at most 1024
   const float inv_n = 1.f / (float)a.n_max;
 #pragma unroll 1
-  for (int r = warp; r < rows; r += kWarps) {
+  for (int x0 = warp;; x0 += kWarps) {  // the x0-th of this group's rows
+    const int r = 8 * NQ * (rg + x0 / (8 * NQ) * row_groups) + x0 % (8 * NQ);
+    if (8 * NQ * (rg + x0 / (8 * NQ) * row_groups) >= rows) break;
+    if (r >= rows) continue;
     const size_t row = q0 + r;
-    float2 x[16];
+    float2 x[16], uv[16];
     float sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = make_float2(0.f, 0.f);
+    for (int k = 0; k < 16; ++k) {
+      x[k] = make_float2(0.f, 0.f);
+      uv[k] = make_float2(0.f, 0.f);
+      if (!a.out_raw && 64 * k + 2 * lane < HD) {  // the gate on its way with the sums
+        const T* uu = static_cast<const T*>(a.u) + row * a.u_stride + 64 * k + 2 * lane;
+        uv[k] = make_float2(as_f(uu[0]), as_f(uu[1]));
+      }
+    }
 #pragma unroll 1
     for (int s = 0; s < parts; ++s) {  // the features' loads are independent
       const float* src = a.o_ws + ((size_t)s * a.T_q + row) * HD + 2 * lane;
@@ -648,15 +661,14 @@ __global__ void __launch_bounds__(kThreads) attn_q4_small_kernel(const AttnArgs 
       }
     const float rstd = rsqrtf(warp_add(sq) / (float)HD + a.ln_eps);
     T* out = static_cast<T*>(a.out) + row * HD + 2 * lane;
-    const T* uu = static_cast<const T*>(a.u) + row * a.u_stride + 2 * lane;
 #pragma unroll
     for (int k = 0; k < 16; ++k)
       if (64 * k + 2 * lane < HD) {
         const int e = 64 * k + 2 * lane;
         const float2 ga = a.ln_gamma ? *reinterpret_cast<const float2*>(a.ln_gamma + e) : make_float2(1.f, 1.f);
         const float2 be = a.ln_beta ? *reinterpret_cast<const float2*>(a.ln_beta + e) : make_float2(0.f, 0.f);
-        const float y0 = ((x[k].x - mean) * rstd * ga.x + be.x) * as_f(uu[64 * k]);
-        const float y1 = ((x[k].y - mean) * rstd * ga.y + be.y) * as_f(uu[64 * k + 1]);
+        const float y0 = ((x[k].x - mean) * rstd * ga.x + be.x) * uv[k].x;
+        const float y1 = ((x[k].y - mean) * rstd * ga.y + be.y) * uv[k].y;
         if constexpr (kF32) *reinterpret_cast<float2*>(out + 64 * k) = make_float2(y0, y1);
         else *reinterpret_cast<__nv_bfloat162*>(out + 64 * k) = __floats2bfloat162_rn(y0, y1);
       }
@@ -696,16 +708,8 @@ bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
   return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535 && pool_rows < 0xFFFFFFFFll;
 }
 
-// Rows of one pass over the cached bytes: 16 where users have more than 8 on
-// average (fp32 calls with d > 64: 8, their three-term fragments fill the registers).
-int attn_q4_small_rows(const AttnArgs& a) {
-  return (long long)a.T_q <= 8ll * a.B || (!a.in_bf16 && a.d > 64) ? 8 : 16;
-}
-
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s) {
-  const int rows = attn_q4_small_rows(a);
-  const int groups = (int)std::max<long long>(1, std::min<long long>(64, ((long long)a.T_q + (long long)a.B * rows - 1) /
-                                                                             ((long long)a.B * rows)));
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
+                                 cudaStream_t s) {
   if (a.in_bf16)
     return rows == 8 ? launch_d<__nv_bfloat16, 1>(a, thr, counters, groups, s)
                      : launch_d<__nv_bfloat16, 2>(a, thr, counters, groups, s);

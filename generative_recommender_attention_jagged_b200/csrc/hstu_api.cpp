@@ -151,12 +151,26 @@ Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
   return use_tensor_cores(p) && (long long)p->total_tokens > 16ll * p->batch ? kQ4Tc : kQ4Small;
 }
 
+// Rows of one pass of the small kernel over the cached bytes: 16 where users have
+// more than 8 on average (fp32 calls with d > 64: 8, their three-term operands fill
+// the registers), and the CTAs that share a user's passes: room for twice the
+// average number of rows, since users differ (a CTA without rows ends at once).
+int q4_small_rows(const hstu_attn_params* p) {
+  const bool wide_f32 = p->dtype == HSTU_DT_F32 && p->head_dim > 64;
+  return (long long)p->total_tokens <= 8ll * p->batch || wide_f32 ? 8 : 16;
+}
+int q4_small_groups(const hstu_attn_params* p) {
+  const long long rows = q4_small_rows(p), per = (long long)p->batch * rows;
+  const long long avg = (p->total_tokens + per - 1) / per;
+  return (int)std::max<long long>(1, std::min<long long>(64, avg <= 1 ? avg : 2 * avg));
+}
+
 Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
-  Layout l;  // header, a counter per user, partial sums
+  Layout l;  // header, a counter per user and row group, partial sums
   l.max_items = 0;
   l.items_off = sizeof(WsHeader);
-  l.o_off = align_up(l.items_off + (kernel == kQ4Small ? (size_t)p->batch * sizeof(int32_t) : 0));
+  l.o_off = align_up(l.items_off + (kernel == kQ4Small ? (size_t)p->batch * q4_small_groups(p) * sizeof(int32_t) : 0));
   l.total = align_up(l.o_off + (size_t)splits * p->total_tokens * p->num_heads * p->head_dim * sizeof(float));
   return l;
 }
@@ -276,7 +290,7 @@ int run(const hstu_attn_params* p, const Common& c) {
     a.num_splits = c.splits;
     int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
     if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
-    return launch_attn_q4_small(a, thr, counters, c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), q4_small_groups(p), c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
     a.num_splits = c.splits;

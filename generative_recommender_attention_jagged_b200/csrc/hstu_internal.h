@@ -133,10 +133,12 @@ cudaError_t launch_attn_sm100_single(const AttnArgs& a, const BucketTable& thr, 
 cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStream_t s);
 
 // A few new rows a user over a 4-bit pool (attn_q4_small.cu): validation,
-// attention and the LayerNorm gate in one launch; counters [B] zeroed before.
-// bf16 and fp32, d = 32, 64, 96 or 128.
+// attention and the LayerNorm gate in one launch; counters [B * groups] zeroed
+// before.  bf16 and fp32, d = 32, 64, 96 or 128.  rows: 8 or 16 of a pass over the
+// cached bytes; groups: CTAs that share a user's passes.
 bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, cudaStream_t s);
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
+                                 cudaStream_t s);
 
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128;
 // partial sums to o_ws, then launch_epilogue.
