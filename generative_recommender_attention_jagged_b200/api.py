@@ -271,7 +271,7 @@ def split_uvqk(uvqk: torch.Tensor, num_heads: int, head_dim: int):
 def kv_params(k_pool: torch.Tensor, page_table: torch.Tensor, k_new: Optional[torch.Tensor] = None) -> _lib.KvParams:
     num_pages, H, P, d = k_pool.shape
     if k_pool.dtype == torch.uint8:  # a 4-bit pool (eviction only moves its page ids)
-        return _q4_kv_params(k_pool, page_table, torch.bfloat16, 0, 0)
+        return _lib.KvParams(page_table.shape[0], H, 2 * d, P, num_pages, page_table.shape[1], 0, 0, _lib.DT_BF16)
     stride = 0 if k_new is None or k_new.shape[0] <= 1 else k_new.stride(0)
     return _lib.KvParams(batch=page_table.shape[0], num_heads=H, head_dim=d, page_size=P, num_pages=num_pages,
                          max_pages_per_user=page_table.shape[1], kv_stride=stride,
@@ -336,38 +336,33 @@ def hstu_kv_evict(evict_mask, k_pool, page_table, cached_lens, free_pages, free_
 # and pointers go to ctypes as plain integers.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _one_device(named) -> int:
-    """Index of the GPU that holds every tensor of `named` ((name, tensor or None) pairs)."""
+def _wrong_device(named):
+    """Says which tensor of `named` ((name, tensor or None) pairs) is not with the first on one GPU."""
     dev = -1
     for name, t in named:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
+        d = t.get_device() if t is not None else dev
+        if t is not None and d < 0:
             raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-        if dev < 0:
-            dev = d
-        elif d != dev:
+        if dev >= 0 and d != dev:
             raise ValueError(f"{name} is on cuda:{d}, the tensors before it on cuda:{dev}")
-    return dev
+        dev = d
+    raise AssertionError("unreachable")
 
 
-def _on_device(dev: int, stream):
-    """(context that makes `dev` current, or None if it is; raw stream of the call)."""
-    if stream is not None and stream.device.index != dev:
+def _elsewhere(t, dev: int) -> bool:
+    return t is not None and t.get_device() != dev
+
+
+def _stream_of(dev: int, stream) -> int:
+    """Raw handle of the call's stream: the given one, else the device's current one."""
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
-    guard = None if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
-    return guard, (_raw_stream(dev) if stream is None else stream.cuda_stream)
-
-
-def _empty(shape, dtype, dev: int, stream):
-    """An output or scratch buffer of this call, kept until its stream has used it."""
-    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    return stream.cuda_stream
 
 
 class _Devices(dict):
@@ -379,15 +374,24 @@ class _Devices(dict):
 _DEVICES = _Devices()
 
 
+def _empty(shape, dtype, dev: int, stream):
+    """An output or scratch buffer of this call, kept until its stream has used it."""
+    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, where: str, guard, *args):
-    if guard is None:
+def _run(fn, where: str, dev: int, *args):
+    """The call, with its tensors' device current."""
+    if _current_device() == dev:
         rc = fn(*args)
     else:
-        with guard:
+        with torch.cuda.device(dev):
             rc = fn(*args)
     if rc:
         _lib.check(rc, where)
@@ -395,20 +399,20 @@ def _call(fn, where: str, guard, *args):
 
 def _need(name: str, t, dtype, shape):
     """A contiguous tensor of this type and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}"
-                         f" with strides {t.stride()}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
 
 
 def _ints(name: str, t, n: int):
-    if t.dtype != torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector of {n}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _token_rows(name: str, t, H: int, d: int) -> int:
     """Token stride of a [T, H, d] view with packed heads."""
     s = t.stride()
-    if t.numel() and (s[2] != 1 or s[1] != d):
+    if (s[2] != 1 or s[1] != d) and t.numel():
         raise ValueError(f"{name}: heads and features must be packed (stride 1 / d)")
     return s[0] if t.shape[0] > 1 else H * d
 
@@ -416,16 +420,18 @@ def _token_rows(name: str, t, H: int, d: int) -> int:
 def hstu_quant_i8_weight(w, *, w_q=None, w_scale=None, stream=None):
     """w [d_in, d_out] (bf16 or fp32) -> (w_q [d_out, d_in] int8, w_scale [d_out]
     fp32): one scale a channel, the layout hstu_linear_i8 reads."""
-    dev = _one_device((("w", w), ("w_q", w_q), ("w_scale", w_scale)))
+    dev = w.get_device()
+    if (dev < 0 or _elsewhere(w_q, dev) or _elsewhere(w_scale, dev)):
+        _wrong_device((("w", w), ("w_q", w_q), ("w_scale", w_scale)))
     if w.dim() != 2 or w.dtype not in _DT or not w.is_contiguous():
         raise ValueError("w must be a contiguous bf16 or fp32 [d_in, d_out] matrix")
     K, N = w.shape
-    guard, raw = _on_device(dev, stream)
+    raw = _stream_of(dev, stream)
     w_q = _empty((N, K), torch.int8, dev, stream) if w_q is None else w_q
     w_scale = _empty((N,), torch.float32, dev, stream) if w_scale is None else w_scale
     _need("w_q", w_q, torch.int8, (N, K))
     _need("w_scale", w_scale, torch.float32, (N,))
-    _call(_lib.load().hstu_quant_i8_weight, "hstu_quant_i8_weight", guard, w.data_ptr(), K, N, _DT[w.dtype],
+    _run(_lib.load().hstu_quant_i8_weight, "hstu_quant_i8_weight", dev, w.data_ptr(), K, N, _DT[w.dtype],
           w_q.data_ptr(), w_scale.data_ptr(), raw)
     return w_q, w_scale
 
@@ -440,8 +446,10 @@ def hstu_linear_i8(x, w_q, w_scale, bias=None, *, silu: bool = False, out=None, 
     """out = act(x W + bias) with x quantised to 8 bits token by token and W held
     in 8 bits channel by channel (hstu_quant_i8_weight); out_dtype defaults to
     x's type."""
-    dev = _one_device((("x", x), ("w_q", w_q), ("w_scale", w_scale), ("bias", bias), ("out", out),
-                       ("workspace", workspace)))
+    dev = x.get_device()
+    if (dev < 0 or w_q.get_device() != dev or w_scale.get_device() != dev or _elsewhere(bias, dev) or
+            _elsewhere(out, dev) or _elsewhere(workspace, dev)):
+        _wrong_device((("x", x), ("w_q", w_q), ("w_scale", w_scale), ("bias", bias), ("out", out), ("workspace", workspace)))
     if x.dim() != 2 or x.dtype not in _DT or (x.stride(1) != 1 and x.numel()):
         raise ValueError("x must be a bf16 or fp32 [T, d_in] matrix with contiguous rows")
     T, K = x.shape
@@ -454,7 +462,7 @@ def hstu_linear_i8(x, w_q, w_scale, bias=None, *, silu: bool = False, out=None, 
     dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else x.dtype)
     if dt not in _DT:
         raise ValueError(f"out must be bf16 or fp32, got {dt}")
-    guard, raw = _on_device(dev, stream)
+    raw = _stream_of(dev, stream)
     if out is None:
         out = _empty((T, N), dt, dev, stream)
     elif out.dtype != dt or tuple(out.shape) != (T, N) or (out.stride(1) != 1 and out.numel()):
@@ -466,31 +474,28 @@ def hstu_linear_i8(x, w_q, w_scale, bias=None, *, silu: bool = False, out=None, 
         workspace = _empty((int(lib.hstu_linear_i8_workspace_size(p)),), torch.uint8, dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(lib.hstu_linear_i8, "hstu_linear_i8", guard, p, x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+    _run(lib.hstu_linear_i8, "hstu_linear_i8", dev, p, x.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(), _ptr(bias),
           out.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
     return out
 
 
-def _q4_kv_params(k_pool, page_table, dtype, stride: int, total: int) -> _lib.KvParams:
-    num_pages, H, P, half = k_pool.shape
-    B, max_pages = page_table.shape
-    return _lib.KvParams(B, H, 2 * half, P, num_pages, max_pages, stride, total, _DT[dtype])
-
-
 def _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H: int, d: int):
-    shape = tuple(k_pool.shape)
+    shape = k_pool.shape
     if len(shape) != 4 or shape[1] != H or 2 * shape[3] != d:
-        raise ValueError(f"k_pool must be [num_pages, {H}, page_size, {d // 2}], got {shape}")
+        raise ValueError(f"k_pool must be [num_pages, {H}, page_size, {d // 2}], got {tuple(shape)}")
     _need("k_pool", k_pool, torch.uint8, shape)
     _need("v_pool", v_pool, torch.uint8, shape)
-    meta = (shape[0], shape[1], shape[2], 2)
+    meta = (shape[0], H, shape[2], 2)
     _need("k_scales", k_scales, torch.bfloat16, meta)
     _need("v_scales", v_scales, torch.bfloat16, meta)
+    return shape
 
 
 def _page_table(name: str, t):
-    if t.dtype != torch.int32 or t.dim() != 2 or not t.is_contiguous():
+    """(batch, max_pages_per_user)"""
+    if t.dtype is not torch.int32 or t.dim() != 2 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [batch, max_pages_per_user] int32 matrix")
+    return t.shape
 
 
 def hstu_kv_q4_workspace_size(batch: int) -> int:
@@ -502,33 +507,38 @@ def hstu_kv_append_q4(k_new, v_new, new_offsets, k_pool, v_pool, k_scales, v_sca
                       free_pages, free_count, *, num_append=None, workspace=None, stream=None):
     """hstu_kv_append into a 4-bit pool (k_pool, v_pool [num_pages, H, page_size,
     d / 2] bytes, k_scales, v_scales [num_pages, H, page_size, 2] bf16); in place."""
-    dev = _one_device((("k_new", k_new), ("v_new", v_new), ("new_offsets", new_offsets), ("k_pool", k_pool),
-                       ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales), ("page_table", page_table),
-                       ("cached_lens", cached_lens), ("free_pages", free_pages), ("free_count", free_count),
-                       ("num_append", num_append), ("workspace", workspace)))
+    dev = k_new.get_device()
+    if (dev < 0 or v_new.get_device() != dev or new_offsets.get_device() != dev or
+            k_pool.get_device() != dev or v_pool.get_device() != dev or k_scales.get_device() != dev or
+            v_scales.get_device() != dev or page_table.get_device() != dev or cached_lens.get_device() != dev or
+            free_pages.get_device() != dev or free_count.get_device() != dev or _elsewhere(num_append, dev) or
+            _elsewhere(workspace, dev)):
+        _wrong_device((("k_new", k_new), ("v_new", v_new), ("new_offsets", new_offsets), ("k_pool", k_pool), ("v_pool",
+                       v_pool), ("k_scales", k_scales), ("v_scales", v_scales), ("page_table", page_table), ("cached_lens",
+                       cached_lens), ("free_pages", free_pages), ("free_count", free_count), ("num_append", num_append),
+                       ("workspace", workspace)))
     if k_new.dim() != 3 or k_new.dtype not in _DT or v_new.dtype != k_new.dtype or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be bf16 or fp32 [T, H, d] tensors")
     T, H, d = k_new.shape
     token = _token_rows("k_new", k_new, H, d)
     if _token_rows("v_new", v_new, H, d) != token:
         raise ValueError("k_new and v_new must share one token stride")
-    _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
-    _page_table("page_table", page_table)
-    B = page_table.shape[0]
+    num_pages, _, P, _ = _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
+    B, max_pages = _page_table("page_table", page_table)
     _ints("new_offsets", new_offsets, B + 1)
     _ints("cached_lens", cached_lens, B)
-    _ints("free_pages", free_pages, k_pool.shape[0])
+    _ints("free_pages", free_pages, num_pages)
     _ints("free_count", free_count, 1)
     if num_append is not None:
         _ints("num_append", num_append, B)
-    guard, raw = _on_device(dev, stream)
-    p = ctypes.byref(_q4_kv_params(k_pool, page_table, k_new.dtype, token, T))
+    raw = _stream_of(dev, stream)
+    p = ctypes.byref(_lib.KvParams(B, H, d, P, num_pages, max_pages, token, T, _DT[k_new.dtype]))
     lib = _lib.load()
     if workspace is None:
         workspace = _empty((int(lib.hstu_kv_q4_workspace_size(p)),), torch.uint8, dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(lib.hstu_kv_append_q4, "hstu_kv_append_q4", guard, p, k_new.data_ptr(), v_new.data_ptr(),
+    _run(lib.hstu_kv_append_q4, "hstu_kv_append_q4", dev, p, k_new.data_ptr(), v_new.data_ptr(),
           new_offsets.data_ptr(), _ptr(num_append), k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
           v_scales.data_ptr(), page_table.data_ptr(), cached_lens.data_ptr(), free_pages.data_ptr(),
           free_count.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
@@ -539,21 +549,25 @@ def hstu_kv_read_q4(k_pool, v_pool, k_scales, v_scales, page_table, cached_lens,
                     total_tokens: int, dtype=torch.bfloat16, k_out=None, v_out=None, workspace=None, stream=None):
     """Dense (k, v) [total_tokens, H, d] of cached tokens: row offsets[u] + i is
     token starts[u] + i of user u."""
-    dev = _one_device((("k_pool", k_pool), ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales),
-                       ("page_table", page_table), ("cached_lens", cached_lens), ("starts", starts),
-                       ("offsets", offsets), ("k_out", k_out), ("v_out", v_out), ("workspace", workspace)))
+    dev = k_pool.get_device()
+    if (dev < 0 or v_pool.get_device() != dev or k_scales.get_device() != dev or
+            v_scales.get_device() != dev or page_table.get_device() != dev or cached_lens.get_device() != dev or
+            starts.get_device() != dev or offsets.get_device() != dev or _elsewhere(k_out, dev) or
+            _elsewhere(v_out, dev) or _elsewhere(workspace, dev)):
+        _wrong_device((("k_pool", k_pool), ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales),
+                       ("page_table", page_table), ("cached_lens", cached_lens), ("starts", starts), ("offsets", offsets),
+                       ("k_out", k_out), ("v_out", v_out), ("workspace", workspace)))
     if k_pool.dim() != 4:
         raise ValueError("k_pool must be [num_pages, H, page_size, d / 2]")
     H, d = k_pool.shape[1], 2 * k_pool.shape[3]
-    _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
-    _page_table("page_table", page_table)
-    B = page_table.shape[0]
+    num_pages, _, P, _ = _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
+    B, max_pages = _page_table("page_table", page_table)
     _ints("cached_lens", cached_lens, B)
     _ints("starts", starts, B)
     _ints("offsets", offsets, B + 1)
     if dtype not in _DT:
         raise ValueError(f"dtype must be bf16 or fp32, got {dtype}")
-    guard, raw = _on_device(dev, stream)
+    raw = _stream_of(dev, stream)
     shape = (total_tokens, H, d)
     if k_out is None:
         k_out = _empty(shape, dtype, dev, stream)
@@ -563,13 +577,13 @@ def hstu_kv_read_q4(k_pool, v_pool, k_scales, v_scales, page_table, cached_lens,
         v_out = _empty(shape, dtype, dev, stream)
     else:
         _need("v_out", v_out, dtype, shape)
-    p = ctypes.byref(_q4_kv_params(k_pool, page_table, dtype, 0, total_tokens))
+    p = ctypes.byref(_lib.KvParams(B, H, d, P, num_pages, max_pages, 0, total_tokens, _DT[dtype]))
     lib = _lib.load()
     if workspace is None:
         workspace = _empty((int(lib.hstu_kv_q4_workspace_size(p)),), torch.uint8, dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(lib.hstu_kv_read_q4, "hstu_kv_read_q4", guard, p, k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
+    _run(lib.hstu_kv_read_q4, "hstu_kv_read_q4", dev, p, k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
           v_scales.data_ptr(), page_table.data_ptr(), cached_lens.data_ptr(), starts.data_ptr(), offsets.data_ptr(),
           k_out.data_ptr(), v_out.data_ptr(), workspace.data_ptr(), workspace.nbytes, raw)
     return k_out, v_out
@@ -596,12 +610,19 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
                            max_cached_len: Optional[int] = None, out=None, workspace=None, raw_av: bool = False,
                            force_simt: bool = False, precise_silu: bool = False, stream=None):
     """hstu_attn_fwd_paged over a prefix held in 4 bits (see hstu_kv_append_q4)."""
-    dev = _one_device((("q", q), ("k", k), ("v", v), ("u", u), ("new_offsets", new_offsets), ("timestamps", timestamps),
-                       ("ts_offsets", ts_offsets), ("rab_pos", rab_pos), ("rab_ts", rab_ts), ("k_pool", k_pool),
-                       ("v_pool", v_pool), ("k_scales", k_scales), ("v_scales", v_scales),
-                       ("kv_page_table", kv_page_table), ("cached_lens", cached_lens),
-                       ("num_candidates", num_candidates), ("ln_gamma", ln_gamma), ("ln_beta", ln_beta), ("out", out),
-                       ("workspace", workspace)))
+    dev = q.get_device()
+    if (dev < 0 or k.get_device() != dev or v.get_device() != dev or u.get_device() != dev or
+            new_offsets.get_device() != dev or timestamps.get_device() != dev or ts_offsets.get_device() != dev or
+            rab_pos.get_device() != dev or rab_ts.get_device() != dev or k_pool.get_device() != dev or
+            v_pool.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev or
+            kv_page_table.get_device() != dev or cached_lens.get_device() != dev or
+            _elsewhere(num_candidates, dev) or _elsewhere(ln_gamma, dev) or _elsewhere(ln_beta, dev) or
+            _elsewhere(out, dev) or _elsewhere(workspace, dev)):
+        _wrong_device((("q", q), ("k", k), ("v", v), ("u", u), ("new_offsets", new_offsets), ("timestamps", timestamps),
+                       ("ts_offsets", ts_offsets), ("rab_pos", rab_pos), ("rab_ts", rab_ts), ("k_pool", k_pool), ("v_pool",
+                       v_pool), ("k_scales", k_scales), ("v_scales", v_scales), ("kv_page_table", kv_page_table),
+                       ("cached_lens", cached_lens), ("num_candidates", num_candidates), ("ln_gamma", ln_gamma),
+                       ("ln_beta", ln_beta), ("out", out), ("workspace", workspace)))
     dt = q.dtype
     if q.dim() != 3 or dt not in _DT or k.shape != q.shape or v.shape != q.shape or k.dtype != dt or v.dtype != dt:
         raise ValueError("q, k and v must be bf16 or fp32 [T, H, d] tensors of one shape and type")
@@ -609,9 +630,8 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
     D = H * d
     if tuple(u.shape) != (T, D) or u.dtype != dt or (u.stride(1) != 1 and u.numel()):
         raise ValueError(f"u must be a {dt} [{T}, {D}] matrix with contiguous rows, got {u.dtype} {tuple(u.shape)}")
-    _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
-    _page_table("kv_page_table", kv_page_table)
-    B, max_pages = kv_page_table.shape
+    num_pages, _, P, _ = _q4_pool_check(k_pool, v_pool, k_scales, v_scales, H, d)
+    B, max_pages = _page_table("kv_page_table", kv_page_table)
     _ints("new_offsets", new_offsets, B + 1)
     _ints("ts_offsets", ts_offsets, B + 1)
     _ints("cached_lens", cached_lens, B)
@@ -629,7 +649,7 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
         raise ValueError("q, k and v must share one token stride")
     flags = ((_lib.F_OUTPUT_RAW_AV if raw_av else 0) | (_lib.F_FORCE_SIMT if force_simt else 0) |
              (_lib.F_PRECISE_SILU if precise_silu else 0))
-    guard, raw = _on_device(dev, stream)
+    raw = _stream_of(dev, stream)
     p = ctypes.byref(_lib.AttnParams(B, H, d, n_max, rab_ts.numel(), T, n_max if max_seq_len is None else max_seq_len,
                                      qs, u.stride(0) if T > 1 else D, d ** -0.5 if alpha is None else alpha, ln_eps,
                                      _DT[dt], flags))
@@ -645,11 +665,11 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
         workspace = _empty((int(lib.hstu_attn_paged_q4_workspace_size(p, num_splits)),), torch.uint8, dev, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _call(lib.hstu_attn_fwd_paged_q4, "hstu_attn_fwd_paged_q4", guard, p, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _run(lib.hstu_attn_fwd_paged_q4, "hstu_attn_fwd_paged_q4", dev, p, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           u.data_ptr(), new_offsets.data_ptr(), timestamps.data_ptr(), ts_offsets.data_ptr(), _ptr(num_candidates),
           rab_pos.data_ptr(), rab_ts.data_ptr(), _ptr(ln_gamma), _ptr(ln_beta), k_pool.data_ptr(), v_pool.data_ptr(),
-          k_scales.data_ptr(), v_scales.data_ptr(), k_pool.shape[0], kv_page_table.data_ptr(), max_pages,
-          k_pool.shape[2], cached_lens.data_ptr(), num_splits, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+          k_scales.data_ptr(), v_scales.data_ptr(), num_pages, kv_page_table.data_ptr(), max_pages,
+          P, cached_lens.data_ptr(), num_splits, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
           raw)
     return out
 

@@ -34,8 +34,11 @@
 //     (128 + kz) sum_e q_ie in fp32 (8 sums of 16 products: the error stays
 //     near 2^-20 of s, against 2^-9 of the rounding of the weights); for V
 //     before it (the sum runs over thousands of keys), one packed subtraction.
-//   - Weights: SiLU in fp32; a_ij vs_j is rounded once to bf16 for the second
-//     product, sums are fp32.
+//   - Weights: SiLU in fp32, sums in fp32.  a_ij vs_j goes into the second product
+//     as one bf16 term in calls with long histories, where its roundings average out
+//     (relative error of y 1.8e-3, of which 1.7e-3 is its own rounding), and as two
+//     where no sequence exceeds kTwoTermLength (with one: 2.3e-3 at 100 keys).  Two
+//     terms for all took 93 us instead of 84 for 64 users of 1000 to 8192 keys.
 //   - fp32 calls split each row element and each weight into three bf16 terms
 //     (8 + 8 + 8 bits: what is left is below 2^-24 of it) and run each product
 //     three times, smallest terms first; code - zero is exact as it is, and every
@@ -67,6 +70,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRing = 2;       // key tiles a warp has in shared memory
 constexpr int kKeys = 32;      // keys of a tile
+constexpr int kTwoTermLength = 2048;  // bound of the sequence lengths up to which bf16 weights are two terms
 constexpr int kMinPart = 256;  // keys below which a part is not split further
 
 template <int D>
@@ -148,11 +152,11 @@ __device__ __forceinline__ float silu_of(float s) {
 __device__ __forceinline__ float as_f(float x) { return x; }
 __device__ __forceinline__ float as_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// x as three bf16 terms, largest first; their sum is x to 2^-24 |x| (exact for
-// the usual range: each term takes 8 of the 24 bits)
-__device__ __forceinline__ void split3(float x, float (&y)[3]) {
+// x as N bf16 terms, largest first; their sum is x to 2^(-8 N) |x| (each term takes 8 bits)
+template <int N>
+__device__ __forceinline__ void split_bf16(float x, float (&y)[N]) {
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
+  for (int p = 0; p < N; ++p) {
     y[p] = __bfloat162float(__float2bfloat16_rn(x));
     // an infinity or NaN (or what rounds to one) stays in the first term
     x = fabsf(y[p]) <= FLT_MAX ? x - y[p] : 0.f;
@@ -180,11 +184,12 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
 }
 
 // (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, int WT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
                                                                  int32_t* counters, int row_groups) {
   constexpr bool kF32 = sizeof(T) == 4;
-  constexpr int kTerms = kF32 ? 3 : 1;
+  constexpr int kTerms = kF32 ? 3 : 1;   // bf16 terms of a row element
+  constexpr int kWTerms = kF32 ? 3 : WT; // and of a weight
   constexpr int kWords = D / 32;   // words of a K row a thread reads (its quarter of the dimensions)
   constexpr int kSteps = D / 16;   // products of 16 dimensions
   constexpr int kTilesM = D / 16;  // 16-dimension tiles of O^T
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
         if constexpr (kF32) {
           float y[4][3];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) split3(x[e], y[e]);
+          for (int e = 0; e < 4; ++e) split_bf16(x[e], y[e]);
 #pragma unroll
           for (int p = 0; p < kTerms; ++p) {
             qf[w][k][0][p] = pack_bf16x2(y[0][p], y[1][p]);
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
       }
       __syncwarp();
       // ---- weights: lane = key, only the rows there are
-      uint32_t p[kTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
+      uint32_t p[kWTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
       {
         const int j = j0 + lane;
         const uint32_t km = st.km[lane], vm = st.vm[lane];
@@ -418,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
         const long long tj = st.ts[lane];
         const float* bias_of = a.rab_pos - min(j, L);
         const float* sc_of = reinterpret_cast<const float*>(xs[lane]);
-        uint32_t pk[kTerms][4 * NQ];
+        uint32_t pk[kWTerms][4 * NQ];
 #pragma unroll
         for (int r = 0; r < 8 * NQ; r += 2) {
           float wt[2] = {0.f, 0.f};
@@ -429,26 +434,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
               const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
               wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
             }
-          if constexpr (kF32) {
-            float y[2][3];
-            split3(wt[0], y[0]);
-            split3(wt[1], y[1]);
+          if constexpr (kWTerms > 1) {
+            float y[2][kWTerms];
+            split_bf16(wt[0], y[0]);
+            split_bf16(wt[1], y[1]);
 #pragma unroll
-            for (int x = 0; x < kTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
+            for (int x = 0; x < kWTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
           } else {
             pk[0][r / 2] = pack_bf16x2(wt[0], wt[1]);
           }
         }
         // the lane's weights over its own scores, then transposed by ldmatrix
 #pragma unroll
-        for (int x = 0; x < kTerms; ++x)
+        for (int x = 0; x < kWTerms; ++x)
 #pragma unroll
           for (int w = 0; w < NQ; ++w)
             *reinterpret_cast<uint4*>(xs[lane] + 16 * (NQ * x + w)) =
                 make_uint4(pk[x][4 * w], pk[x][4 * w + 1], pk[x][4 * w + 2], pk[x][4 * w + 3]);
         __syncwarp();
 #pragma unroll
-        for (int x = 0; x < kTerms; ++x)
+        for (int x = 0; x < kWTerms; ++x)
 #pragma unroll
           for (int w = 0; w < NQ; ++w)
             asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
           av[half][3] = sub_bf16x2(widen(vh[half][1][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][1]);
         }
 #pragma unroll
-        for (int x = kTerms - 1; x >= 0; --x)
+        for (int x = kWTerms - 1; x >= 0; --x)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -675,30 +680,30 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
   }
 }
 
-template <typename T, int D, int NQ>
+template <typename T, int D, int NQ, int WT>
 cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<T, D, NQ>);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<T, D, NQ>,
+    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<T, D, NQ, WT>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  attn_q4_small_kernel<T, D, NQ>
+  attn_q4_small_kernel<T, D, NQ, WT>
       <<<dim3(a.num_splits * row_groups, a.H, a.B), kThreads, smem, s>>>(a, thr, counters, row_groups);
   return cudaGetLastError();
 }
 
-template <typename T, int NQ>
+template <typename T, int NQ, int WT>
 cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
   switch (a.d) {
-    case 32: return launch<T, 32, NQ>(a, thr, counters, row_groups, s);
-    case 64: return launch<T, 64, NQ>(a, thr, counters, row_groups, s);
-    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ>(a, thr, counters, row_groups, s);
-    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ>(a, thr, counters, row_groups, s);
+    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, row_groups, s);
+    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, row_groups, s);
+    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, row_groups, s);
+    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, row_groups, s);
   }
 }
 
@@ -709,11 +714,15 @@ bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
 }
 
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
-                                 cudaStream_t s) {
-  if (a.in_bf16)
-    return rows == 8 ? launch_d<__nv_bfloat16, 1>(a, thr, counters, groups, s)
-                     : launch_d<__nv_bfloat16, 2>(a, thr, counters, groups, s);
-  return rows == 8 ? launch_d<float, 1>(a, thr, counters, groups, s) : launch_d<float, 2>(a, thr, counters, groups, s);
+                                 int max_seq_len, cudaStream_t s) {
+  using bf16 = __nv_bfloat16;
+  if (!a.in_bf16)
+    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, groups, s)
+                     : launch_d<float, 2, 3>(a, thr, counters, groups, s);
+  if (std::min(max_seq_len, a.n_max) <= kTwoTermLength)
+    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, groups, s)
+                     : launch_d<bf16, 2, 2>(a, thr, counters, groups, s);
+  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, groups, s) : launch_d<bf16, 2, 1>(a, thr, counters, groups, s);
 }
 
 }  // namespace hstu

@@ -290,7 +290,7 @@ int run(const hstu_attn_params* p, const Common& c) {
     a.num_splits = c.splits;
     int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
     if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
-    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), q4_small_groups(p), c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), q4_small_groups(p), p->max_seq_len, c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
     a.num_splits = c.splits;

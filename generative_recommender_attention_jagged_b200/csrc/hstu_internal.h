@@ -138,7 +138,7 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStre
 // cached bytes; groups: CTAs that share a user's passes.
 bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
-                                 cudaStream_t s);
+                                 int max_seq_len, cudaStream_t s);
 
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128;
 // partial sums to o_ws, then launch_epilogue.
