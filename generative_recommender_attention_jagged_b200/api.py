@@ -270,8 +270,6 @@ def split_uvqk(uvqk: torch.Tensor, num_heads: int, head_dim: int):
 
 def kv_params(k_pool: torch.Tensor, page_table: torch.Tensor, k_new: Optional[torch.Tensor] = None) -> _lib.KvParams:
     num_pages, H, P, d = k_pool.shape
-    if k_pool.dtype == torch.uint8:  # a 4-bit pool (eviction only moves its page ids)
-        return _lib.KvParams(page_table.shape[0], H, 2 * d, P, num_pages, page_table.shape[1], 0, 0, _lib.DT_BF16)
     stride = 0 if k_new is None or k_new.shape[0] <= 1 else k_new.stride(0)
     return _lib.KvParams(batch=page_table.shape[0], num_heads=H, head_dim=d, page_size=P, num_pages=num_pages,
                          max_pages_per_user=page_table.shape[1], kv_stride=stride,
@@ -319,7 +317,11 @@ def hstu_kv_evict(evict_mask, k_pool, page_table, cached_lens, free_pages, free_
     """Returns the pages of every user with evict_mask[u] != 0 to the free stack; in place."""
     _kv_check(k_pool, page_table, cached_lens, free_pages, free_count)
     _need_cuda("evict_mask", evict_mask, torch.int32)
-    p = kv_params(k_pool, page_table)
+    if k_pool.dtype == torch.uint8:  # a 4-bit pool: only its page ids move
+        num_pages, H, P, d2 = k_pool.shape
+        p = _lib.KvParams(page_table.shape[0], H, 2 * d2, P, num_pages, page_table.shape[1], 0, 0, _lib.DT_BF16)
+    else:
+        p = kv_params(k_pool, page_table)
     if workspace is None:
         workspace = torch.empty(hstu_kv_workspace_size(p), dtype=torch.uint8, device=k_pool.device)
     rc = _lib.load().hstu_kv_evict(ctypes.byref(p), _p(evict_mask), _p(page_table), _p(cached_lens),
@@ -375,11 +377,12 @@ _DEVICES = _Devices()
 
 
 def _empty(shape, dtype, dev: int, stream):
-    """An output or scratch buffer of this call, kept until its stream has used it."""
-    t = torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    """An output or scratch buffer of this call, from the memory of its stream (memory of another stream may still be
+    in use there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[dev])
 
 
 def _ptr(t):

@@ -168,3 +168,20 @@ def test_captured_replay_and_second_stream(T):
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(other, first)
     assert hstu.hstu_check_device_error(buf) == 0
+
+
+def test_output_on_another_stream_takes_no_memory_in_use():
+    """The result of a call on a side stream may not land in memory that the current stream still reads."""
+    x, wq, ws = torch.randn(256, 64, device="cuda"), torch.ones(64, 64, dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    copy = torch.empty(256, 64, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        kept = torch.full((256, 64), 7.0, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(2_000_000)          # about a millisecond
+        copy.copy_(kept)
+        del kept
+        hstu.hstu_linear_i8(x, wq, ws, stream=side)
+        torch.cuda.synchronize()
+        assert (copy == 7.0).all()

@@ -131,6 +131,8 @@ def test_attn_q4_refusals(lib):
     assert call_attn(lib, attn(), splits=0) == -1 and call_attn(lib, attn(), splits=65) == -1
     assert call_attn(lib, attn(), ws=64) == -5
     assert call_attn(lib, attn(flags=0x1000)) == -1
+    for stage in (_lib.F_STAGE_PLAN, _lib.F_STAGE_ATTN, _lib.F_STAGE_EPILOGUE):
+        assert call_attn(lib, attn(flags=stage)) == -2
     p = attn(head_dim=48)
     assert lib.hstu_attn_paged_q4_workspace_size(ctypes.byref(p), 1) == 0
     assert hstu.hstu_attn_paged_q4_workspace_size(batch=2, num_heads=4, head_dim=128, n_max=1024, total_tokens=300,
@@ -154,3 +156,9 @@ def test_bindings_refuse_cpu_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         hstu.hstu_attn_fwd_paged_q4(k, k, k, k.view(4, 32), i, i.long(), i, torch.zeros(7), torch.zeros(128), pool, pool,
                                     meta, meta, i.view(1, 1), i, n_max=4)
+
+
+def test_the_bf16_cache_has_no_4bit_parameters():
+    pool = torch.zeros(4, 1, 8, 16, dtype=torch.uint8)
+    with pytest.raises(KeyError):
+        hstu.api.kv_params(pool, torch.zeros(2, 2, dtype=torch.int32))
