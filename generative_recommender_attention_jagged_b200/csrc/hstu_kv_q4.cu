@@ -11,9 +11,9 @@
 //
 // Append is one launch for up to 256 users: every block works the allocation out
 // for itself (one user a thread, one block-wide scan) from lengths, table and
-// stack as they were, copies its tokens, and the block that finishes last writes
-// the new table entries, lengths and stack height.  Nothing is changed before every
-// block has read it, and nothing at all if the batch does not fit.  More users take
+// stack as they were, and copies its tokens; the block that was the last to read them
+// (a counter) also writes the new table entries, lengths and stack height.  Nothing is
+// changed before every block has read it, and nothing at all if the batch does not fit.  More users take
 // the plan launch of hstu_kv.cu first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -48,6 +48,7 @@ struct FusedPlan {
   int32_t old[kFusedUsers];      // cached tokens before
   int32_t app[kFusedUsers];      // appended tokens
   int32_t pre[kFusedUsers];      // pages taken by the users before
+  int32_t part[kFusedUsers];     // the partly filled last page, where tokens go into it
   int32_t warp_sum[kRowWarps];
   int32_t err, total, fc, last;
 };
@@ -79,6 +80,7 @@ __device__ void plan_append(const KvArgs& a, FusedPlan& p) {
         if (app > 0 && L % a.P != 0) {  // the partly filled last page receives tokens
           const int pid = a.page_table[(size_t)u * a.max_pages + L / a.P];
           if (pid < 0 || pid >= a.num_pages) atomicCAS(&p.err, 0, kErrPage);
+          p.part[u] = pid;
         }
       }
     }
@@ -189,6 +191,12 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_q4_kernel(const KvArgs 
       if (blockIdx.x == 0 && threadIdx.x == 0) report_error(a.hdr, p.err, 0);
       return;
     }
+    // this block has read all that an append changes (the stack's entries stay as they are)
+    if (threadIdx.x == 0) {
+      __threadfence();
+      p.last = atomicAdd(&a.hdr->blocks_done, 1) == (int)gridDim.x - 1;
+      __threadfence();
+    }
   } else {
     if (a.hdr->pad[0] != 1) return;
   }
@@ -203,16 +211,14 @@ __global__ void __launch_bounds__(kRowThreads) kv_append_q4_kernel(const KvArgs 
     int pid;
     if constexpr (FUSED) {
       const int have = (old[u] + a.P - 1) / a.P;
-      pid = page < have ? a.page_table[(size_t)u * a.max_pages + page] : a.free_pages[p.fc - 1 - p.pre[u] - (page - have)];
+      pid = page < have ? p.part[u] : a.free_pages[p.fc - 1 - p.pre[u] - (page - have)];
     } else {
       pid = a.page_table[(size_t)u * a.max_pages + page];
     }
     quantise_token<T, G, W>(a, pool, row, (size_t)pid * a.H, pos - page * a.P);
   }
   if constexpr (FUSED) {
-    // the block that is last to have read everything writes the new state
-    __syncthreads();
-    if (threadIdx.x == 0) p.last = atomicAdd(&a.hdr->blocks_done, 1) == (int)gridDim.x - 1;
+    // the block that was last to read the old state writes the new one
     __syncthreads();
     if (!p.last) return;
     const int u = threadIdx.x;
