@@ -29,8 +29,8 @@
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
 // row that is not finite is stored as zeros and its scale set to NaN: the mask is
 // applied to the finished weight, so rows that may not see the key stay finite.
-// There is no plan launch: a CTA finds its (user, tile) by a scan of the offsets,
-// looks at the page ids it uses and, for head 0, at the order of the timestamps.  Every wait is bounded.
+// A CTA looks at the page ids it uses and, for head 0, at the order of the timestamps (users without
+// new rows, which have no CTA, are checked for their lengths only).  Every wait is bounded.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -85,8 +85,6 @@ struct __align__(1024) SmemQ4 {
   uint64_t bar_o_full;
   uint32_t tmem_base;
   int abort;
-  int item_user, item_tile;
-  int scan[kThreads / 32];
 };
 constexpr size_t kSmemBytes = sizeof(SmemQ4) + 1024;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
@@ -231,62 +229,10 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The user and 128-row tile of the qt-th query tile of the batch, into sm.item_user (-1: none) and
-// sm.item_tile; all threads.  Up to kThreads users are taken in the order of their lengths, longest
-// first, so that the last CTAs to start are short ones; larger batches, which have many CTAs an SM
-// anyway, in their own order.
-__device__ __forceinline__ void find_item(const AttnArgs& a, SmemQ4& sm, int qt) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int* len = reinterpret_cast<int*>(sm.q);  // the tiles of shared memory are free so far
-  int* user = len + kThreads;
-  const bool sorted = a.B <= kThreads;
-  auto tiles_of = [&](int u) {
-    return max(0, (int)(((long long)a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile));
-  };
-  if (tid == 0) sm.item_user = -1;
-  if (sorted) {
-    const int mine = tid < a.B ? a.cached_lens[tid] : 0;
-    len[tid] = mine;
-    __syncthreads();
-    if (tid < a.B) {
-      int rank = 0;
-      for (int u = 0; u < a.B; ++u) rank += len[u] > mine || (len[u] == mine && u < tid);
-      user[rank] = tid;
-    }
-    __syncthreads();
-  }
-  const int per = (a.B + kThreads - 1) / kThreads;
-  const int lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-  int mine = 0;
-  for (int x = lo; x < hi; ++x) mine += tiles_of(sorted ? user[x] : x);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) sm.scan[warp] = incl;
-  __syncthreads();
-  int before = incl - mine;
-  for (int w = 0; w < warp; ++w) before += sm.scan[w];
-  if (qt >= before && qt < before + mine) {
-    int at = before;
-    for (int x = lo; x < hi; ++x) {
-      const int u = sorted ? user[x] : x, tiles = tiles_of(u);
-      if (qt < at + tiles) {
-        sm.item_user = u;
-        sm.item_tile = qt - at;
-        break;
-      }
-      at += tiles;
-    }
-  }
-  __syncthreads();
-}
-
 template <bool PRECISE>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_q4_sm100_kernel(const AttnArgs a, const BucketTable tab, const __grid_constant__ CUtensorMap tm_q) {
+    attn_q4_sm100_kernel(const AttnArgs a, const BucketTable tab, const int2* tiles,
+                         const __grid_constant__ CUtensorMap tm_q) {
   extern __shared__ uint8_t smem_raw[];
   SmemQ4& sm = aligned_smem<SmemQ4>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -294,20 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head = (int)(blockIdx.x / a.num_splits) % a.H;
   const int qt = (int)(blockIdx.x / a.num_splits) / a.H;
 
-  if (blockIdx.x == 0)  // users without a tile of their own are checked here
-    for (int u = threadIdx.x; u < a.B; u += kThreads) {
-      int n, tso, pages;
-      if (!check_user(a, u, n, tso, pages)) report_error(a.hdr, kErrLength, u);
-    }
-  find_item(a, sm, qt);
-  const int user = sm.item_user;
+  if (a.hdr->pad[0] != 1) return;  // a user's lengths do not hold
+  const int2 item = tiles[qt];
+  const int user = item.x;
   if (user < 0) return;
-  int n_all, tso, pages_all;
-  if (!check_user(a, user, n_all, tso, pages_all)) {
-    if (threadIdx.x == 0) report_error(a.hdr, kErrLength, user);
-    return;
-  }
-  const TileGeom g = tile_geom(a, user, sm.item_tile);
+  const TileGeom g = tile_geom(a, user, item.y);
   // The last tiles (recent keys: a bucket edge every few columns; masked and new ones) take two to
   // three times the others' time: they count for more when the keys are split.
   int tb, te;
@@ -319,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int prmin = min(g.qs, g.h);
   const int32_t* table = a.page_table + (size_t)user * a.max_pages;
   // head 0 of the user's last tile (it sees every key but the candidates) checks the timestamps on the way
-  const bool checks = head == 0 && (sm.item_tile + 1) * kTile >= g.n - g.L;
+  const bool checks = head == 0 && (item.y + 1) * kTile >= g.n - g.L;
 
   if (threadIdx.x == 0) {
     mbar_init(&sm.bar_q, 1);
@@ -715,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const CUtensorMap& tm_q, cudaStream_t s) {
+cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const int2* tiles, const CUtensorMap& tm_q,
+                                 cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static unsigned long long attr_set = 0;  // one bit per device
@@ -727,14 +665,12 @@ cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, cons
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  // sum over users of ceil(rows / 128) <= T / 128 + B query tiles
-  const long long tiles = (long long)a.T_q / kTile + a.B;
-  const long long ctas = tiles * a.H * a.num_splits;
+  const long long ctas = ((long long)a.T_q / kTile + a.B) * a.H * a.num_splits;  // a CTA per listed tile, head and split
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   if (a.precise_silu)
-    attn_q4_sm100_kernel<true><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tm_q);
+    attn_q4_sm100_kernel<true><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tiles, tm_q);
   else
-    attn_q4_sm100_kernel<false><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tm_q);
+    attn_q4_sm100_kernel<false><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tiles, tm_q);
   return cudaGetLastError();
 }
 

@@ -51,7 +51,7 @@
 // The new rows' own keys are a few: each warp takes rows and does the allowed
 // pairs in fp32 FMAs, so that what a mask hides is never touched.  The CTA that
 // finishes a group of rows last (a counter in the workspace) adds the parts in order,
-// normalises and gates: one launch besides the clearing of the counters.
+// normalises and gates: one launch behind the plan (plan_q4_kernel).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -103,7 +103,6 @@ struct __align__(16) SmallSmem {
   long long thr[kMaxBuckets];
   float rts[kMaxBuckets];
   uint4 oct[32];
-  int order[kThreads];  // the users' lengths, at the start
   int last;
 };
 
@@ -185,8 +184,8 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
 
 // (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
 template <typename T, int D, int NQ, int WT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) attn_q4_small_kernel(const AttnArgs a, const BucketTable tab,
-                                                                 int32_t* counters, int row_groups) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
+    attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int32_t* order, int row_groups) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kTerms = kF32 ? 3 : 1;   // bf16 terms of a row element
   constexpr int kWTerms = kF32 ? 3 : WT; // and of a weight
@@ -199,35 +198,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  // Up to kThreads users come in the order of their lengths, longest first: their parts differ in size
-  // (64 users of 1000 to 8192 tokens in their own order kept a third of the SMs waiting for the last ones).
-  int u = blockIdx.z;
-  if (a.B > 1 && a.B <= kThreads) {
-    const int mine = threadIdx.x < a.B ? a.cached_lens[threadIdx.x] : 0;
-    if (threadIdx.x < a.B) sm.order[threadIdx.x] = mine;
-    __syncthreads();
-    if (threadIdx.x < a.B) {
-      int rank = 0;
-      for (int x = 0; x < a.B; ++x) rank += sm.order[x] > mine || (sm.order[x] == mine && x < (int)threadIdx.x);
-      if (rank == (int)blockIdx.z) sm.last = threadIdx.x;
-    }
-    __syncthreads();
-    u = sm.last;
-  }
-  int n, tso, pages;
-  if (!check_user(a, u, n, tso, pages)) {
-    if (threadIdx.x == 0) report_error(a.hdr, kErrLength, u);
-    return;
-  }
+  if (a.hdr->pad[0] != 1) return;  // a user's lengths do not hold
+  const int u = order[blockIdx.z];
   const int q0 = a.q_offsets[u], rows = a.q_offsets[u + 1] - q0;
-  const int L = a.cached_lens[u];
+  const int L = a.cached_lens[u], n = L + rows;
   const int part = part_keys(L, a.num_splits);
   const int parts = max(1, (L + part - 1) / part);
   if (split >= parts) return;
   const int k_lo = split * part, k_hi = min(L, k_lo + part);
   const int hist = n - (a.num_cand ? a.num_cand[u] : 0);
   const int32_t* table = a.page_table + (size_t)u * a.max_pages;
-  const int64_t* ts = a.ts + tso;
+  const int64_t* ts = a.ts + a.ts_offsets[u];
 
   // this part's page ids and timestamps (the first part also has the new tokens')
   auto check_keys = [&] {
@@ -681,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3) a
 }
 
 template <typename T, int D, int NQ, int WT>
-cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
+cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order, int row_groups,
+                   cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<T, D, NQ>);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -693,17 +675,18 @@ cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters,
     attr_set |= 1ull << dev;
   }
   attn_q4_small_kernel<T, D, NQ, WT>
-      <<<dim3(a.num_splits * row_groups, a.H, a.B), kThreads, smem, s>>>(a, thr, counters, row_groups);
+      <<<dim3(a.num_splits * row_groups, a.H, a.B), kThreads, smem, s>>>(a, thr, counters, order, row_groups);
   return cudaGetLastError();
 }
 
 template <typename T, int NQ, int WT>
-cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int row_groups, cudaStream_t s) {
+cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
+                     int row_groups, cudaStream_t s) {
   switch (a.d) {
-    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, row_groups, s);
-    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, row_groups, s);
-    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, row_groups, s);
-    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, row_groups, s);
+    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, order, row_groups, s);
+    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, order, row_groups, s);
+    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, order, row_groups, s);
+    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, order, row_groups, s);
   }
 }
 
@@ -713,16 +696,16 @@ bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
   return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535 && pool_rows < 0xFFFFFFFFll;
 }
 
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
-                                 int max_seq_len, cudaStream_t s) {
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
+                                 int rows, int groups, int max_seq_len, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   if (!a.in_bf16)
-    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, groups, s)
-                     : launch_d<float, 2, 3>(a, thr, counters, groups, s);
+    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, order, groups, s)
+                     : launch_d<float, 2, 3>(a, thr, counters, order, groups, s);
   if (std::min(max_seq_len, a.n_max) <= kTwoTermLength)
-    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, groups, s)
-                     : launch_d<bf16, 2, 2>(a, thr, counters, groups, s);
-  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, groups, s) : launch_d<bf16, 2, 1>(a, thr, counters, groups, s);
+    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, order, groups, s)
+                     : launch_d<bf16, 2, 2>(a, thr, counters, order, groups, s);
+  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, order, groups, s) : launch_d<bf16, 2, 1>(a, thr, counters, order, groups, s);
 }
 
 }  // namespace hstu

@@ -165,12 +165,17 @@ int q4_small_groups(const hstu_attn_params* p) {
   return (int)std::max<long long>(1, std::min<long long>(64, avg <= 1 ? avg : 2 * avg));
 }
 
+// at most this many 128-row query tiles: sum over users of ceil(rows / 128)
+int q4_tiles(const hstu_attn_params* p) { return p->total_tokens / kTile + p->batch; }
+
 Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
-  Layout l;  // header, a counter per user and row group, partial sums
+  Layout l;  // header, the plan (few rows: users in order, a counter per user and row group; else tiles), partial sums
   l.max_items = 0;
   l.items_off = sizeof(WsHeader);
-  l.o_off = align_up(l.items_off + (kernel == kQ4Small ? (size_t)p->batch * q4_small_groups(p) * sizeof(int32_t) : 0));
+  const size_t plan = kernel == kQ4Small ? (size_t)p->batch * (1 + q4_small_groups(p)) * sizeof(int32_t)
+                                         : (size_t)q4_tiles(p) * sizeof(int2);
+  l.o_off = align_up(l.items_off + plan);
   l.total = align_up(l.o_off + (size_t)splits * p->total_tokens * p->num_heads * p->head_dim * sizeof(float));
   return l;
 }
@@ -288,22 +293,29 @@ int run(const hstu_attn_params* p, const Common& c) {
   cudaError_t e = cudaSuccess;
   if (q4_kernel == kQ4Small) {
     a.num_splits = c.splits;
-    int32_t* counters = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
-    if (cudaMemsetAsync(c.ws, 0, l.o_off, c.stream) != cudaSuccess) return HSTU_ERR_CUDA;
-    return launch_attn_q4_small(a, thr, counters, q4_small_rows(p), q4_small_groups(p), p->max_seq_len, c.stream) == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
+    int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
+    int32_t* counters = order + a.B;
+    const int groups = q4_small_groups(p);
+    if (launch_plan_q4(a, counters, a.B * groups, order, nullptr, 0, c.stream) != cudaSuccess ||
+        launch_attn_q4_small(a, thr, counters, order, q4_small_rows(p), groups, p->max_seq_len, c.stream) != cudaSuccess)
+      return HSTU_ERR_CUDA;
+    return HSTU_OK;
   }
   if (q4_kernel == kQ4Tc) {
     a.num_splits = c.splits;
     a.self_term = 1;
     CUtensorMap tq;
     if (!encode_rows(&tq, c.q, a.T_q, a.H, a.d, a.qkv_stride)) return HSTU_ERR_CUDA;
-    if (cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream) != cudaSuccess ||
-        launch_attn_q4_sm100(a, thr, tq, c.stream) != cudaSuccess || launch_epilogue(a, c.stream) != cudaSuccess)
+    int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
+    if (launch_plan_q4(a, nullptr, 0, nullptr, tiles, q4_tiles(p), c.stream) != cudaSuccess ||
+        launch_attn_q4_sm100(a, thr, tiles, tq, c.stream) != cudaSuccess || launch_epilogue(a, c.stream) != cudaSuccess)
       return HSTU_ERR_CUDA;
     return HSTU_OK;
   }
   if (stages & HSTU_F_STAGE_PLAN) {
-    if ((e = cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
+    e = q4 ? launch_plan_q4(a, nullptr, 0, nullptr, nullptr, 0, c.stream)
+           : cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream);
+    if (e != cudaSuccess) return HSTU_ERR_CUDA;
     if ((e = launch_plan(a, tc, p->max_seq_len, c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
   }
   if (a.T_q == 0) return HSTU_OK;

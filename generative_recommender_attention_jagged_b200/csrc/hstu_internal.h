@@ -132,17 +132,22 @@ cudaError_t launch_attn_sm100_single(const AttnArgs& a, const BucketTable& thr, 
                                      const CUtensorMap& tm_kpool, const CUtensorMap& tm_vpool, cudaStream_t s);
 cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStream_t s);
 
-// A few new rows a user over a 4-bit pool (attn_q4_small.cu): validation,
-// attention and the LayerNorm gate in one launch; counters [B * groups] zeroed
-// before.  bf16 and fp32, d = 32, 64, 96 or 128.  rows: 8 or 16 of a pass over the
-// cached bytes; groups: CTAs that share a user's passes.
-bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, int rows, int groups,
-                                 int max_seq_len, cudaStream_t s);
+// Checks of the users and the order of the work for the 4-bit kernels (hstu_kernels.cu).
+cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
+                           int n_tiles, cudaStream_t s);
 
-// Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128;
-// partial sums to o_ws, then launch_epilogue.
-cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const CUtensorMap& tm_q, cudaStream_t s);
+// A few new rows a user over a 4-bit pool (attn_q4_small.cu): attention and the
+// LayerNorm gate in one launch behind launch_plan_q4; counters [B * groups] zeroed,
+// order [B] of the users.  bf16 and fp32, d = 32, 64, 96 or 128.  rows: 8 or 16 of a
+// pass over the cached bytes; groups: CTAs that share a user's passes.
+bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
+                                 int rows, int groups, int max_seq_len, cudaStream_t s);
+
+// Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128, tiles
+// [T_q / 128 + B] as launch_plan_q4 lists them; partial sums to o_ws, then launch_epilogue.
+cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const int2* tiles, const CUtensorMap& tm_q,
+                                 cudaStream_t s);
 
 // Backward of the attention core on CUDA cores (hstu_bwd.cu); gradients fp32,
 // d_rp / d_rt must be zeroed by the caller.

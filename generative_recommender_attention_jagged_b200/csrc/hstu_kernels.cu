@@ -109,6 +109,7 @@ __device__ void build_schedule(const AttnArgs& a, int* hist, int* start) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, int parts, int schedule) {
+  if (a.k_scales && a.hdr->pad[0] != 1) return;  // 4-bit calls: plan_q4_kernel has checked the users
   const int u = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
   __shared__ int s_ok, s_n, s_tso, s_pages, s_last;
@@ -152,6 +153,73 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, in
     return;
   }
   build_schedule(a, hist, start);
+}
+
+// ---------------------------------------------------------------------------
+// plan of the 4-bit cache's kernels, in one block: clears the header and the
+// counters, checks every user's offsets, lengths and candidate count (hdr->pad[0] =
+// 1 if all are good; the kernels behind return otherwise, so nothing is read by way
+// of offsets that do not hold), and lists the users (order) or their 128-row query
+// tiles (tiles: user and tile; -1 behind the last).  Up to kPlanUsers users come in
+// the order of their lengths, longest first, so that the last CTAs to start are short
+// ones: 64 users of 1000 to 8192 tokens in their own order kept a third of the SMs
+// waiting for the longest (97 us against 81).  Larger batches, whose users each get a
+// small part of the GPU, keep their own order.
+// ---------------------------------------------------------------------------
+constexpr int kPlanUsers = 512;
+
+__global__ void __launch_bounds__(kPlanUsers) plan_q4_kernel(const AttnArgs a, int32_t* counters, int n_counters,
+                                                             int32_t* order, int2* tiles, int n_tiles) {
+  __shared__ int len[kPlanUsers], user[kPlanUsers], scan[kPlanUsers / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  for (int x = tid; x < (int)(sizeof(WsHeader) / 4); x += threads) reinterpret_cast<int32_t*>(a.hdr)[x] = 0;
+  for (int x = tid; x < n_counters; x += threads) counters[x] = 0;
+  const bool sorted = a.B <= threads;
+  const int mine = sorted && tid < a.B ? a.cached_lens[tid] : 0;
+  if (sorted) len[tid] = mine;
+  __syncthreads();
+  int bad = 0;
+  for (int u = tid; u < a.B; u += threads) {
+    int n, tso, pages;
+    if (!check_user(a, u, n, tso, pages)) {
+      report_error(a.hdr, kErrLength, u);
+      bad = 1;
+    }
+  }
+  if (sorted && tid < a.B) {
+    int rank = 0;
+    for (int u = 0; u < a.B; ++u) rank += len[u] > mine || (len[u] == mine && u < tid);
+    user[rank] = tid;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) return;
+  if (tid == 0) a.hdr->pad[0] = 1;
+  if (order)
+    for (int x = tid; x < a.B; x += threads) order[x] = sorted ? user[x] : x;
+  if (!tiles) return;
+  // thread t lists the tiles of users t * per .. (in the order above) behind those of the threads before
+  const int per = (a.B + threads - 1) / threads, lo = min(a.B, tid * per), hi = min(a.B, lo + per);
+  auto tiles_of = [&](int u) { return (a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile; };
+  int count = 0;
+  for (int x = lo; x < hi; ++x) count += tiles_of(sorted ? user[x] : x);
+  int incl = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int at = incl - count, total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < warp) at += scan[w];
+    total += scan[w];
+  }
+  for (int x = lo; x < hi; ++x) {
+    const int u = sorted ? user[x] : x, m = tiles_of(u);
+    for (int t = 0; t < m; ++t) tiles[at++] = make_int2(u, t);
+  }
+  for (int x = total + tid; x < n_tiles; x += threads) tiles[x] = make_int2(-1, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -585,6 +653,13 @@ cudaError_t launch_plan(const AttnArgs& a, bool schedule, int max_seq_len, cudaS
   // enough blocks per user that a long user's timestamps are checked in parallel
   const int parts = std::max(1, std::min(16, ceil_div(std::max(max_seq_len, 1), 1024)));
   plan_kernel<<<a.B * parts, kPlanThreads, 0, s>>>(a, parts, schedule ? 1 : 0);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
+                           int n_tiles, cudaStream_t s) {
+  const int threads = std::min(kPlanUsers, std::max(64, (a.B + 31) / 32 * 32));
+  plan_q4_kernel<<<1, threads, 0, s>>>(a, counters, n_counters, order, tiles, n_tiles);
   return cudaGetLastError();
 }
 

@@ -124,6 +124,26 @@ def test_append_many_users_and_long_rows():
     c.assert_same()
 
 
+@pytest.mark.parametrize("B", [255, 256, 257])
+def test_append_users_of_one_block(B):
+    rng = np.random.default_rng(B)
+    c = Cache4(B, 1, 32, num_pages=2 * B, max_pages=3, P=8, seed=B)
+    for _ in range(2):
+        counts = rng.integers(0, 8, size=B)
+        counts[-1] = 5
+        T = int(counts.sum())
+        assert c.append(rows_of(rng, T, 1, 32, "bf16"), rows_of(rng, T, 1, 32, "bf16"), counts) == (0, 0)
+        c.assert_same()
+
+
+def test_the_other_pools_append_takes_no_4bit_pool():
+    c = Cache4(2, 1, 32, num_pages=4, max_pages=2, P=8, seed=1)
+    k = torch.zeros(3, 1, 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(KeyError):
+        hstu.hstu_kv_append(k, k, dev(np.array([0, 2, 3], np.int32)), c.g[0], c.g[1], c.table, c.lens, c.free, c.fc)
+    c.assert_same()
+
+
 def test_append_failures_change_nothing():
     rng = np.random.default_rng(4)
     H, d = 2, 64
@@ -394,6 +414,57 @@ def test_device_errors(rows):
     off[2] -= 1
     assert status(dataclasses.replace(pb, ts_offsets=off)) == -4
     assert status(pb) == 0
+    check_raw(pb, p4, val, True)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(force_simt=True)])
+@pytest.mark.parametrize("rows", [1, 20, 200])
+def test_offsets_past_the_timestamps_are_not_followed(rows, kw):
+    """User 1's own numbers hold, but only user 0's wrong ones put its timestamps where they are said to be."""
+    pb, p4, val = batch([100, 60], [rows, rows], [0, 0], seed=21)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    off = np.array([0, 10 ** 9, 10 ** 9 + 60 + rows], np.int32)
+    run_q4(dataclasses.replace(pb, ts_offsets=off), p4, workspace=ws, **kw)
+    assert hstu.hstu_check_device_error(ws) == -4
+    check_raw(pb, p4, val, not kw, **kw)
+
+
+@pytest.mark.parametrize("H,d", [(2, 128), (3, 64), (1, 32), (2, 96)])
+@pytest.mark.parametrize("acts,cands", [([1, 2], [0, 0]), ([4, 9], [6, 3])])
+def test_long_histories(H, d, acts, cands):
+    """Sequences past the length up to which a weight of a few-row call is held in two bf16 terms."""
+    pb, p4, val = batch([2500, 130], acts, cands, H, d, n_max=4096, seed=d, gamma=True)
+    check_raw(pb, p4, val, True)
+    check_y(pb, p4, val)
+
+
+@pytest.mark.parametrize("B,rows", [(150, 2), (513, 1), (600, 3), (530, 17)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_users(B, rows, dtype):
+    """More users than are put in order of their lengths, some without cached and some without new tokens."""
+    rng = np.random.default_rng(B)
+    cached = rng.integers(0, 40, size=B)
+    acts = rng.integers(0, 2 * rows + 1, size=B)
+    acts[7] = acts[-1] = rows
+    pb, p4, val = batch(cached, acts, rng.integers(0, 2, size=B), 1, 128, 256, 8, dtype, seed=B)
+    check_raw(pb, p4, val, dtype == "bf16")
+
+
+def test_one_user_has_most_of_the_rows():
+    pb, p4, val = batch([3] * 20 + [333], [1] * 20 + [150], [0] * 20 + [90], 2, seed=22)
+    check_raw(pb, p4, val, True)
+    check_y(pb, p4, val)
+    pb, p4, val = batch([3] * 20 + [333], [1] * 20 + [150], [0] * 20 + [90], 2, 64, dtype="f32", seed=23)
+    check_raw(pb, p4, val, False)
+
+
+def test_users_without_new_rows_are_checked_in_small_calls():
+    pb, p4, val = batch([100, 60, 20], [1, 0, 2], [0, 0, 0], seed=24)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    table = pb.kv_page_table.copy()
+    table[1, 0] = p4.k_pool.shape[0]
+    run_q4(dataclasses.replace(pb, kv_page_table=table), p4, workspace=ws)
+    assert hstu.hstu_check_device_error(ws) == -9
     check_raw(pb, p4, val, True)
 
 
