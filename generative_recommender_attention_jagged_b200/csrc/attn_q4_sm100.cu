@@ -22,9 +22,9 @@
 //     two V rows (cp.async) into places of its own two tiles ahead, so nothing is handed
 //     over; four lanes a row (64 contiguous bytes).  One set of sixteen warps doing both in
 //     turn took 2.9 us a tile: every warp waits for the same barriers at the same time.
-//   - they also look the tiles' pages, scales and timestamps up (KeyInfo, 4 stages: page id,
-//     scales and codes each a tile ahead of the next); one more warp builds the position
-//     window (2 stages), one issues the MMAs.
+//   - they also look the tiles' pages, scales and timestamps up, for two tiles at once (KeyInfo,
+//     8 stages: page ids, scales and codes each two tiles ahead of the next); one more warp
+//     builds the position window (2 stages), one issues the MMAs.
 //
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
 // row that is not finite is stored as zeros and its scale set to NaN: the mask is
@@ -46,7 +46,7 @@ constexpr int kWideThreads = 32 * kWideWarps;
 constexpr int kMmaWarp = kEwWarps + kWideWarps;  // MMA issuer, TMEM owner, Q
 constexpr int kWinWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 2);
-constexpr int kKeyStages = 4;
+constexpr int kKeyStages = 8;
 constexpr int kWinStages = 2;
 constexpr int kTailTiles = 4;             // what a user's last tiles cost beyond the others, in tiles
 constexpr uint32_t kTmemCols = 512;       // S0 [0,128) S1 [128,256) O [256,384)
@@ -388,79 +388,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     // eight different places
     const int wr = 16 * (warp - kEwWarps) + (lane >> 2), wq = lane & 3;
     const int flip = wq & 2;
-    const uint32_t wbase = (wq >> 1) * kHalfBytes + wr * 128;
-    const int wchunk = 4 * (wq & 1);
-    // The warp looks its 16 keys up itself, one a lane (lanes 16 .. 31 as lanes 0 .. 15): page id,
-    // then scales and time, then the codes, each a tile ahead of the next.
-    const int kc = 16 * (warp - kEwWarps) + (lane & 15);
+    uint32_t place[4];  // of the four chunks of row wr in a tile (row wr + 8: 1024 bytes on)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      place[c] = (wq >> 1) * kHalfBytes + wr * 128 + (((4 * (wq & 1) + (c ^ flip)) ^ (wr & 7)) << 4);
+    // The warp looks its 16 keys up itself, one a lane and two tiles at once (lanes 0 .. 15: the even
+    // one): page id, then scales and time, then the codes, each two tiles ahead of the next.
+    const int kc = 16 * (warp - kEwWarps) + (lane & 15), odd = lane >> 4;
+    constexpr uint32_t kNoRow = ~0u;  // (a pool has fewer rows: attn_q4_small_supported)
     int pid = 0;
-    long long row = -1, ts = 0, ts_before = 0;
+    uint32_t row = kNoRow, row_next = kNoRow;  // pool row of the lane's key
+    long long ts = 0, ts_before = 0;
     uint32_t km = 0, vm = 0;
-    uint32_t zz0 = 0, zz1 = 0, zz2 = 0;  // 128 + zero of key | value as bf16: of the tile being widened and the next two
+    uint32_t zz0 = 0, zz1 = 0;  // 128 + zero of key | value as bf16: of the tiles being widened and the next two
     bool sorted = true;
     auto in_range = [](long long x) { return x <= kTsLimit && x >= -kTsLimit; };
     auto load_page = [&](int t) {
       int k0, width;
-      key_tile(g, tb + t, k0, width);
+      if (t + odd >= cnt) return;
+      key_tile(g, tb + t + odd, k0, width);
       pid = k0 < g.L ? table[page_index(a, k0 + min(kc, width - 1))] : 0;
     };
     auto load_scales = [&](int t) {
       int k0, width;
-      key_tile(g, tb + t, k0, width);
+      row_next = kNoRow;
+      if (t + odd >= cnt) return;
+      key_tile(g, tb + t + odd, k0, width);
       const int j = k0 + min(kc, width - 1);
       const bool in = pid >= 0 && pid < a.num_pages;
       if (!in) report_error(a.hdr, kErrPage, user);
-      row = ((long long)(in ? pid : 0) * a.H + head) * a.page_size + (k0 < g.L ? j - page_index(a, j) * a.page_size : 0);
-      km = a.k_scales[row];
-      vm = a.v_scales[row];
+      const uint32_t r = ((uint32_t)(in ? pid : 0) * a.H + head) * a.page_size +
+                         (k0 < g.L ? j - page_index(a, j) * a.page_size : 0);
+      km = a.k_scales[r];
+      vm = a.v_scales[r];
       ts = a.ts[g.tso + j];
-      ts_before = checks && j > 0 ? a.ts[g.tso + j - 1] : LLONG_MIN;
-      if (!in || k0 >= g.L || kc >= width) row = -1;
+      if (checks) ts_before = j > 0 ? a.ts[g.tso + j - 1] : LLONG_MIN;
+      if (in && k0 < g.L && kc < width) row_next = r;
     };
-    // tile t's KeyInfo, and its codes into this thread's own places
+    // the KeyInfo of tiles t and t + 1
     auto announce = [&](int t) {
       int k0, width;
-      key_tile(g, tb + t, k0, width);
-      KeyInfo& key = sm.key[t % kKeyStages];
-      const bool held = row >= 0, fresh = k0 >= g.L && kc < width;  // cached; a new token
-      sorted &= !checks || (ts >= ts_before && in_range(ts));
-      if (lane < 16) {
+      row = row_next;
+      const bool held = row != kNoRow;  // cached
+      const int tl = t + odd;
+      if (tl < cnt) {
+        key_tile(g, tb + tl, k0, width);
+        const bool fresh = k0 >= g.L && kc < width;  // a new token
+        KeyInfo& key = sm.key[tl % kKeyStages];
+        if (checks) sorted &= ts >= ts_before && in_range(ts);
         key.ts[kc] = ts;
         key.ks[kc] = held ? 0.5f * a.alpha * meta_scale(km) : fresh ? 0.5f * a.alpha : 0.f;
         reinterpret_cast<uint16_t*>(key.vs)[kc] = (uint16_t)(held ? vm : fresh ? 0x3F80u : 0u);
       }
-      zz2 = held ? pack_bf16x2(128.f + meta_zero(km), 128.f + meta_zero(vm)) : 0x43004300u;  // exact
-      warp_arrive(&sm.bar_key_full[t % kKeyStages]);
+      zz1 = held ? pack_bf16x2(128.f + meta_zero(km), 128.f + meta_zero(vm)) : 0x43004300u;  // exact
+      __syncwarp();
+      if ((lane & 15) == 0 && tl < cnt) mbar_arrive(&sm.bar_key_full[tl % kKeyStages]);
+    };
+    // tile t's codes into this thread's own places
+    auto copy_codes = [&](int t) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const long long r = __shfl_sync(~0u, row, (lane >> 2) + 8 * x);
-        if (r >= 0) {
-          cp16_ca(&sm.codes[t & 1][0][x][wt], kp + r * 64 + 16 * wq);
-          cp16_ca(&sm.codes[t & 1][1][x][wt], vp + r * 64 + 16 * wq);
+        const uint32_t r = __shfl_sync(~0u, row, 16 * (t & 1) + (lane >> 2) + 8 * x);
+        if (r != kNoRow) {
+          cp16_ca(&sm.codes[t & 1][0][x][wt], kp + (size_t)r * 64 + 16 * wq);
+          cp16_ca(&sm.codes[t & 1][1][x][wt], vp + (size_t)r * 64 + 16 * wq);
         }
       }
     };
     auto store_rows = [&](uint8_t* tile, int t, int which) {  // which: 0 K, 1 V
-      KeyInfo& key = sm.key[t % kKeyStages];
       int k0, width;
       key_tile(g, tb + t, k0, width);
+      const uint32_t base = smem_u32(tile);
       if (k0 < g.L) {  // cached keys
         uint4 w[2];
         uint32_t zz[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           w[x] = sm.codes[t & 1][which][x][wt];
-          const uint32_t z = __shfl_sync(~0u, zz0, (lane >> 2) + 8 * x);
+          const uint32_t z = __shfl_sync(~0u, zz0, 16 * (t & 1) + (lane >> 2) + 8 * x);
           zz[x] = __byte_perm(z, z, which ? 0x3232 : 0x1010);
           // (rows past the width: what an earlier tile left, finite numbers under scales of 0)
           if (flip) w[x] = make_uint4(w[x].z, w[x].w, w[x].x, w[x].y);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const uint32_t base = smem_u32(tile) + wbase + x * 8 * 128;
           const uint32_t ww[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) sts_v4(base + (((wchunk + (c ^ flip)) ^ (wr & 7)) << 4), widen8(ww[c], zz[x]));
+          for (int c = 0; c < 4; ++c) sts_v4(base + place[c] + 1024 * x, widen8(ww[c], zz[x]));
         }
       } else {  // new tokens: bf16 rows as they are (zeros past the width)
 #pragma unroll 1
@@ -474,27 +488,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool bad = false;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            w[c] = on ? src[c] : make_uint4(0, 0, 0, 0);
+            w[c] = on ? src[c ^ flip] : make_uint4(0, 0, 0, 0);
             bad |= not_finite(w[c].x) | not_finite(w[c].y) | not_finite(w[c].z) | not_finite(w[c].w);
           }
           if (which) {  // a value row that is not finite: zeros, and a weight of NaN for the rows that see it
             bad = __any_sync(0xFu << (lane & ~3), bad);
-            if (bad && wq == 0) reinterpret_cast<uint16_t*>(key.vs)[r] = 0x7FC0u;
+            if (bad && wq == 0) reinterpret_cast<uint16_t*>(sm.key[t % kKeyStages].vs)[r] = 0x7FC0u;
           }
-          const uint32_t base = smem_u32(tile) + wbase + x * 8 * 128;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            sts_v4(base + (((wchunk + c) ^ (wr & 7)) << 4), which && bad ? make_uint4(0, 0, 0, 0) : w[c]);
+            sts_v4(base + place[c] + 1024 * x, which && bad ? make_uint4(0, 0, 0, 0) : w[c]);
         }
       }
       fence_proxy_async_smem();
     };
     bool ok = true;
 #pragma unroll 1
-    for (int t = -4; ok && t < cnt; ++t) {
+    for (int t = -6; ok && t < cnt; ++t) {
       const int b = t & 1;
-      zz0 = zz1;
-      zz1 = zz2;
+      if (b == 0) zz0 = zz1;
       if (t >= 0) {
         cp_wait<1>();
         // K(t) over K(t - 2), which S(t - 2) has read; then V(t) over V(t - 2)
@@ -508,16 +520,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (t + 2 >= 0 && t + 2 < cnt) {
-        const int s = (t + 2) % kKeyStages;
-        if (t + 2 >= kKeyStages)
-          ok = warp_wait(&sm.bar_key_empty[s], (((t + 2) / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51);
-        if (!ok) break;
-        announce(t + 2);
+      if (t >= -2 && t + 2 < cnt) {
+        if (b == 0) {  // tiles t + 2 and t + 3
+          const int tl = t + 2 + odd;
+          if ((lane & 15) == 0 && tl < cnt && tl >= kKeyStages)
+            ok = lane_wait(&sm.bar_key_empty[tl % kKeyStages], ((tl / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          announce(t + 2);
+        }
+        copy_codes(t + 2);
       }
       if (t >= -2) cp_commit();
-      if (t + 3 >= 0 && t + 3 < cnt) load_scales(t + 3);
-      if (t + 4 < cnt) load_page(t + 4);
+      if (b == 0) {
+        if (t >= -4 && t + 4 < cnt) load_scales(t + 4);
+        if (t + 6 < cnt) load_page(t + 6);
+      }
     }
     if (checks && split == a.num_splits - 1 && warp == kEwWarps)  // the candidates, which are no tile's keys
       for (int j = g.h + lane; j < g.n; j += 32)
