@@ -240,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head = (int)(blockIdx.x / a.num_splits) % a.H;
   const int qt = (int)(blockIdx.x / a.num_splits) / a.H;
 
-  if (a.hdr->pad[0] != 1) return;  // a user's lengths do not hold
+  grid_dependency_wait();
+  const int valid = a.hdr->pad[0];
   const int2 item = tiles[qt];
   const int user = item.x;
-  if (user < 0) return;
+  if (valid != 1 || user < 0) return;  // a user's lengths do not hold, or no tile
   const TileGeom g = tile_geom(a, user, item.y);
   // The last tiles (recent keys: a bucket edge every few columns; masked and new ones) take two to
   // three times the others' time: they count for more when the keys are split.
@@ -685,11 +686,8 @@ cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, cons
   }
   const long long ctas = ((long long)a.T_q / kTile + a.B) * a.H * a.num_splits;  // a CTA per listed tile, head and split
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  if (a.precise_silu)
-    attn_q4_sm100_kernel<true><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tiles, tm_q);
-  else
-    attn_q4_sm100_kernel<false><<<(unsigned)ctas, kThreads, kSmemBytes, s>>>(a, thr, tiles, tm_q);
-  return cudaGetLastError();
+  return launch_dependent(a.precise_silu ? attn_q4_sm100_kernel<true> : attn_q4_sm100_kernel<false>,
+                          dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, a, thr, tiles, tm_q);
 }
 
 }  // namespace hstu

@@ -106,14 +106,13 @@ struct __align__(16) SmallSmem {
   int last;
 };
 
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
-               : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp8(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 8 : 0)
-               : "memory");
+__device__ __forceinline__ void cp8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
+// (zero where off)
 __device__ __forceinline__ void cp4(void* dst, const void* src, bool on) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
                : "memory");
@@ -198,8 +197,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  if (a.hdr->pad[0] != 1) return;  // a user's lengths do not hold
-  const int u = order[blockIdx.z];
+  grid_dependency_wait();
+  const int valid = a.hdr->pad[0], u = order[blockIdx.z];
+  if (valid != 1) return;  // a user's lengths do not hold
   const int q0 = a.q_offsets[u], rows = a.q_offsets[u + 1] - q0;
   const int L = a.cached_lens[u], n = L + rows;
   const int part = part_keys(L, a.num_splits);
@@ -307,24 +307,25 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     auto fetch = [&](int m, int pid) {
       if (m < mine) {
         const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
-        // a page id out of range is reported above; its rows are not touched
-        const bool on = j < k_hi && pid >= 0 && pid < a.num_pages;
+        // past the part's end and for a page id out of range (reported by check_keys) the codes are those of
+        // the pool's first row, under scales and zero points of 0
+        const bool on = j < k_hi && (unsigned)pid < (unsigned)a.num_pages;
         Stage<D>& st = ring[m % kRing];
         // (the pool has fewer than 2^32 rows: attn_q4_small_supported)
         const uint32_t slot =
-            on ? ((uint32_t)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : ~0u;
+            on ? ((uint32_t)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : 0;
         constexpr int kPieces = D / 32;  // 16-byte pieces of a row
+        const uint32_t k_to = smem_u32(st.k), v_to = smem_u32(st.v);
 #pragma unroll
         for (int x = 0; x < kPieces; ++x) {
           const int c = 32 * x + lane, row = c / kPieces, piece = c % kPieces;
           const uint32_t s = __shfl_sync(~0u, slot, row);
-          const size_t from = s == ~0u ? 0 : (size_t)s * (D / 2) + piece * 16;
-          cp16(st.k + row * (D / 2) + piece * 16, kp + from, s != ~0u);
-          cp16(st.v + row * Stage<D>::kVRow + piece * 16, vp + from, s != ~0u);
+          cp16(k_to + row * (D / 2) + piece * 16, kp + piece * 16 + (size_t)s * (D / 2));
+          cp16(v_to + row * Stage<D>::kVRow + piece * 16, vp + piece * 16 + (size_t)s * (D / 2));
         }
-        cp4(&st.km[lane], a.k_scales + (on ? slot : 0), on);
-        cp4(&st.vm[lane], a.v_scales + (on ? slot : 0), on);
-        cp8(&st.ts[lane], ts + min(j, n - 1), true);
+        cp4(&st.km[lane], a.k_scales + slot, on);
+        cp4(&st.vm[lane], a.v_scales + slot, on);
+        cp8(&st.ts[lane], ts + min(j, n - 1));
       }
       cp_commit();
     };
@@ -674,9 +675,8 @@ cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters,
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  attn_q4_small_kernel<T, D, NQ, WT>
-      <<<dim3(a.num_splits * row_groups, a.H, a.B), kThreads, smem, s>>>(a, thr, counters, order, row_groups);
-  return cudaGetLastError();
+  return launch_dependent(attn_q4_small_kernel<T, D, NQ, WT>, dim3(a.num_splits * row_groups, a.H, a.B), dim3(kThreads),
+                          smem, s, a, thr, counters, order, row_groups);
 }
 
 template <typename T, int NQ, int WT>

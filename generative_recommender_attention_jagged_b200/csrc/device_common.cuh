@@ -110,6 +110,11 @@ __device__ __forceinline__ void split_range(int n_tiles, int s, int S, int& tb, 
   te = (int)(((long long)n_tiles * (s + 1)) / S);
 }
 
+// Programmatic dependent launch (launch_dependent in hstu_internal.h): the kernel in front lets the next one's
+// blocks start, and they wait here until it has completed and its writes are seen.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 constexpr long long kTsLimit = 1ll << 61;  // |timestamp| bound that keeps t_i + 1 - thr in range
 
 // checks of one user's offsets, lengths and candidate count (0 = bad)

@@ -132,6 +132,23 @@ cudaError_t launch_attn_sm100_single(const AttnArgs& a, const BucketTable& thr, 
                                      const CUtensorMap& tm_kpool, const CUtensorMap& tm_vpool, cudaStream_t s);
 cudaError_t launch_attn_simt(const AttnArgs& a, const BucketTable& thr, cudaStream_t s);
 
+// Launches a kernel whose blocks may start before the kernel in front of it on the stream has completed; it calls
+// grid_dependency_wait before it touches anything that kernel writes (or that kernels before it read).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Checks of the users and the order of the work for the 4-bit kernels (hstu_kernels.cu).
 cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
                            int n_tiles, cudaStream_t s);

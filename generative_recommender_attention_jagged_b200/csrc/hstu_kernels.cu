@@ -171,6 +171,7 @@ constexpr int kPlanUsers = 512;
 __global__ void __launch_bounds__(kPlanUsers) plan_q4_kernel(const AttnArgs a, int32_t* counters, int n_counters,
                                                              int32_t* order, int2* tiles, int n_tiles) {
   __shared__ int len[kPlanUsers], user[kPlanUsers], scan[kPlanUsers / 32];
+  grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   for (int x = tid; x < (int)(sizeof(WsHeader) / 4); x += threads) reinterpret_cast<int32_t*>(a.hdr)[x] = 0;
   for (int x = tid; x < n_counters; x += threads) counters[x] = 0;
