@@ -595,17 +595,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   __threadfence();
   const int HD = a.H * D;  // a multiple of 32, at most 1024
   const float inv_n = 1.f / (float)a.n_max;
+  static_assert(sizeof(sm.ring) >= kWarps * 1024 * sizeof(float));
+  float* sums = reinterpret_cast<float*>(sm.ring);  // [kWarps][HD]
+  // four rows at a time: all threads add their parts (eight loads each on the way), then a warp finishes a row
 #pragma unroll 1
-  for (int x0 = warp;; x0 += kWarps) {  // the x0-th of this group's rows
-    const int r = 8 * NQ * (rg + x0 / (8 * NQ) * row_groups) + x0 % (8 * NQ);
-    if (8 * NQ * (rg + x0 / (8 * NQ) * row_groups) >= rows) break;
-    if (r >= rows) continue;
-    const size_t row = q0 + r;
+  for (int x0 = 0;; x0 += kWarps) {
+    const int base = 8 * NQ * (rg + x0 / (8 * NQ) * row_groups), first = base + x0 % (8 * NQ);
+    if (base >= rows) break;
+    const int nr = min(kWarps, rows - first);
+    if (nr <= 0) continue;
+    const size_t row = q0 + first + min(warp, nr - 1);
     float2 x[16], uv[16];
-    float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      x[k] = make_float2(0.f, 0.f);
       uv[k] = make_float2(0.f, 0.f);
       if (!a.out_raw && 64 * k + 2 * lane < HD) {  // the gate on its way with the sums
         const T* uu = static_cast<const T*>(a.u) + row * a.u_stride + 64 * k + 2 * lane;
@@ -613,24 +615,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
       }
     }
 #pragma unroll 1
-    for (int s = 0; s < parts; ++s) {  // the features' loads are independent
-      const float* src = a.o_ws + ((size_t)s * a.T_q + row) * HD + 2 * lane;
-      float2 y[16];
+    for (int e = 4 * threadIdx.x; e < nr * HD; e += 4 * kThreads) {
+      const float* src = a.o_ws + (size_t)(q0 + first) * HD + e;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int part0 = 0; part0 < parts; part0 += 8) {
+        float4 y[8];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        y[k] = 64 * k + 2 * lane < HD ? __ldcg(reinterpret_cast<const float2*>(src + 64 * k)) : make_float2(0.f, 0.f);
+        for (int i = 0; i < 8; ++i)
+          y[i] = part0 + i < parts ? __ldcg(reinterpret_cast<const float4*>(src + (size_t)(part0 + i) * a.T_q * HD))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        x[k].x += y[k].x;
-        x[k].y += y[k].y;
+        for (int i = 0; i < 8; ++i) {
+          s.x += y[i].x;
+          s.y += y[i].y;
+          s.z += y[i].z;
+          s.w += y[i].w;
+        }
       }
+      *reinterpret_cast<float4*>(sums + e) = make_float4(s.x * inv_n, s.y * inv_n, s.z * inv_n, s.w * inv_n);
     }
+    __syncthreads();
+    float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      x[k].x *= inv_n;
-      x[k].y *= inv_n;
+      x[k] = 64 * k + 2 * lane < HD ? *reinterpret_cast<const float2*>(sums + min(warp, nr - 1) * HD + 64 * k + 2 * lane)
+                                    : make_float2(0.f, 0.f);
       sum += x[k].x + x[k].y;
     }
+    __syncthreads();  // (the next rows' sums go over these)
+    if (warp >= nr) continue;
     if (a.out_raw) {
       float* out = static_cast<float*>(a.out) + row * HD + 2 * lane;
 #pragma unroll

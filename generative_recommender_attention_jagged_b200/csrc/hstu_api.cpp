@@ -454,9 +454,11 @@ int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max
     const long long s = std::max<long long>(1, num_sms() / units);
     return (int32_t)std::max<long long>(1, std::min<long long>({s, (key_tiles + 1) / 2, kMaxSplits}));
   }
-  // about eight CTAs an SM: two waves of them even out users of different length
-  const long long tiles = std::max<long long>(p->batch, p->total_tokens / 16);
-  const long long s = std::max<long long>(1, (long long)num_sms() * 8 / (tiles * p->num_heads));
+  // about six CTAs an SM, which even out users of different length (64 users of 1000 to 8192 keys, 4 heads: 1, 2, 3,
+  // 4 and 6 splits took 141, 88, 79, 81 and 86 us; 16 users: 6, 9, 13, 18 and 27 took 38, 38, 38, 41 and 44), and
+  // two parts a user as long as that is not two waves of CTAs too many (200 users: 177 us against 191)
+  const long long units = std::max<long long>(p->batch, p->total_tokens / 16) * p->num_heads, sms = num_sms();
+  const long long s = std::max<long long>(units <= 8 * sms ? 2 : 1, 6 * sms / units);
   const long long most = std::max(1, (max_cached_len + 255) / 256);  // parts of 256 keys or more
   return (int32_t)std::min<long long>({s, most, kMaxSplits});
 }
