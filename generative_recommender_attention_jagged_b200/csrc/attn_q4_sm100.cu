@@ -109,7 +109,8 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 }
 // 8 codes of a word -> 8 bf16 code - zero (zz = the bf16 pair 128 + zero)
 __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t zz) {
-  return make_uint4(sub_bf16x2((w & 0x000F000Fu) | 0x43004300u, zz), sub_bf16x2(((w >> 4) & 0x000F000Fu) | 0x43004300u, zz),
+  return make_uint4(sub_bf16x2((w & 0x000F000Fu) | 0x43004300u, zz),
+                    sub_bf16x2(((w >> 4) & 0x000F000Fu) | 0x43004300u, zz),
                     sub_bf16x2(((w >> 8) & 0x000F000Fu) | 0x43004300u, zz),
                     sub_bf16x2(((w >> 12) & 0x000F000Fu) | 0x43004300u, zz));
 }
@@ -680,11 +681,13 @@ cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, cons
     cudaError_t e = cudaFuncSetAttribute(attn_q4_sm100_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_q4_sm100_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+      e = cudaFuncSetAttribute(attn_q4_sm100_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  const long long ctas = ((long long)a.T_q / kTile + a.B) * a.H * a.num_splits;  // a CTA per listed tile, head and split
+  // a CTA per listed tile, head and split
+  const long long ctas = ((long long)a.T_q / kTile + a.B) * a.H * a.num_splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   return launch_dependent(a.precise_silu ? attn_q4_sm100_kernel<true> : attn_q4_sm100_kernel<false>,
                           dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, a, thr, tiles, tm_q);

@@ -38,7 +38,7 @@
 //     as one bf16 term in calls with long histories, where its roundings average out
 //     (relative error of y 1.8e-3, of which 1.7e-3 is its own rounding), and as two
 //     where no sequence exceeds kTwoTermLength (with one: 2.3e-3 at 100 keys).  Two
-//     terms for all took 93 us instead of 84 for 64 users of 1000 to 8192 keys.
+//     terms for all took 90 us instead of 77 for 64 users of 1000 to 8192 keys.
 //   - fp32 calls split each row element and each weight into three bf16 terms
 //     (8 + 8 + 8 bits: what is left is below 2^-24 of it) and run each product
 //     three times, smallest terms first; code - zero is exact as it is, and every
@@ -184,7 +184,8 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
 // (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
 template <typename T, int D, int NQ, int WT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
-    attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int32_t* order, int row_groups) {
+    attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int32_t* order,
+                         int row_groups) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kTerms = kF32 ? 3 : 1;   // bf16 terms of a row element
   constexpr int kWTerms = kF32 ? 3 : WT; // and of a weight
@@ -444,8 +445,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
                          : "memory");
       }
       // ---- O^T += (codes' - vz) P^T
-      constexpr int kHalves = D / 32;  // 16-bit pieces (4 codes) of a V row a thread reads: its eighth of the dimensions
-      uint32_t vh[2][2][kHalves];      // [16 keys][lo, hi]: keys 2 t, 2 t + 1 (lo) or 2 t + 8, 2 t + 9 (hi) side by side
+      // 16-bit pieces (4 codes) of a V row a thread reads: its eighth of the dimensions
+      constexpr int kHalves = D / 32;
+      // [16 keys][lo, hi]: keys 2 t, 2 t + 1 (lo) or 2 t + 8, 2 t + 9 (hi) side by side
+      uint32_t vh[2][2][kHalves];
       uint32_t vz[2][2];
 #pragma unroll
       for (int half = 0; half < 2; ++half)
@@ -499,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int w = 0; w < NQ; ++w)
-              mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half], p[x][w][2 * half + 1]);
+              mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half],
+                       p[x][w][2 * half + 1]);
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
 #pragma unroll
@@ -639,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      x[k] = 64 * k + 2 * lane < HD ? *reinterpret_cast<const float2*>(sums + min(warp, nr - 1) * HD + 64 * k + 2 * lane)
-                                    : make_float2(0.f, 0.f);
+      const float* src = sums + min(warp, nr - 1) * HD + 64 * k + 2 * lane;
+      x[k] = 64 * k + 2 * lane < HD ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
       sum += x[k].x + x[k].y;
     }
     __syncthreads();  // (the next rows' sums go over these)
@@ -719,7 +723,8 @@ cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int3
   if (std::min(max_seq_len, a.n_max) <= kTwoTermLength)
     return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, order, groups, s)
                      : launch_d<bf16, 2, 2>(a, thr, counters, order, groups, s);
-  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, order, groups, s) : launch_d<bf16, 2, 1>(a, thr, counters, order, groups, s);
+  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, order, groups, s)
+                   : launch_d<bf16, 2, 1>(a, thr, counters, order, groups, s);
 }
 
 }  // namespace hstu

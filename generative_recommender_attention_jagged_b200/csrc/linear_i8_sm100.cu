@@ -60,7 +60,8 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ uint32_t amax(uint32_t m) const {
-    uint32_t p = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+    const uint32_t abs = 0x7FFF7FFFu;
+    const uint32_t p = __vmaxu2(__vmaxu2(v.x & abs, v.y & abs), __vmaxu2(v.z & abs, v.w & abs));
     return max(m, max(p & 0xFFFF0000u, p << 16));
   }
   __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -452,38 +453,15 @@ __device__ __forceinline__ bool group_all(bool ok, int group) {
   return r != 0;
 }
 
-// packed fp32 pairs
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // two int32 as fp32, each rounded once: the signed upper and unsigned lower 16 bits sit
 // exactly in the mantissa of 2^23
 __device__ __forceinline__ uint64_t ints_to_float2(uint32_t a, uint32_t b) {
-  const uint64_t hi = pack2(__uint_as_float(__byte_perm(a ^ 0x80000000u, 0x4B000000u, 0x7632)),
+  const uint64_t hi = pack_pair(__uint_as_float(__byte_perm(a ^ 0x80000000u, 0x4B000000u, 0x7632)),
                             __uint_as_float(__byte_perm(b ^ 0x80000000u, 0x4B000000u, 0x7632)));
-  const uint64_t lo = pack2(__uint_as_float((a & 0xFFFFu) | 0x4B000000u), __uint_as_float((b & 0xFFFFu) | 0x4B000000u));
-  const uint64_t h = add2(hi, pack2(-8421376.f, -8421376.f));  // 2^23 + 2^15
-  return fma2(h, pack2(65536.f, 65536.f), add2(lo, pack2(-8388608.f, -8388608.f)));
+  const uint64_t lo = pack_pair(__uint_as_float((a & 0xFFFFu) | 0x4B000000u),
+                                __uint_as_float((b & 0xFFFFu) | 0x4B000000u));
+  const uint64_t h = add_pair(hi, pack_pair(-8421376.f, -8421376.f));  // 2^23 + 2^15
+  return fma_pair(h, pack_pair(65536.f, 65536.f), add_pair(lo, pack_pair(-8388608.f, -8388608.f)));
 }
 
 template <typename TOut, bool SILU>
@@ -595,7 +573,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int row0 = (u / tiles_n) * 2 * kBM + rank * kBM;
       const int n0 = (u % tiles_n) * kPairBN + 64 * grp;
       const float xs = kFactor * (row0 + r < a.T ? a.x_scale[row0 + r] : 0.f);
-      const uint64_t xs2 = pack2(xs, xs);
+      const uint64_t xs2 = pack_pair(xs, xs);
       // the scales and biases of the group's columns (the barrier of the last tile's box is behind its reads)
       if (te < 64) {
         const int n = n0 + te;
@@ -635,13 +613,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int q = 0; q < 4; q += 2) {
               const uint32_t i0 = acc[x][e + k + q], i1 = acc[x][e + k + q + 1];
               // without tanh the special-function unit is free for the conversion
-              const uint64_t f2 = SILU ? ints_to_float2(i0, i1) : pack2(__int2float_rn((int)i0), __int2float_rn((int)i1));
-              const uint64_t v2 = fma2(f2, mul2(xs2, q ? pack2(wv.z, wv.w) : pack2(wv.x, wv.y)),
-                                       q ? pack2(bv.z, bv.w) : pack2(bv.x, bv.y));
+              const uint64_t f2 =
+                  SILU ? ints_to_float2(i0, i1) : pack_pair(__int2float_rn((int)i0), __int2float_rn((int)i1));
+              const uint64_t v2 = fma_pair(f2, mul_pair(xs2, q ? pack_pair(wv.z, wv.w) : pack_pair(wv.x, wv.y)),
+                                       q ? pack_pair(bv.z, bv.w) : pack_pair(bv.x, bv.y));
               float v0, v1;
-              unpack2(v2, v0, v1);
+              unpack_pair(v2, v0, v1);
               if constexpr (SILU && kBf16) {
-                unpack2(fma2(v2, pack2(tanh_approx(v0), tanh_approx(v1)), v2), y[k + q], y[k + q + 1]);
+                unpack_pair(fma_pair(v2, pack_pair(tanh_approx(v0), tanh_approx(v1)), v2), y[k + q], y[k + q + 1]);
               } else {
                 y[k + q] = SILU ? act_i8<TOut>(v0, 1) : v0;
                 y[k + q + 1] = SILU ? act_i8<TOut>(v1, 1) : v1;
@@ -825,7 +804,9 @@ using namespace hstu;
 
 extern "C" {
 
-size_t hstu_linear_i8_workspace_size(const hstu_linear_i8_params* p) { return check(p) == HSTU_OK ? ws_bytes_for(p) : 0; }
+size_t hstu_linear_i8_workspace_size(const hstu_linear_i8_params* p) {
+  return check(p) == HSTU_OK ? ws_bytes_for(p) : 0;
+}
 
 int hstu_quant_i8_weight(const void* w, int32_t d_in, int32_t d_out, hstu_dtype dtype, int8_t* w_q, float* w_scale,
                          hstu_stream_t stream) {
@@ -882,7 +863,8 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
     e = p->out_dtype == HSTU_DT_BF16
             ? (a.silu ? launch_pair<__nv_bfloat16, true>(a, xq, w_q, dev, sms, s)
                       : launch_pair<__nv_bfloat16, false>(a, xq, w_q, dev, sms, s))
-            : (a.silu ? launch_pair<float, true>(a, xq, w_q, dev, sms, s) : launch_pair<float, false>(a, xq, w_q, dev, sms, s));
+            : (a.silu ? launch_pair<float, true>(a, xq, w_q, dev, sms, s)
+                      : launch_pair<float, false>(a, xq, w_q, dev, sms, s));
   else
     e = p->out_dtype == HSTU_DT_BF16 ? launch_single<128, __nv_bfloat16>(a, xq, w_q, dev, s)
                                      : launch_single<128, float>(a, xq, w_q, dev, s);

@@ -80,13 +80,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// packed fp32 pairs (one instruction for two operations, each rounded as its scalar form)
+__device__ __forceinline__ uint64_t pack_pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack_pair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // x / s for |x / s| < 2^20, s and inv ~ 1 / s normal: the remainder of a first
 // product is exact, and adding its share again gives the quotient to half an ulp and
 // exactly where it has a short binary fraction (the correction is then off by far less
-// than the last bit).  Three operations of the FMA pipe.
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  const float q = x * inv;
-  return fmaf(fmaf(-q, s, x), inv, q);
+// than the last bit).  Three operations of the FMA pipe for two quotients.
+__device__ __forceinline__ uint64_t quotients(uint64_t x, uint64_t minus_s, uint64_t inv) {
+  const uint64_t q = mul_pair(x, inv);
+  return fma_pair(fma_pair(q, minus_s, x), inv, q);
 }
 
 struct Quant4 {
@@ -121,29 +146,47 @@ __device__ __forceinline__ Quant4 quant4_of(float lo, float hi, bool& clamp) {
 template <bool BF16>
 __device__ __forceinline__ uint32_t quant4_word(float s, float inv, float z, bool clamp, const float (&x)[8]) {
   if (s == 0.f) return 0;
-  float m[8];
+  const uint64_t ms2 = pack_pair(-s, -s), inv2 = pack_pair(inv, inv), magic2 = pack_pair(kRoundMagic, kRoundMagic),
+                 back2 = pack_pair(-kRoundMagic, -kRoundMagic);
+  uint64_t m[4];  // pairs of elements 2 i, 2 i + 1: kRoundMagic + rounded quotient
   bool half = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = quotient(x[i], s, inv);
-    m[i] = q + kRoundMagic;
-    if constexpr (!BF16) half = half || fabsf(q - (m[i] - kRoundMagic)) == 0.5f;
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t q = quotients(pack_pair(x[2 * i], x[2 * i + 1]), ms2, inv2);
+    m[i] = add_pair(q, magic2);
+    if constexpr (!BF16) {
+      float q0, q1, m0, m1;
+      unpack_pair(q, q0, q1);
+      unpack_pair(add_pair(m[i], back2), m0, m1);
+      half = half || fabsf(q0 - m0) == 0.5f || fabsf(q1 - m1) == 0.5f;
+    }
   }
   if (!BF16 && half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fix_quotient(x[i], s, m[i]);
+    for (int i = 0; i < 4; ++i) {
+      float m0, m1;
+      unpack_pair(m[i], m0, m1);
+      m[i] = pack_pair(fix_quotient(x[2 * i], s, m0), fix_quotient(x[2 * i + 1], s, m1));
+    }
   }
   if (clamp) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fminf(fmaxf(m[i], kRoundMagic - z), kRoundMagic + 15.f - z);
+    for (int i = 0; i < 4; ++i) {
+      float m0, m1;
+      unpack_pair(m[i], m0, m1);
+      m[i] = pack_pair(fminf(fmaxf(m0, kRoundMagic - z), kRoundMagic + 15.f - z),
+                   fminf(fmaxf(m1, kRoundMagic - z), kRoundMagic + 15.f - z));
+    }
   }
-  float even = z * 4369.f, odd = even;  // 0x1111
+  uint64_t sum = pack_pair(z * 4369.f, z * 4369.f);  // 0x1111
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    even = fmaf(m[2 * i] - kRoundMagic, (float)(1 << (4 * i)), even);
-    odd = fmaf(m[2 * i + 1] - kRoundMagic, (float)(1 << (4 * i)), odd);
+    const float w = (float)(1 << (4 * i));
+    sum = fma_pair(add_pair(m[i], back2), pack_pair(w, w), sum);
   }
-  return __byte_perm(__float_as_uint(even + 8388608.f), __float_as_uint(odd + 8388608.f), 0x5410);
+  float even, odd;
+  unpack_pair(add_pair(sum, pack_pair(8388608.f, 8388608.f)), even, odd);
+  return __byte_perm(__float_as_uint(even), __float_as_uint(odd), 0x5410);
 }
 
 // scale and zero point of a stored word
