@@ -704,7 +704,7 @@ cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counter
     case 32: return launch<T, 32, NQ, WT>(a, thr, counters, order, row_groups, s);
     case 64: return launch<T, 64, NQ, WT>(a, thr, counters, order, row_groups, s);
     case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, order, row_groups, s);
-    default: return launch<T, 128, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, order, row_groups, s);
+    default: return launch<T, 128, 1, WT>(a, thr, counters, order, row_groups, s);
   }
 }
 

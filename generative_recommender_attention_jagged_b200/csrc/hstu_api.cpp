@@ -139,25 +139,27 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
 }
 
 // ---- the 4-bit cache's kernels ----
-// kQ4Tc: bf16, d = 128 and on average more than 16 new rows a user: 128-row
+// kQ4Tc: bf16, d = 128 and on average more than 8 new rows a user: 128-row
 // tiles on tcgen05.  kQ4Small: the others up to d = 128, 8 or 16 rows a pass.
-// kQ4Simt: d > 128, or on request.
+// kQ4Simt: d > 128, or on request.  Small against Tc in us, 4 heads: 9 rows of one
+// user of 100 keys 34 / 23, of 8 users of 4000 keys 61 / 45, 12 rows of 64 users of up
+// to 8192 keys 180 / 189; with 8 rows 27 / 23, 43 / 45 and 119 / 189.
 enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 
 // pool_rows: num_pages * H * page_size, 0 where it is not known yet (workspace sizes: the CUDA-core kernel,
 // which pools of 2^32 rows fall back to, needs the least)
 Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
   if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, p->batch, pool_rows)) return kQ4Simt;
-  return use_tensor_cores(p) && (long long)p->total_tokens > 16ll * p->batch ? kQ4Tc : kQ4Small;
+  return use_tensor_cores(p) && (long long)p->total_tokens > 8ll * p->batch ? kQ4Tc : kQ4Small;
 }
 
 // Rows of one pass of the small kernel over the cached bytes: 16 where users have
 // more than 8 on average (fp32 calls with d > 64: 8, their three-term operands fill
-// the registers), and the CTAs that share a user's passes: room for twice the
+// the registers; bf16 calls with d = 128 and that many rows are kQ4Tc's), and the CTAs that share a user's passes: room for twice the
 // average number of rows, since users differ (a CTA without rows ends at once).
 int q4_small_rows(const hstu_attn_params* p) {
-  const bool wide_f32 = p->dtype == HSTU_DT_F32 && p->head_dim > 64;
-  return (long long)p->total_tokens <= 8ll * p->batch || wide_f32 ? 8 : 16;
+  const bool wide = p->head_dim > (p->dtype == HSTU_DT_F32 ? 64 : 96);
+  return (long long)p->total_tokens <= 8ll * p->batch || wide ? 8 : 16;
 }
 int q4_small_groups(const hstu_attn_params* p) {
   const long long rows = q4_small_rows(p), per = (long long)p->batch * rows;

@@ -856,10 +856,14 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   a.bias = bias;
   a.out = out;
   a.hdr = hdr;
-  // 256 x 256 tiles on SM pairs once they fill most of the GPU; 128 x 128 tiles on
-  // single SMs below (four times as many)
+  // 128 x 128 tiles on single SMs while one wave of them does; 256 x 256 tiles on SM
+  // pairs, persistent, above.  Single against pairs in us (with the quantisation of x):
+  // rows x d_in x d_out 700 x 208 x 40 7.3 / 9.8, 8 x 512 x 2048 9.2 / 10.0, 1024 x 512 x
+  // 2048 (128 tiles) 12.2 / 11.8, 2048 x 512 x 2048 (256) 20.5 / 12.1, 16384 x 512 x 512
+  // (512) 40 / 20.
+  const long long single_tiles = ((p->rows + kBM - 1) / kBM) * ((p->d_out + 127) / 128);
   cudaError_t e;
-  if (pair_units(p->rows, p->d_out) * 2 >= sms)
+  if (single_tiles > sms)
     e = p->out_dtype == HSTU_DT_BF16
             ? (a.silu ? launch_pair<__nv_bfloat16, true>(a, xq, w_q, dev, sms, s)
                       : launch_pair<__nv_bfloat16, false>(a, xq, w_q, dev, sms, s))

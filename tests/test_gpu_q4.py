@@ -314,6 +314,10 @@ CASES = [
     ([50], [6], [3], 4, 32, 7),
     ([40, 2], [2, 1], [1, 1], 3, 256, 16),
     ([45], [5], [0], 5, 96, 20),
+    ([70, 20], [10, 3], [4, 12], 2, 64, 16),
+    ([70, 20], [10, 3], [4, 12], 2, 96, 16),
+    ([70, 20], [8, 0], [0, 8], 4, 128, 16),
+    ([70, 20], [9, 0], [0, 8], 4, 128, 16),
 ]
 
 
