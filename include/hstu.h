@@ -215,9 +215,14 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
  * head_dim a multiple of 32, any positive page_size; the HSTU_F_STAGE_* flags
  * are not taken (HSTU_ERR_UNSUPPORTED).  A cached row with scale NaN makes the
  * rows that attend to it NaN.  After a device error `out` holds nothing of use.
- * The products use the codes as exact integers (code - zero is exact in bf16)
- * and apply the scales to the fp32 sums, so bf16 calls round what
- * hstu_attn_fwd_paged rounds (the weights a) and the cache adds no rounding.
+ * Lengths, offsets and candidate counts are checked for every user; page ids and
+ * timestamps at least for the users with new rows.
+ * The products use the codes as exact integers (code - zero is exact in bf16).
+ * A key's scale is applied to the fp32 score; a value's scale to the weight a, which
+ * bf16 calls round to bf16 as hstu_attn_fwd_paged does: once with its scale where
+ * users have 8 new rows or fewer on average (to two bf16 terms if no sequence
+ * exceeds 2048), before and after the scale where they have more.  fp32 calls keep
+ * 24 bits throughout.
  */
 size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_splits);
 int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len);
@@ -310,8 +315,9 @@ int hstu_layer_f2(const hstu_linear_params* p, const void* y, const void* w2, co
  *   scale_x[t] = max_k |x[t,k]| / 127             (fp32; 0 if below 2^-126)
  *   code[t,k]  = x[t,k] / scale_x[t] to the nearest integer, ties to even
  *   out[t,n]   = act(scale_x[t] * scale_w[n] * sum_k code[t,k] w_q[n,k] + bias[n])
- * with scale, bias and activation in fp32 and one rounding to out's type.  A
- * row of x with an infinity or NaN gives a row of NaN.
+ * with scales (multiplied with each other first), bias and activation in fp32
+ * and one rounding to out's type.  A row of x with an infinity or NaN gives a row
+ * of NaN.
  */
 #define HSTU_I8_MAX_D_IN 131072 /* 127 * 127 * d_in stays below 2^31 */
 
