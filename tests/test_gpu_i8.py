@@ -106,6 +106,22 @@ def test_ties_and_special_rows():
     check(y[ok], x[ok], wq.cpu().numpy(), ws.cpu().numpy(), b, False, "f32")
 
 
+def test_row_scales_are_exact():
+    """An element of code 1 under an identity matrix comes out as its row's scale, for amax over the whole fp32 range."""
+    rng = np.random.default_rng(77)
+    amax = rng.integers(1, 0x7F800000, size=20000, dtype=np.int64).astype(np.int32).view(np.float32)
+    edge = np.float32(127) * np.float32(2.0 ** -126)
+    amax[:64] = (np.full(64, edge).view(np.int32) + np.arange(-32, 32, dtype=np.int32)).view(np.float32)
+    amax[64:67] = np.finfo(np.float32).max, np.float32(2.0 ** -149), 127.0
+    want = amax / np.float32(127)             # IEEE division: rounded once
+    want[want < 2.0 ** -126] = 0
+    x = np.zeros((len(amax), 16), np.float32)
+    x[:, 0], x[:, 1] = amax, want
+    out = hstu.hstu_linear_i8(torch.from_numpy(x).cuda(), torch.eye(16, dtype=torch.int8, device="cuda"),
+                              torch.ones(16, device="cuda"))
+    assert np.array_equal(out[:, 1].cpu().numpy(), want)
+
+
 def test_strided_rows_and_neighbours_left_alone():
     T, K, N = 70, 256, 136
     xt, w, b = inputs(T, K, N, "bf16", seed=11)
