@@ -408,6 +408,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
         const long long tj = st.ts[lane];
         const float* bias_of = a.rab_pos - min(j, L);
         const float* sc_of = reinterpret_cast<const float*>(xs[lane]);
+        float pos_bias[8 * NQ];  // all rows' loads on the way before the first is used
+#pragma unroll
+        for (int r = 0; r < 8 * NQ; ++r) {
+          if (r >= nr) break;
+          pos_bias[r] = __ldg(bias_of + sm.rp[r]);
+        }
         uint32_t pk[kWTerms][4 * NQ];
 #pragma unroll
         for (int r = 0; r < 8 * NQ; r += 2) {
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if (r + e < nr) {
-              const float bias = __ldg(bias_of + sm.rp[r + e]) + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
+              const float bias = pos_bias[r + e] + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
               const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
               wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
             }
