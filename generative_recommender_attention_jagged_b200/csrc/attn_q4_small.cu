@@ -39,7 +39,7 @@
 //   - Weights: SiLU in fp32, sums in fp32.  a_ij vs_j goes into the second product
 //     as one bf16 term in calls with long histories, where its roundings average out
 //     (relative error of y 1.8e-3, of which 1.7e-3 is its own rounding), and as two
-//     where no sequence exceeds kTwoTermLength (with one: 2.3e-3 at 100 keys).  Two
+//     where no sequence exceeds kShortSequence (with one: 2.3e-3 at 100 keys).  Two
 //     terms for all took 90 us instead of 77 for 64 users of 1000 to 8192 keys.
 //   - fp32 calls split each row element and each weight into three bf16 terms
 //     (8 + 8 + 8 bits: what is left is below 2^-24 of it) and run each product
@@ -72,7 +72,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRing = 2;       // key tiles a warp has in shared memory
 constexpr int kKeys = 32;      // keys of a tile
-constexpr int kTwoTermLength = 2048;  // bound of the sequence lengths up to which bf16 weights are two terms
 constexpr int kMinPart = 256;  // keys below which a part is not split further
 
 template <int D>
@@ -728,7 +727,7 @@ cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int3
   if (!a.in_bf16)
     return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, order, groups, s)
                      : launch_d<float, 2, 3>(a, thr, counters, order, groups, s);
-  if (std::min(max_seq_len, a.n_max) <= kTwoTermLength)
+  if (std::min(max_seq_len, a.n_max) <= kShortSequence)
     return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, order, groups, s)
                      : launch_d<bf16, 2, 2>(a, thr, counters, order, groups, s);
   return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, order, groups, s)

@@ -172,7 +172,8 @@ int q4_tiles(const hstu_attn_params* p) { return p->total_tokens / kTile + p->ba
 
 Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
-  Layout l;  // header, the plan (few rows: users in order, a counter per user and row group; else tiles), partial sums
+  // header, the plan (few rows: users in order, a counter per user and row group; else tiles), partial sums
+  Layout l;
   l.max_items = 0;
   l.items_off = sizeof(WsHeader);
   const size_t plan = kernel == kQ4Small ? (size_t)p->batch * (1 + q4_small_groups(p)) * sizeof(int32_t)
@@ -298,10 +299,10 @@ int run(const hstu_attn_params* p, const Common& c) {
     int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
     int32_t* counters = order + a.B;
     const int groups = q4_small_groups(p);
-    if (launch_plan_q4(a, counters, a.B * groups, order, nullptr, 0, c.stream) != cudaSuccess ||
-        launch_attn_q4_small(a, thr, counters, order, q4_small_rows(p), groups, p->max_seq_len, c.stream) != cudaSuccess)
-      return HSTU_ERR_CUDA;
-    return HSTU_OK;
+    e = launch_plan_q4(a, counters, a.B * groups, order, nullptr, 0, c.stream);
+    if (e == cudaSuccess)
+      e = launch_attn_q4_small(a, thr, counters, order, q4_small_rows(p), groups, p->max_seq_len, c.stream);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
     a.num_splits = c.splits;
@@ -309,10 +310,10 @@ int run(const hstu_attn_params* p, const Common& c) {
     CUtensorMap tq;
     if (!encode_rows(&tq, c.q, a.T_q, a.H, a.d, a.qkv_stride)) return HSTU_ERR_CUDA;
     int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
-    if (launch_plan_q4(a, nullptr, 0, nullptr, tiles, q4_tiles(p), c.stream) != cudaSuccess ||
-        launch_attn_q4_sm100(a, thr, tiles, tq, c.stream) != cudaSuccess || launch_epilogue(a, c.stream) != cudaSuccess)
-      return HSTU_ERR_CUDA;
-    return HSTU_OK;
+    e = launch_plan_q4(a, nullptr, 0, nullptr, tiles, q4_tiles(p), c.stream);
+    if (e == cudaSuccess) e = launch_attn_q4_sm100(a, thr, tiles, tq, p->max_seq_len, c.stream);
+    if (e == cudaSuccess) e = launch_epilogue(a, c.stream);
+    return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (stages & HSTU_F_STAGE_PLAN) {
     e = q4 ? launch_plan_q4(a, nullptr, 0, nullptr, nullptr, 0, c.stream)

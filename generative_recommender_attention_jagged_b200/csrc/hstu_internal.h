@@ -149,6 +149,10 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// 4-bit bf16 calls in which no sequence exceeds this take the finer rounding of the weights (see the kernels): over
+// more keys the roundings average out.
+constexpr int kShortSequence = 2048;
+
 // Checks of the users and the order of the work for the 4-bit kernels (hstu_kernels.cu).
 cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
                            int n_tiles, cudaStream_t s);
@@ -164,7 +168,7 @@ cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int3
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128, tiles
 // [T_q / 128 + B] as launch_plan_q4 lists them; partial sums to o_ws, then launch_epilogue.
 cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const int2* tiles, const CUtensorMap& tm_q,
-                                 cudaStream_t s);
+                                 int max_seq_len, cudaStream_t s);
 
 // Backward of the attention core on CUDA cores (hstu_bwd.cu); gradients fp32,
 // d_rp / d_rt must be zeroed by the caller.

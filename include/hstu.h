@@ -219,10 +219,10 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
  * timestamps at least for the users with new rows.
  * The products use the codes as exact integers (code - zero is exact in bf16).
  * A key's scale is applied to the fp32 score; a value's scale to the weight a, which
- * bf16 calls round to bf16 as hstu_attn_fwd_paged does: once with its scale where
- * users have 8 new rows or fewer on average (to two bf16 terms if no sequence
- * exceeds 2048), before and after the scale where they have more.  fp32 calls keep
- * 24 bits throughout.
+ * bf16 calls round to bf16 as hstu_attn_fwd_paged does: once with its scale where no
+ * sequence exceeds 2048 (max_seq_len, n_max) or users have 8 new rows or fewer on
+ * average (to two bf16 terms if both hold), before and after the scale otherwise.
+ * fp32 calls keep 24 bits throughout.
  */
 size_t hstu_attn_paged_q4_workspace_size(const hstu_attn_params* p, int32_t num_splits);
 int32_t hstu_attn_paged_q4_default_splits(const hstu_attn_params* p, int32_t max_cached_len);

@@ -442,6 +442,15 @@ def test_long_histories(H, d, acts, cands):
     check_y(pb, p4, val)
 
 
+@pytest.mark.parametrize("cached,acts,cands", [([2500, 130], [20, 9], [6, 3]), ([1500, 2300], [70, 140], [64, 128])])
+def test_long_histories_with_many_rows(cached, acts, cands):
+    """The packed weights of calls with long sequences."""
+    pb, p4, val = batch(cached, acts, cands, 2, n_max=4096, seed=5, gamma=True)
+    check_raw(pb, p4, val, True)
+    check_raw(pb, p4, val, True, precise_silu=True)
+    check_y(pb, p4, val)
+
+
 @pytest.mark.parametrize("B,rows", [(150, 2), (513, 1), (600, 3), (530, 17)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_many_users(B, rows, dtype):
