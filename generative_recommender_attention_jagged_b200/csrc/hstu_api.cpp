@@ -155,8 +155,9 @@ Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
 
 // Rows of one pass of the small kernel over the cached bytes: 16 where users have
 // more than 8 on average (fp32 calls with d > 64: 8, their three-term operands fill
-// the registers; bf16 calls with d = 128 and that many rows are kQ4Tc's), and the CTAs that share a user's passes: room for twice the
-// average number of rows, since users differ (a CTA without rows ends at once).
+// the registers; bf16 calls with d = 128 and that many rows are kQ4Tc's), and the CTAs
+// that share a user's passes: room for twice the average number of rows, since users
+// differ (a CTA without rows ends at once).
 int q4_small_rows(const hstu_attn_params* p) {
   const bool wide = p->head_dim > (p->dtype == HSTU_DT_F32 ? 64 : 96);
   return (long long)p->total_tokens <= 8ll * p->batch || wide ? 8 : 16;
