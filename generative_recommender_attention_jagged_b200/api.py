@@ -412,12 +412,23 @@ def _ints(name: str, t, n: int):
         raise ValueError(f"{name} must be a contiguous int32 vector of {n}, got {t.dtype} {tuple(t.shape)}")
 
 
+def _row_stride(name: str, t, n: int) -> int:
+    """Elements between the rows (n elements each) of t.  A broadcast over the rows has stride 0, which the library
+    takes for packed rows: it would read or write past the tensor's end."""
+    if t.shape[0] <= 1:
+        return n
+    s = t.stride(0)
+    if s < n:
+        raise ValueError(f"{name}: rows of {n} elements may not overlap (row stride {s}; a broadcast must be copied)")
+    return s
+
+
 def _token_rows(name: str, t, H: int, d: int) -> int:
     """Token stride of a [T, H, d] view with packed heads."""
     s = t.stride()
     if (s[2] != 1 or s[1] != d) and t.numel():
         raise ValueError(f"{name}: heads and features must be packed (stride 1 / d)")
-    return s[0] if t.shape[0] > 1 else H * d
+    return _row_stride(name, t, H * d)
 
 
 def hstu_quant_i8_weight(w, *, w_q=None, w_scale=None, stream=None):
@@ -465,13 +476,14 @@ def hstu_linear_i8(x, w_q, w_scale, bias=None, *, silu: bool = False, out=None, 
     dt = out_dtype if out_dtype is not None else (out.dtype if out is not None else x.dtype)
     if dt not in _DT:
         raise ValueError(f"out must be bf16 or fp32, got {dt}")
+    if out is not None and (out.dtype != dt or tuple(out.shape) != (T, N) or (out.stride(1) != 1 and out.numel())):
+        raise ValueError(f"out must be a {dt} [{T}, {N}] matrix with contiguous rows, got {out.dtype} {tuple(out.shape)}")
+    x_stride, out_stride = _row_stride("x", x, K), N if out is None else _row_stride("out", out, N)
     raw = _stream_of(dev, stream)
     if out is None:
         out = _empty((T, N), dt, dev, stream)
-    elif out.dtype != dt or tuple(out.shape) != (T, N) or (out.stride(1) != 1 and out.numel()):
-        raise ValueError(f"out must be a {dt} [{T}, {N}] matrix with contiguous rows, got {out.dtype} {tuple(out.shape)}")
-    p = ctypes.byref(_lib.LinearI8Params(T, K, N, x.stride(0) if T > 1 else K, out.stride(0) if T > 1 else N,
-                                         _DT[x.dtype], _DT[dt], _lib.LIN_SILU if silu else 0))
+    p = ctypes.byref(_lib.LinearI8Params(T, K, N, x_stride, out_stride, _DT[x.dtype], _DT[dt],
+                                         _lib.LIN_SILU if silu else 0))
     lib = _lib.load()
     if workspace is None:
         workspace = _empty((int(lib.hstu_linear_i8_workspace_size(p)),), torch.uint8, dev, stream)
@@ -652,9 +664,10 @@ def hstu_attn_fwd_paged_q4(q, k, v, u, new_offsets, timestamps, ts_offsets, rab_
         raise ValueError("q, k and v must share one token stride")
     flags = ((_lib.F_OUTPUT_RAW_AV if raw_av else 0) | (_lib.F_FORCE_SIMT if force_simt else 0) |
              (_lib.F_PRECISE_SILU if precise_silu else 0))
+    us = _row_stride("u", u, D)
     raw = _stream_of(dev, stream)
     p = ctypes.byref(_lib.AttnParams(B, H, d, n_max, rab_ts.numel(), T, n_max if max_seq_len is None else max_seq_len,
-                                     qs, u.stride(0) if T > 1 else D, d ** -0.5 if alpha is None else alpha, ln_eps,
+                                     qs, us, d ** -0.5 if alpha is None else alpha, ln_eps,
                                      _DT[dt], flags))
     lib = _lib.load()
     if num_splits is None:
