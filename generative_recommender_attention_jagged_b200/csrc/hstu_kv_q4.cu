@@ -278,20 +278,22 @@ struct ReadArgs {
 };
 
 // Rows are independent: a user whose range or page is bad reports its error and
-// its rows stay as they were.
+// its rows stay as they were.  The first block also looks at the offsets, since a
+// user's rows past the output have no warp that would report them.
 template <typename T, int G, int W>
 __global__ void __launch_bounds__(kRowThreads) kv_read_q4_kernel(const ReadArgs a, const Q4Pool pool) {
   const int lane = threadIdx.x & 31, g = lane % G;
   const int words = a.d / 8;
   constexpr int kHeads = 32 / G;
+  if (blockIdx.x == 0)
+    for (int u = threadIdx.x; u < a.B; u += kRowThreads) {
+      const int r0 = a.offsets[u], r1 = a.offsets[u + 1];
+      if ((u == 0 && r0 != 0) || r1 < r0 || r1 > a.total) report_error(a.hdr, kErrLength, u);
+    }
   for (int row = blockIdx.x * kRowWarps + (threadIdx.x >> 5); row < a.total; row += gridDim.x * kRowWarps) {
     const int u = user_of(a.offsets, a.B, row);
     const int r0 = a.offsets[u], r1 = a.offsets[u + 1];
-    if (row < r0 || row >= r1) {
-      // before the first user, behind the last, or offsets that decrease
-      if (lane == 0 && (a.offsets[0] != 0 || r1 < r0)) report_error(a.hdr, kErrLength, u);
-      continue;
-    }
+    if (row < r0 || row >= r1) continue;  // before the first user, behind the last, or offsets that decrease
     const long long pos = (long long)a.starts[u] + (row - r0);
     const int page = (int)(pos / a.P);
     if (a.starts[u] < 0 || pos >= a.cached_lens[u] || page >= a.max_pages) {
@@ -478,7 +480,6 @@ int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_p
   if (workspace_bytes < sizeof(WsHeader)) return HSTU_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(WsHeader), s) != cudaSuccess) return HSTU_ERR_CUDA;
-  if (p->total_new == 0) return HSTU_OK;
   ReadArgs a;
   a.B = p->batch;
   a.H = p->num_heads;

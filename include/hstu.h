@@ -504,7 +504,9 @@ int hstu_kv_append_q4(const hstu_kv_params* p, const void* k_new, const void* v_
  * token starts[u] + i of user u, i < offsets[u+1] - offsets[u].  A range outside
  * 0 .. cached_lens[u]-1 or a bad page id is reported in the workspace's status
  * word (HSTU_ERR_LENGTH, HSTU_ERR_PAGE); the rows it names are left as they
- * were, and so are rows behind offsets[batch]. */
+ * were, and so are rows behind offsets[batch].  Offsets that do not begin at 0,
+ * decrease or go past total_new are HSTU_ERR_LENGTH too (rows of the output that
+ * they name may have been written). */
 int hstu_kv_read_q4(const hstu_kv_params* p, const void* k_pool, const void* v_pool, const void* k_scales,
                     const void* v_scales, const int32_t* page_table, const int32_t* cached_lens,
                     const int32_t* starts, const int32_t* offsets, void* k_out, void* v_out, void* workspace,
