@@ -7,8 +7,8 @@
 //
 // Two launches: the rows are quantised into the workspace (one warp a row, one
 // read of x), then the GEMM runs on the codes.  53,095 x 512 -> 2048 with bias and
-// SiLU, bf16: 20 + 70 us (the bf16 GEMM of gemm_sm100.cu: 98 us); 8 rows of it 9 us,
-// 1024 x 512 -> 512 12 us, both two launches' latencies.
+// SiLU, bf16: 20 + 80 us (without SiLU 20 + 59); 8 rows of it 9 us, 1024 x 512 -> 512
+// 12 us, both two launches' latencies.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -270,17 +270,27 @@ __device__ __forceinline__ void mma_i8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// SiLU for a bf16 result: h + h tanh h with h = x / 2 (error of tanh.approx
-// 2^-11, below the rounding to bf16); for an fp32 result x / (1 + exp(-x)).
+// SiLU for a bf16 result: x / (1 + exp(-x)) with the hardware's exponential and reciprocal,
+// relative error below 2^-21 + 2^-23 |x| (0 for x < -87), far below the rounding to bf16.
+// (h + h tanh h with h = x / 2 takes one such operation instead of two, but cancels for
+// negative x: 2^-11 of |h| is three quarters of SiLU(-8).)  For an fp32 result the exact forms.
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kMinusLog2e = -1.4426950408889634f;
+
 template <typename TOut>
 __device__ __forceinline__ float act_i8(float x, int silu) {
   if (!silu) return x;
-  if constexpr (sizeof(TOut) == 2) {
-    const float h = 0.5f * x;
-    return fmaf(h, tanh_approx(h), h);
-  } else {
-    return x / (1.f + expf(-x));
-  }
+  if constexpr (sizeof(TOut) == 2) return x * rcp_approx(1.f + ex2_approx(kMinusLog2e * x));
+  else return x / (1.f + expf(-x));
 }
 
 // One CTA per 128 x BN output tile.  Warp 0: TMA producer; warp 1: MMA issuer
@@ -395,12 +405,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // same time for twice the K.
 //
 // At K = 512 the epilogue has as much to do as the tensor core: 128 x 256 sums per
-// CTA and 2048 cycles of MMAs leave 8 cycles a warp row of 32.  The special-function
-// unit gives one of tanh and int-to-float conversion in that time, so the conversion
-// is done on the other pipes: the halves of the int32 go into the mantissa of 2^23
-// (exact), 65536 hi + lo is one rounded FMA, and the multiplications are packed in
-// pairs.  Sixteen epilogue warps (four to a scheduler, to cover their latencies) work
-// in four groups of 64 columns, each with a staging box and barriers of its own.
+// CTA and 2048 cycles of MMAs leave 8 cycles a warp row of 32, the time of one
+// operation of the special-function unit.  SiLU takes two (exponential and reciprocal),
+// so the int-to-float conversion, a third, is done on the other pipes: the halves of the
+// int32 go into the mantissa of 2^23 (exact), 65536 hi + lo is one rounded FMA, and the
+// multiplications are packed in pairs.  53,095 x 512 -> 2048 with both launches takes
+// 100 us; one reciprocal for two outputs (1 / d0 = d1 / (d0 d1)) 103, -log2(e) folded
+// into the scales 102, and SiLU by one tanh, which does not hold its precision below 0, 91.
+// Sixteen epilogue warps (four to a scheduler, to cover their latencies) work in four
+// groups of 64 columns, each with a staging box and barriers of its own.
 constexpr int kPairStages = 4;
 constexpr int kPairStage = kBM * kBK;   // 16 KB: this CTA's 128 rows of x, or 128 channels of w
 constexpr int kPairEpiWarps = 16;      // four groups of 64 columns, a warp per 32 rows
@@ -557,7 +570,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     constexpr bool kBf16 = sizeof(TOut) == 2;        // a box (128 bytes a row) holds 64 bf16 or 32 fp32 columns
-    constexpr float kFactor = kBf16 && SILU ? 0.5f : 1.f;  // half of x where SiLU wants x / 2
     const int quarter = warp & 3, grp = (warp - 2) >> 2;
     const int te = threadIdx.x - 64 - 128 * grp;     // thread of the group
     const bool issuer = te == 0;
@@ -574,13 +586,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int b = tc & 1;
       const int row0 = (u / tiles_n) * 2 * kBM + rank * kBM;
       const int n0 = (u % tiles_n) * kPairBN + 64 * grp;
-      const float xs = kFactor * (row0 + r < a.T ? a.x_scale[row0 + r] : 0.f);
+      const float xs = row0 + r < a.T ? a.x_scale[row0 + r] : 0.f;
       const uint64_t xs2 = pack_pair(xs, xs);
       // the scales and biases of the group's columns (the barrier of the last tile's box is behind its reads)
       if (te < 64) {
         const int n = n0 + te;
         ws[te] = n < a.N ? __ldg(a.w_scale + n) : 0.f;
-        bs[te] = n < a.N && a.bias ? kFactor * __ldg(a.bias + n) : 0.f;
+        bs[te] = n < a.N && a.bias ? __ldg(a.bias + n) : 0.f;
       }
       const bool ok = group_all(mbar_wait(&sm.acc_full[b], (tc >> 1) & 1, abort_flag, a.hdr, 34), grp);
       if (!ok) break;
@@ -614,7 +626,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
               const uint32_t i0 = acc[x][e + k + q], i1 = acc[x][e + k + q + 1];
-              // without tanh the special-function unit is free for the conversion
+              // without SiLU the special-function unit is free for the conversion
               const uint64_t f2 =
                   SILU ? ints_to_float2(i0, i1) : pack_pair(__int2float_rn((int)i0), __int2float_rn((int)i1));
               const uint64_t v2 = fma_pair(f2, mul_pair(xs2, q ? pack_pair(wv.z, wv.w) : pack_pair(wv.x, wv.y)),
@@ -622,7 +634,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               float v0, v1;
               unpack_pair(v2, v0, v1);
               if constexpr (SILU && kBf16) {
-                unpack_pair(fma_pair(v2, pack_pair(tanh_approx(v0), tanh_approx(v1)), v2), y[k + q], y[k + q + 1]);
+                float n0, n1, d0, d1;
+                unpack_pair(mul_pair(v2, pack_pair(kMinusLog2e, kMinusLog2e)), n0, n1);
+                unpack_pair(add_pair(pack_pair(ex2_approx(n0), ex2_approx(n1)), pack_pair(1.f, 1.f)), d0, d1);
+                unpack_pair(mul_pair(v2, pack_pair(rcp_approx(d0), rcp_approx(d1))), y[k + q], y[k + q + 1]);
               } else {
                 y[k + q] = SILU ? act_i8<TOut>(v0, 1) : v0;
                 y[k + q + 1] = SILU ? act_i8<TOut>(v1, 1) : v1;
