@@ -229,12 +229,18 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, int* abor
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, int* abort, WsHeader* hdr, int where) {
   return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, hdr, where);
 }
-// A warp waits for a phase: one lane polls (32 lanes of 16 waiting warps polling keep the
-// shared-memory pipe from the warps that work), the others follow.
+// One lane polls for a warp (32 lanes of 16 waiting warps polling keep the shared-memory pipe from
+// the warps that work).  The vote hands its answer to the others; what the barrier published is
+// seen by them through the warp barrier behind it.
+__device__ __forceinline__ bool warp_agree(bool ok) {
+  ok = __all_sync(~0u, ok);
+  __syncwarp();
+  return ok;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, WsHeader* hdr, int where) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = lane_wait(bar, parity, abort, hdr, where);
-  return __shfl_sync(~0u, ok, 0);
+  return warp_agree(ok);
 }
 // A warp arrives once, when all its lanes are there.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tl = t + 2 + odd;
           if ((lane & 15) == 0 && tl < cnt && tl >= kKeyStages)
             ok = lane_wait(&sm.bar_key_empty[tl % kKeyStages], ((tl / kKeyStages) & 1) ^ 1, abort_flag, a.hdr, 51);
-          ok = __all_sync(~0u, ok);
+          ok = warp_agree(ok);
           if (!ok) break;
           announce(t + 2);
         }
@@ -583,10 +589,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = t & 1;
       int k0, width;
       key_tile(g, tb + t, k0, width);
-      ok = warp_wait(&sm.bar_win_full[t % kWinStages], (t / kWinStages) & 1, abort_flag, a.hdr, 56);
-      ok = ok && warp_wait(&sm.bar_s_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
-      // a tile of new tokens: the NaN scales of its value rows are set
-      if (k0 >= g.L) ok = ok && warp_wait(&sm.bar_v_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
+      if (lane == 0) {
+        ok = lane_wait(&sm.bar_win_full[t % kWinStages], (t / kWinStages) & 1, abort_flag, a.hdr, 56) &&
+             lane_wait(&sm.bar_s_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
+        // a tile of new tokens: the NaN scales of its value rows are set
+        if (k0 >= g.L) ok = ok && lane_wait(&sm.bar_v_full[b], (t >> 1) & 1, abort_flag, a.hdr, 56);
+      }
+      ok = warp_agree(ok);
       if (!ok) break;
       tc_fence_after();
       const KeyInfo& key = sm.key[t % kKeyStages];
