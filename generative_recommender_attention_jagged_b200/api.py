@@ -34,6 +34,17 @@ def _need_cuda(name: str, t: Optional[torch.Tensor], dtype=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _row_stride(name: str, t, n: int) -> int:
+    """Elements between the rows (n elements each) of t.  A broadcast over the rows has stride 0, which the library
+    takes for packed rows: it would read or write past the tensor's end."""
+    if t.shape[0] <= 1:
+        return n
+    s = t.stride(0)
+    if s < n:
+        raise ValueError(f"{name}: rows of {n} elements may not overlap (row stride {s}; a broadcast must be copied)")
+    return s
+
+
 def _rows_view(name: str, t: torch.Tensor, H: int, d: int) -> int:
     """Token stride (elements) of a [T,H,d] (or [T,H*d]) view with packed heads."""
     if t.numel() == 0:
@@ -44,7 +55,7 @@ def _rows_view(name: str, t: torch.Tensor, H: int, d: int) -> int:
         ok = t.stride(1) == 1
     if not ok:
         raise ValueError(f"{name}: heads and features must be packed (stride 1 / d)")
-    return t.stride(0) if t.shape[0] > 1 else H * d
+    return _row_stride(name, t, H * d)
 
 
 def attn_params(*, batch: int, num_heads: int, head_dim: int, n_max: int, total_tokens: int,
@@ -194,6 +205,8 @@ def hstu_attn_fwd_static_ws(q, k, v, u, seq_offsets, timestamps, rab_pos, rab_ts
     for name, t in (("q", q), ("k", k), ("v", v), ("u", u)):
         _need_cuda(name, t, dt)
     qs = _rows_view("q", q, H, d)
+    if _rows_view("k", k, H, d) != qs or _rows_view("v", v, H, d) != qs:
+        raise ValueError("q, k and v must share one token stride")
     us = _rows_view("u", u, H, d)
     params = attn_params(batch=seq_offsets.numel() - 1, num_heads=H, head_dim=d, n_max=n_max,
                          total_tokens=T, max_seq_len=n_max if max_seq_len is None else max_seq_len,
@@ -211,8 +224,8 @@ def hstu_attn_fwd_static_ws(q, k, v, u, seq_offsets, timestamps, rab_pos, rab_ts
 def linear_params(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, silu: bool,
                   force_cublas: bool = False) -> _lib.LinearParams:
     return _lib.LinearParams(rows=x.shape[0], d_in=x.shape[1], d_out=w.shape[1],
-                             x_stride=x.stride(0) if x.shape[0] > 1 else x.shape[1],
-                             out_stride=out.stride(0) if out.shape[0] > 1 else out.shape[1],
+                             x_stride=_row_stride("x", x, x.shape[1]),
+                             out_stride=_row_stride("out", out, out.shape[1]),
                              dtype=_DT[x.dtype],
                              flags=(_lib.LIN_SILU if silu else 0) | (_lib.LIN_CUBLAS if force_cublas else 0))
 
@@ -270,7 +283,7 @@ def split_uvqk(uvqk: torch.Tensor, num_heads: int, head_dim: int):
 
 def kv_params(k_pool: torch.Tensor, page_table: torch.Tensor, k_new: Optional[torch.Tensor] = None) -> _lib.KvParams:
     num_pages, H, P, d = k_pool.shape
-    stride = 0 if k_new is None or k_new.shape[0] <= 1 else k_new.stride(0)
+    stride = 0 if k_new is None or k_new.shape[0] <= 1 else _row_stride("k_new", k_new, H * d)
     return _lib.KvParams(batch=page_table.shape[0], num_heads=H, head_dim=d, page_size=P, num_pages=num_pages,
                          max_pages_per_user=page_table.shape[1], kv_stride=stride,
                          total_new=0 if k_new is None else k_new.shape[0], dtype=_DT[k_pool.dtype])
@@ -410,17 +423,6 @@ def _need(name: str, t, dtype, shape):
 def _ints(name: str, t, n: int):
     if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 vector of {n}, got {t.dtype} {tuple(t.shape)}")
-
-
-def _row_stride(name: str, t, n: int) -> int:
-    """Elements between the rows (n elements each) of t.  A broadcast over the rows has stride 0, which the library
-    takes for packed rows: it would read or write past the tensor's end."""
-    if t.shape[0] <= 1:
-        return n
-    s = t.stride(0)
-    if s < n:
-        raise ValueError(f"{name}: rows of {n} elements may not overlap (row stride {s}; a broadcast must be copied)")
-    return s
 
 
 def _token_rows(name: str, t, H: int, d: int) -> int:
