@@ -205,8 +205,8 @@ __device__ __forceinline__ int chunk_mode(Walk& w, const long long* ts, int col0
   if (!__all_sync(~0u, uni)) {
     const long long tlim2 = w.b > 0 ? w.t_i + 1 - thr[w.b - 1] : LLONG_MIN;
     const bool one = uni || t_last <= tlim2;              // at most one edge in the chunk
-    // octave mode needs |dt| + 1 < 2^32 at the chunk's first allowed column
-    const bool narrow = uni || (w.t_i + 1 - ts[col0]) < (1ll << 32);
+    // octave mode, which every lane then takes, needs |dt| + 1 < 2^32 at the chunk's first allowed column
+    const bool narrow = none || (w.t_i + 1 - ts[col0]) < (1ll << 32);
     if (__all_sync(~0u, one)) {
       mode = kBiasEdge;
       if (!uni) {
