@@ -124,7 +124,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, in
     s_tso = tso;
     s_pages = pages;
   }
-  __syncthreads();
+  // A paged user's timestamps lie where the users before it put them, so theirs are read only if all of those
+  // hold too (4-bit calls: plan_q4_kernel).  The last threads take the first users: thread 0 has its own.
+  int before = 1;
+  if (a.paged && !a.k_scales)
+    for (int v = blockDim.x - 1 - threadIdx.x; v < u; v += blockDim.x) {
+      int n, tso, pages;
+      before &= check_user(a, v, n, tso, pages);
+    }
+  before = __syncthreads_and(before);
   if (s_ok) {
     // this block's share of the user's page ids and timestamps
     const int stride = blockDim.x * parts;
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, in
       }
     }
     const int64_t* ts = a.ts + s_tso;
-    for (int j = part * blockDim.x + threadIdx.x; j < s_n; j += stride) {
+    for (int j = part * blockDim.x + threadIdx.x; before && j < s_n; j += stride) {
       const long long t = ts[j];
       if (t > kTsLimit || t < -kTsLimit || (j > 0 && t < ts[j - 1])) report_error(a.hdr, kErrUnsorted, u);
     }
