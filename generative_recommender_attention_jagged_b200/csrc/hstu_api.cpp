@@ -317,8 +317,8 @@ int run(const hstu_attn_params* p, const Common& c) {
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (stages & HSTU_F_STAGE_PLAN) {
-    e = q4 ? launch_plan_q4(a, nullptr, 0, nullptr, nullptr, 0, c.stream)
-           : cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream);
+    e = plan_checks_users_first(a) ? launch_plan_q4(a, nullptr, 0, nullptr, nullptr, 0, c.stream)
+                                   : cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream);
     if (e != cudaSuccess) return HSTU_ERR_CUDA;
     if ((e = launch_plan(a, tc, p->max_seq_len, c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;
   }

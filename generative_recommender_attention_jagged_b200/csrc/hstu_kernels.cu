@@ -109,7 +109,8 @@ __device__ void build_schedule(const AttnArgs& a, int* hist, int* start) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, int parts, int schedule) {
-  if (a.k_scales && a.hdr->pad[0] != 1) return;  // 4-bit calls: plan_q4_kernel has checked the users
+  const bool checked = plan_checks_users_first(a);
+  if (checked && a.hdr->pad[0] != 1) return;
   const int u = blockIdx.x / parts;
   const int part = blockIdx.x % parts;
   __shared__ int s_ok, s_n, s_tso, s_pages, s_last;
@@ -124,10 +125,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, in
     s_tso = tso;
     s_pages = pages;
   }
-  // A paged user's timestamps lie where the users before it put them, so theirs are read only if all of those
-  // hold too (4-bit calls: plan_q4_kernel).  The last threads take the first users: thread 0 has its own.
+  // A paged user's timestamps lie where the users before it put them, so they are read only if all of those
+  // hold too.  The last threads take the first users: thread 0 has its own.
   int before = 1;
-  if (a.paged && !a.k_scales)
+  if (a.paged && !checked)
     for (int v = blockDim.x - 1 - threadIdx.x; v < u; v += blockDim.x) {
       int n, tso, pages;
       before &= check_user(a, v, n, tso, pages);

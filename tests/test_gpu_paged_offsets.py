@@ -19,7 +19,7 @@ LENGTH = -4
 @pytest.mark.parametrize("force_simt", [False, True])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows", [1, 20, 200])
-@pytest.mark.parametrize("B", [2, 300])        # 300: more users than a block has threads
+@pytest.mark.parametrize("B", [2, 300, 1100])  # more users than a block has threads, than a block checks
 def test_offsets_past_the_timestamps_are_not_followed(B, rows, dtype, force_simt):
     acts = [rows, rows] + [0] * (B - 2)
     pb = synth.paged_batch([100, 60] + [5] * (B - 2), acts, [0] * B, 2, 128, 512, rng=np.random.default_rng(rows),
