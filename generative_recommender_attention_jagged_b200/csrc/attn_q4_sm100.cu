@@ -13,9 +13,9 @@
 //
 // With 128 rows against a key tile the step is bound by instruction issue and by the
 // latencies of its chain (S, SiLU, P), not by the cache's bytes (16 KB a tile).  16 users
-// of 2048 to 4096 keys with 512 candidates, 4 heads: 147 us, 360 TFLOP/s, 59% of the issue
-// slots used (75% while a block is in its loop); 8 users of 6144 to 8192 keys with 128
-// rows: 60 us.
+// of 2048 to 4096 keys with 512 candidates, 4 heads: 156 us with the plan and the epilogue,
+// 340 TFLOP/s, 59% of the issue slots used (75% while a block is in its loop); 8 users of
+// 6144 to 8192 keys with 128 rows: 66 us.
 //
 //   - eight elementwise warps (two 32-key chunks of each tile each) turn S(t) into P(t).
 //     S is double-buffered in tensor memory, so the tensor core does O += P(t - 1) V(t - 1)
@@ -34,7 +34,10 @@
 // with long sequences; in fp32 with one rounding at the end where no sequence exceeds
 // kShortSequence, and on request (HSTU_F_PRECISE_SILU): relative error of y 2.0e-3 against
 // 1.8e-3 at 4000 keys, 2.5e-3 against 1.8e-3 at 1500 and 3.4e-3 against 2.2e-3 at 200, for
-// 1-3% of the time in short calls and 5-6% in long ones.
+// 1-3% of the time in short calls and 5-6% in long ones.  In both, the position bias is in
+// bf16 (as in attn_sm100_single.cu), and where a row's 32 keys lie in more than one time
+// bucket the time bias and the sum of the two are (one packed addition instead of a copy of
+// the weights' code for each mode); in one bucket the time bias is added in fp32.
 //
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
 // row that is not finite is stored as zeros and its scale set to NaN: the mask is

@@ -33,9 +33,11 @@
 //     the rows there are cost anything (a request with one new action has one of
 //     eight); the weights come back by a transposing ldmatrix.
 //   - For K the 128 + kz of each element is taken off after the product, as
-//     (128 + kz) sum_e q_ie in fp32 (8 sums of 16 products: the error stays
-//     near 2^-20 of s, against 2^-9 of the rounding of the weights); for V
-//     before it (the sum runs over thousands of keys), one packed subtraction.
+//     (128 + kz) sum_e q_ie in fp32.  What cancels is of the size of 128 sum_e |q_ie|,
+//     whatever s is, so the error of s is absolute: up to 2^-11 alpha ks_j sum_e |q_ie|
+//     (D / 16 sums of 16 products, each to 2^-22 of them).  fp32 calls, which need
+//     more, subtract first.  For V it is taken off before the product (the sum runs
+//     over thousands of keys), one packed subtraction.
 //   - Weights: SiLU in fp32, sums in fp32.  a_ij vs_j goes into the second product
 //     as one bf16 term in calls with long histories, where its roundings average out
 //     (relative error of y 1.8e-3, of which 1.7e-3 is its own rounding), and as two

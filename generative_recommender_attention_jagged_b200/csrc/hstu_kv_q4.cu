@@ -2,11 +2,12 @@
 //
 // The pool has the paged layout of hstu_kv.cu with a row of d / 2 bytes for
 // each token and head and one (scale, zero) word beside it; the row format is
-// in quant_common.cuh.  Both kernels move each row once.  The bytes of k_new and
-// v_new (of the dense output) would take 16 us (16) for 24576 tokens of 4 heads of
-// 128 bf16 elements; the append takes 31 us, bound by instruction issue and the
-// latencies of a token's steps (21 instructions an element for the exact codes, the
-// row's extremes and its format), the read-back 16 us.
+// in quant_common.cuh.  Both kernels move each row once.  24576 tokens of 4 heads of
+// 128 bf16 elements and their rows in the pool are 64 MB, 9.8 us at the copy's
+// bandwidth.  The append takes 31 us: 21 instructions an element for the exact codes,
+// the row's extremes and its format fill 60% of the issue slots, and a token's steps
+// wait for one another.  The read-back takes 17 us: 56% of the issue slots, the rest
+// mostly waits for the chain offsets - page table - row (34 warps an SM).
 //
 // A warp takes a token: G lanes hold a row (8 W elements each), so 32 / G heads
 // go at once, K and V of two such groups of heads together (four independent

@@ -874,10 +874,10 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   a.out = out;
   a.hdr = hdr;
   // 128 x 128 tiles on single SMs while one wave of them does; 256 x 256 tiles on SM
-  // pairs, persistent, above.  Single against pairs in us (with the quantisation of x):
-  // rows x d_in x d_out 700 x 208 x 40 7.3 / 9.8, 8 x 512 x 2048 9.2 / 10.0, 1024 x 512 x
-  // 2048 (128 tiles) 12.2 / 11.8, 2048 x 512 x 2048 (256) 20.5 / 12.1, 16384 x 512 x 512
-  // (512) 40 / 20.
+  // pairs, persistent, above.  Single against pairs in us (with the quantisation of x; bf16,
+  // with SiLU): rows x d_in x d_out 700 x 208 x 40 7.7 / 10.7, 8 x 512 x 2048 10.8 / 11.3,
+  // 1024 x 512 x 2048 (128 tiles) 13.8 / 13.3, 2048 x 512 x 2048 (256) 23.2 / 13.8,
+  // 16384 x 512 x 512 (512) 44 / 21.
   const long long single_tiles = ((p->rows + kBM - 1) / kBM) * ((p->d_out + 127) / 128);
   cudaError_t e;
   if (single_tiles > sms)
