@@ -49,13 +49,13 @@
 //     tile's O^T is summed from zero and added to the running sum in fp32, since
 //     the tensor core's own sums are not rounded to nearest.
 //
-// Calls with more rows than a tile (fp32, or a head size that the tcgen05 kernel
-// does not take) run a CTA per group of row tiles.
+// Users with more rows than a pass takes (fp32, or a head size that the tcgen05 kernel
+// does not take, or one such user among others) have a CTA for each 8 or 16 of them.
 //
 // The new rows' own keys are a few: each warp takes rows and does the allowed
 // pairs in fp32 FMAs, so that what a mask hides is never touched.  The CTA that
-// finishes a group of rows last (a counter in the workspace) adds the parts in order,
-// normalises and gates: one launch behind the plan (plan_q4_kernel).
+// finishes a tile of rows last (a counter in the workspace) adds the parts in order,
+// normalises and gates: one launch behind the plan (plan_q4_kernel), which lists the tiles.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -187,8 +187,7 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
 // (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
 template <typename T, int D, int NQ, int WT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
-    attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int32_t* order,
-                         int row_groups) {
+    attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int2* row_tiles) {
   constexpr bool kF32 = sizeof(T) == 4;
   constexpr int kTerms = kF32 ? 3 : 1;   // bf16 terms of a row element
   constexpr int kWTerms = kF32 ? 3 : WT; // and of a weight
@@ -197,13 +196,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   constexpr int kTilesM = D / 16;  // 16-dimension tiles of O^T
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SmallSmem<T, D, NQ>& sm = *reinterpret_cast<SmallSmem<T, D, NQ>*>(smem_raw);
-  const int split = blockIdx.x % a.num_splits, rg = blockIdx.x / a.num_splits, head = blockIdx.y;
+  const int split = blockIdx.x % a.num_splits, head = (int)(blockIdx.x / a.num_splits) % a.H;
+  const int tile = (int)(blockIdx.x / a.num_splits) / a.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
   grid_dependency_wait();
-  const int valid = a.hdr->pad[0], u = order[blockIdx.z];
-  if (valid != 1) return;  // a user's lengths do not hold
+  const int valid = a.hdr->pad[0];
+  const int2 item = row_tiles[tile];
+  const int u = item.x, r0 = 8 * NQ * item.y;
+  if (valid != 1 || u < 0) return;  // a user's lengths do not hold, or no tile
   const int q0 = a.q_offsets[u], rows = a.q_offsets[u + 1] - q0;
   const int L = a.cached_lens[u], n = L + rows;
   const int part = part_keys(L, a.num_splits);
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
       if (t > kTsLimit || t < -kTsLimit || (j > 0 && t < ts[j - 1])) report_error(a.hdr, kErrUnsorted, u);
     }
   };
-  const bool checks = head == 0 && rg == 0;
+  const bool checks = head == 0 && r0 == 0;
   if (rows == 0) {
     if (checks) check_keys();
     return;
@@ -250,359 +252,357 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   const int tiles = (k_hi - k_lo + kKeys - 1) / kKeys;
   const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;  // tiles warp, warp + 4, ...
 
-  for (int r0 = 8 * NQ * rg; r0 < rows; r0 += 8 * NQ * row_groups) {
-    const int nr = min(8 * NQ, rows - r0);
-    // ---- the rows: fragments of Q^T, their sums, times and positions
-    uint32_t qf[NQ][kSteps][2][kTerms];
+  const int nr = min(8 * NQ, rows - r0);
+  // ---- the rows: fragments of Q^T, their sums, times and positions
+  uint32_t qf[NQ][kSteps][2][kTerms];
 #pragma unroll
-    for (int w = 0; w < NQ; ++w) {
-      const int r = 8 * w + g;
-      const T* qr = q + (size_t)(q0 + r0 + min(r, nr - 1)) * a.qkv_stride + head * D + (D / 4) * t;
-      float s = 0.f;
+  for (int w = 0; w < NQ; ++w) {
+    const int r = 8 * w + g;
+    const T* qr = q + (size_t)(q0 + r0 + min(r, nr - 1)) * a.qkv_stride + head * D + (D / 4) * t;
+    float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        float x[4];
-        if constexpr (kF32) {
-          const float4 f = *reinterpret_cast<const float4*>(qr + 4 * k);
-          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-        } else {
-          const uint2 f = *reinterpret_cast<const uint2*>(qr + 4 * k);
-          x[0] = __uint_as_float(f.x << 16), x[1] = __uint_as_float(f.x & 0xFFFF0000u);
-          x[2] = __uint_as_float(f.y << 16), x[3] = __uint_as_float(f.y & 0xFFFF0000u);
-        }
-        s += (x[0] + x[1]) + (x[2] + x[3]);
-        if constexpr (kF32) {
-          float y[4][3];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split_bf16(x[e], y[e]);
-#pragma unroll
-          for (int p = 0; p < kTerms; ++p) {
-            qf[w][k][0][p] = pack_bf16x2(y[0][p], y[1][p]);
-            qf[w][k][1][p] = pack_bf16x2(y[2][p], y[3][p]);
-          }
-        } else {
-          qf[w][k][0][0] = pack_bf16x2(x[0], x[1]);
-          qf[w][k][1][0] = pack_bf16x2(x[2], x[3]);
-        }
+    for (int k = 0; k < kSteps; ++k) {
+      float x[4];
+      if constexpr (kF32) {
+        const float4 f = *reinterpret_cast<const float4*>(qr + 4 * k);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+      } else {
+        const uint2 f = *reinterpret_cast<const uint2*>(qr + 4 * k);
+        x[0] = __uint_as_float(f.x << 16), x[1] = __uint_as_float(f.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(f.y << 16), x[3] = __uint_as_float(f.y & 0xFFFF0000u);
       }
-      s += __shfl_xor_sync(~0u, s, 1);
-      s += __shfl_xor_sync(~0u, s, 2);
-      if (warp == 0 && t == 0) {  // what the weights need of row r
-        const int i = L + r0 + min(r, nr - 1);
-        sm.qsum[r] = s;
-        sm.t_i[r] = ts[i];
-        sm.rp[r] = min(i, hist) + a.n_max - 1;
+      s += (x[0] + x[1]) + (x[2] + x[3]);
+      if constexpr (kF32) {
+        float y[4][3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16(x[e], y[e]);
+#pragma unroll
+        for (int p = 0; p < kTerms; ++p) {
+          qf[w][k][0][p] = pack_bf16x2(y[0][p], y[1][p]);
+          qf[w][k][1][p] = pack_bf16x2(y[2][p], y[3][p]);
+        }
+      } else {
+        qf[w][k][0][0] = pack_bf16x2(x[0], x[1]);
+        qf[w][k][1][0] = pack_bf16x2(x[2], x[3]);
       }
     }
-    __syncthreads();
-    float o[NQ][kTilesM][4];
+    s += __shfl_xor_sync(~0u, s, 1);
+    s += __shfl_xor_sync(~0u, s, 2);
+    if (warp == 0 && t == 0) {  // what the weights need of row r
+      const int i = L + r0 + min(r, nr - 1);
+      sm.qsum[r] = s;
+      sm.t_i[r] = ts[i];
+      sm.rp[r] = min(i, hist) + a.n_max - 1;
+    }
+  }
+  __syncthreads();
+  float o[NQ][kTilesM][4];
 #pragma unroll
-    for (int w = 0; w < NQ; ++w)
+  for (int w = 0; w < NQ; ++w)
 #pragma unroll
-      for (int m = 0; m < kTilesM; ++m)
+    for (int m = 0; m < kTilesM; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[w][m][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[w][m][e] = 0.f;
 
-    // page id of this lane's key of the warp's m-th tile (loaded one tile ahead of its copy)
-    auto page_of = [&](int m) -> int {
+  // page id of this lane's key of the warp's m-th tile (loaded one tile ahead of its copy)
+  auto page_of = [&](int m) -> int {
+    const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
+    return m < mine && j < k_hi ? table[page_index(a, j)] : 0;
+  };
+  auto fetch = [&](int m, int pid) {
+    if (m < mine) {
       const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
-      return m < mine && j < k_hi ? table[page_index(a, j)] : 0;
-    };
-    auto fetch = [&](int m, int pid) {
-      if (m < mine) {
-        const int j = k_lo + (warp + m * kWarps) * kKeys + lane;
-        // past the part's end and for a page id out of range (reported by check_keys) the codes are those of
-        // the pool's first row, under scales and zero points of 0
-        const bool on = j < k_hi && (unsigned)pid < (unsigned)a.num_pages;
-        Stage<D>& st = ring[m % kRing];
-        // (the pool has fewer than 2^32 rows: attn_q4_small_supported)
-        const uint32_t slot =
-            on ? ((uint32_t)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : 0;
-        constexpr int kPieces = D / 32;  // 16-byte pieces of a row
-        const uint32_t k_to = smem_u32(st.k), v_to = smem_u32(st.v);
+      // past the part's end and for a page id out of range (reported by check_keys) the codes are those of
+      // the pool's first row, under scales and zero points of 0
+      const bool on = j < k_hi && (unsigned)pid < (unsigned)a.num_pages;
+      Stage<D>& st = ring[m % kRing];
+      // (the pool has fewer than 2^32 rows: attn_q4_small_supported)
+      const uint32_t slot =
+          on ? ((uint32_t)pid * a.H + head) * a.page_size + (j - page_index(a, j) * a.page_size) : 0;
+      constexpr int kPieces = D / 32;  // 16-byte pieces of a row
+      const uint32_t k_to = smem_u32(st.k), v_to = smem_u32(st.v);
 #pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-          const int c = 32 * x + lane, row = c / kPieces, piece = c % kPieces;
-          const uint32_t s = __shfl_sync(~0u, slot, row);
-          cp16(k_to + row * (D / 2) + piece * 16, kp + piece * 16 + (size_t)s * (D / 2));
-          cp16(v_to + row * Stage<D>::kVRow + piece * 16, vp + piece * 16 + (size_t)s * (D / 2));
-        }
-        cp4(&st.km[lane], a.k_scales + slot, on);
-        cp4(&st.vm[lane], a.v_scales + slot, on);
-        cp8(&st.ts[lane], ts + min(j, n - 1));
+      for (int x = 0; x < kPieces; ++x) {
+        const int c = 32 * x + lane, row = c / kPieces, piece = c % kPieces;
+        const uint32_t s = __shfl_sync(~0u, slot, row);
+        cp16(k_to + row * (D / 2) + piece * 16, kp + piece * 16 + (size_t)s * (D / 2));
+        cp16(v_to + row * Stage<D>::kVRow + piece * 16, vp + piece * 16 + (size_t)s * (D / 2));
       }
-      cp_commit();
-    };
+      cp4(&st.km[lane], a.k_scales + slot, on);
+      cp4(&st.vm[lane], a.v_scales + slot, on);
+      cp8(&st.ts[lane], ts + min(j, n - 1));
+    }
+    cp_commit();
+  };
 
-    int pid = page_of(0);
+  int pid = page_of(0);
 #pragma unroll
-    for (int m = 0; m < kRing - 1; ++m) {
-      const int next = page_of(m + 1);
-      fetch(m, pid);
+  for (int m = 0; m < kRing - 1; ++m) {
+    const int next = page_of(m + 1);
+    fetch(m, pid);
+    pid = next;
+  }
+  for (int m = 0; m < mine; ++m) {
+    {
+      const int next = page_of(m + kRing);
+      fetch(m + kRing - 1, pid);
       pid = next;
     }
-    for (int m = 0; m < mine; ++m) {
-      {
-        const int next = page_of(m + kRing);
-        fetch(m + kRing - 1, pid);
-        pid = next;
-      }
-      cp_wait<kRing - 1>();
-      __syncwarp();
-      const Stage<D>& st = ring[m % kRing];
-      const int j0 = k_lo + (warp + m * kWarps) * kKeys;
-      uint8_t(&xs)[kKeys][kXRow<T, NQ>] = sm.xs[warp];
-      // ---- S^T = (128 + codes) Q^T (fp32: (codes - kz) Q^T), 16 keys at a time
+    cp_wait<kRing - 1>();
+    __syncwarp();
+    const Stage<D>& st = ring[m % kRing];
+    const int j0 = k_lo + (warp + m * kWarps) * kKeys;
+    uint8_t(&xs)[kKeys][kXRow<T, NQ>] = sm.xs[warp];
+    // ---- S^T = (128 + codes) Q^T (fp32: (codes - kz) Q^T), 16 keys at a time
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float s[NQ][4];
+    for (int half = 0; half < 2; ++half) {
+      float s[NQ][4];
+#pragma unroll
+      for (int w = 0; w < NQ; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[w][e] = 0.f;
+      uint32_t ka[kWords], kb[kWords];
+      const uint8_t* krow = st.k + (16 * half + g) * (D / 2) + t * (D / 8);
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(krow);
+        *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(krow + 8 * (D / 2));
+      } else {
+#pragma unroll
+        for (int c = 0; c < kWords; ++c) {
+          ka[c] = reinterpret_cast<const uint32_t*>(krow)[c];
+          kb[c] = reinterpret_cast<const uint32_t*>(krow + 8 * (D / 2))[c];
+        }
+      }
+      uint32_t za = 0, zb = 0;
+      if constexpr (kF32) {
+        const uint32_t ma = st.km[16 * half + g], mb = st.km[16 * half + g + 8];
+        za = add_bf16x2_(__byte_perm(ma, ma, 0x3232), 0x43004300u);
+        zb = add_bf16x2_(__byte_perm(mb, mb, 0x3232), 0x43004300u);
+      }
+#pragma unroll
+      for (int p = kTerms - 1; p >= 0; --p)
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const int i = 2 * (k & 1);
+          uint32_t a0 = widen(ka[k >> 1], i), a1 = widen(kb[k >> 1], i), a2 = widen(ka[k >> 1], i + 1),
+                   a3 = widen(kb[k >> 1], i + 1);
+          if constexpr (kF32) {
+            a0 = sub_bf16x2(a0, za), a1 = sub_bf16x2(a1, zb), a2 = sub_bf16x2(a2, za), a3 = sub_bf16x2(a3, zb);
+          }
+#pragma unroll
+          for (int w = 0; w < NQ; ++w) mma16816(s[w], a0, a1, a2, a3, qf[w][k][0][p], qf[w][k][1][p]);
+        }
+#pragma unroll
+      for (int w = 0; w < NQ; ++w)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          *reinterpret_cast<float2*>(xs[16 * half + 8 * x + g] + 4 * (8 * w + 2 * t)) =
+              make_float2(s[w][2 * x], s[w][2 * x + 1]);
+    }
+    __syncwarp();
+    // ---- weights: lane = key, only the rows there are
+    uint32_t p[kWTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
+    {
+      const int j = j0 + lane;
+      const uint32_t km = st.km[lane], vm = st.vm[lane];
+      const float ks = a.alpha * meta_scale(km), kz = kF32 ? 0.f : -(128.f + meta_zero(km));
+      const float vs = meta_scale(vm);
+      const long long tj = st.ts[lane];
+      const float* bias_of = a.rab_pos - min(j, L);
+      const float* sc_of = reinterpret_cast<const float*>(xs[lane]);
+      float pos_bias[8 * NQ];  // all rows' loads on the way before the first is used
+#pragma unroll
+      for (int r = 0; r < 8 * NQ; ++r) {
+        if (r >= nr) break;
+        pos_bias[r] = __ldg(bias_of + sm.rp[r]);
+      }
+      uint32_t pk[kWTerms][4 * NQ];
+#pragma unroll
+      for (int r = 0; r < 8 * NQ; r += 2) {
+        float wt[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (r + e < nr) {
+            const float bias = pos_bias[r + e] + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
+            const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
+            wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
+          }
+        if constexpr (kWTerms > 1) {
+          float y[2][kWTerms];
+          split_bf16(wt[0], y[0]);
+          split_bf16(wt[1], y[1]);
+#pragma unroll
+          for (int x = 0; x < kWTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
+        } else {
+          pk[0][r / 2] = pack_bf16x2(wt[0], wt[1]);
+        }
+      }
+      // the lane's weights over its own scores, then transposed by ldmatrix
+#pragma unroll
+      for (int x = 0; x < kWTerms; ++x)
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
+          *reinterpret_cast<uint4*>(xs[lane] + 16 * (NQ * x + w)) =
+              make_uint4(pk[x][4 * w], pk[x][4 * w + 1], pk[x][4 * w + 2], pk[x][4 * w + 3]);
+      __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[w][e] = 0.f;
-        uint32_t ka[kWords], kb[kWords];
-        const uint8_t* krow = st.k + (16 * half + g) * (D / 2) + t * (D / 8);
-        if constexpr (D == 128) {
-          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(krow);
-          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(krow + 8 * (D / 2));
+      for (int x = 0; x < kWTerms; ++x)
+#pragma unroll
+        for (int w = 0; w < NQ; ++w)
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(p[x][w][0]), "=r"(p[x][w][1]), "=r"(p[x][w][2]), "=r"(p[x][w][3])
+                       : "r"(smem_u32(xs[lane] + 16 * (NQ * x + w)))
+                       : "memory");
+    }
+    // ---- O^T += (codes' - vz) P^T
+    // 16-bit pieces (4 codes) of a V row a thread reads: its eighth of the dimensions
+    constexpr int kHalves = D / 32;
+    // [16 keys][lo, hi]: keys 2 t, 2 t + 1 (lo) or 2 t + 8, 2 t + 9 (hi) side by side
+    uint32_t vh[2][2][kHalves];
+    uint32_t vz[2][2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int key = 16 * half + 8 * x + 2 * t;
+        const uint8_t* va = st.v + key * Stage<D>::kVRow + g * (D / 16);
+        const uint8_t* vb = va + Stage<D>::kVRow;
+        if constexpr (kHalves % 2 == 0) {
+          uint32_t wa[kHalves / 2], wb[kHalves / 2];
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(va);
+            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(vb);
+          } else {
+            wa[0] = *reinterpret_cast<const uint32_t*>(va);
+            wb[0] = *reinterpret_cast<const uint32_t*>(vb);
+          }
+#pragma unroll
+          for (int c = 0; c < kHalves / 2; ++c) {
+            vh[half][x][2 * c] = __byte_perm(wa[c], wb[c], 0x5410);
+            vh[half][x][2 * c + 1] = __byte_perm(wa[c], wb[c], 0x7632);
+          }
         } else {
 #pragma unroll
-          for (int c = 0; c < kWords; ++c) {
-            ka[c] = reinterpret_cast<const uint32_t*>(krow)[c];
-            kb[c] = reinterpret_cast<const uint32_t*>(krow + 8 * (D / 2))[c];
-          }
+          for (int c = 0; c < kHalves; ++c)
+            vh[half][x][c] = (uint32_t)reinterpret_cast<const uint16_t*>(va)[c] |
+                             ((uint32_t)reinterpret_cast<const uint16_t*>(vb)[c] << 16);
         }
-        uint32_t za = 0, zb = 0;
-        if constexpr (kF32) {
-          const uint32_t ma = st.km[16 * half + g], mb = st.km[16 * half + g + 8];
-          za = add_bf16x2_(__byte_perm(ma, ma, 0x3232), 0x43004300u);
-          zb = add_bf16x2_(__byte_perm(mb, mb, 0x3232), 0x43004300u);
-        }
-#pragma unroll
-        for (int p = kTerms - 1; p >= 0; --p)
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            const int i = 2 * (k & 1);
-            uint32_t a0 = widen(ka[k >> 1], i), a1 = widen(kb[k >> 1], i), a2 = widen(ka[k >> 1], i + 1),
-                     a3 = widen(kb[k >> 1], i + 1);
-            if constexpr (kF32) {
-              a0 = sub_bf16x2(a0, za), a1 = sub_bf16x2(a1, zb), a2 = sub_bf16x2(a2, za), a3 = sub_bf16x2(a3, zb);
-            }
-#pragma unroll
-            for (int w = 0; w < NQ; ++w) mma16816(s[w], a0, a1, a2, a3, qf[w][k][0][p], qf[w][k][1][p]);
-          }
-#pragma unroll
-        for (int w = 0; w < NQ; ++w)
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-            *reinterpret_cast<float2*>(xs[16 * half + 8 * x + g] + 4 * (8 * w + 2 * t)) =
-                make_float2(s[w][2 * x], s[w][2 * x + 1]);
+        vz[half][x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
       }
-      __syncwarp();
-      // ---- weights: lane = key, only the rows there are
-      uint32_t p[kWTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
-      {
-        const int j = j0 + lane;
-        const uint32_t km = st.km[lane], vm = st.vm[lane];
-        const float ks = a.alpha * meta_scale(km), kz = kF32 ? 0.f : -(128.f + meta_zero(km));
-        const float vs = meta_scale(vm);
-        const long long tj = st.ts[lane];
-        const float* bias_of = a.rab_pos - min(j, L);
-        const float* sc_of = reinterpret_cast<const float*>(xs[lane]);
-        float pos_bias[8 * NQ];  // all rows' loads on the way before the first is used
+    // row g of tile m is the thread's nibble m of its D / 8, row g + 8 its nibble m + D / 16
 #pragma unroll
-        for (int r = 0; r < 8 * NQ; ++r) {
-          if (r >= nr) break;
-          pos_bias[r] = __ldg(bias_of + sm.rp[r]);
-        }
-        uint32_t pk[kWTerms][4 * NQ];
+    for (int m2 = 0; m2 < kTilesM; ++m2) {
+      constexpr int kSecond = D / 16;
+      float f[NQ][4];
 #pragma unroll
-        for (int r = 0; r < 8 * NQ; r += 2) {
-          float wt[2] = {0.f, 0.f};
+      for (int w = 0; w < NQ; ++w)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (r + e < nr) {
-              const float bias = pos_bias[r + e] + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
-              const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
-              wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
-            }
-          if constexpr (kWTerms > 1) {
-            float y[2][kWTerms];
-            split_bf16(wt[0], y[0]);
-            split_bf16(wt[1], y[1]);
+        for (int e = 0; e < 4; ++e) f[w][e] = kF32 ? 0.f : o[w][m2][e];
+      uint32_t av[2][4];
 #pragma unroll
-            for (int x = 0; x < kWTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
-          } else {
-            pk[0][r / 2] = pack_bf16x2(wt[0], wt[1]);
-          }
-        }
-        // the lane's weights over its own scores, then transposed by ldmatrix
+      for (int half = 0; half < 2; ++half) {
+        av[half][0] = sub_bf16x2(widen(vh[half][0][m2 >> 2], m2 & 3), vz[half][0]);
+        av[half][1] = sub_bf16x2(widen(vh[half][0][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][0]);
+        av[half][2] = sub_bf16x2(widen(vh[half][1][m2 >> 2], m2 & 3), vz[half][1]);
+        av[half][3] = sub_bf16x2(widen(vh[half][1][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][1]);
+      }
 #pragma unroll
-        for (int x = 0; x < kWTerms; ++x)
+      for (int x = kWTerms - 1; x >= 0; --x)
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int w = 0; w < NQ; ++w)
-            *reinterpret_cast<uint4*>(xs[lane] + 16 * (NQ * x + w)) =
-                make_uint4(pk[x][4 * w], pk[x][4 * w + 1], pk[x][4 * w + 2], pk[x][4 * w + 3]);
-        __syncwarp();
+            mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half],
+                     p[x][w][2 * half + 1]);
 #pragma unroll
-        for (int x = 0; x < kWTerms; ++x)
+      for (int w = 0; w < NQ; ++w)
 #pragma unroll
-          for (int w = 0; w < NQ; ++w)
-            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(p[x][w][0]), "=r"(p[x][w][1]), "=r"(p[x][w][2]), "=r"(p[x][w][3])
-                         : "r"(smem_u32(xs[lane] + 16 * (NQ * x + w)))
-                         : "memory");
-      }
-      // ---- O^T += (codes' - vz) P^T
-      // 16-bit pieces (4 codes) of a V row a thread reads: its eighth of the dimensions
-      constexpr int kHalves = D / 32;
-      // [16 keys][lo, hi]: keys 2 t, 2 t + 1 (lo) or 2 t + 8, 2 t + 9 (hi) side by side
-      uint32_t vh[2][2][kHalves];
-      uint32_t vz[2][2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = 16 * half + 8 * x + 2 * t;
-          const uint8_t* va = st.v + key * Stage<D>::kVRow + g * (D / 16);
-          const uint8_t* vb = va + Stage<D>::kVRow;
-          if constexpr (kHalves % 2 == 0) {
-            uint32_t wa[kHalves / 2], wb[kHalves / 2];
-            if constexpr (D == 128) {
-              *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(va);
-              *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(vb);
-            } else {
-              wa[0] = *reinterpret_cast<const uint32_t*>(va);
-              wb[0] = *reinterpret_cast<const uint32_t*>(vb);
-            }
-#pragma unroll
-            for (int c = 0; c < kHalves / 2; ++c) {
-              vh[half][x][2 * c] = __byte_perm(wa[c], wb[c], 0x5410);
-              vh[half][x][2 * c + 1] = __byte_perm(wa[c], wb[c], 0x7632);
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < kHalves; ++c)
-              vh[half][x][c] = (uint32_t)reinterpret_cast<const uint16_t*>(va)[c] |
-                               ((uint32_t)reinterpret_cast<const uint16_t*>(vb)[c] << 16);
-          }
-          vz[half][x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
-        }
-      // row g of tile m is the thread's nibble m of its D / 8, row g + 8 its nibble m + D / 16
-#pragma unroll
-      for (int m2 = 0; m2 < kTilesM; ++m2) {
-        constexpr int kSecond = D / 16;
-        float f[NQ][4];
-#pragma unroll
-        for (int w = 0; w < NQ; ++w)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[w][e] = kF32 ? 0.f : o[w][m2][e];
-        uint32_t av[2][4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          av[half][0] = sub_bf16x2(widen(vh[half][0][m2 >> 2], m2 & 3), vz[half][0]);
-          av[half][1] = sub_bf16x2(widen(vh[half][0][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][0]);
-          av[half][2] = sub_bf16x2(widen(vh[half][1][m2 >> 2], m2 & 3), vz[half][1]);
-          av[half][3] = sub_bf16x2(widen(vh[half][1][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][1]);
-        }
-#pragma unroll
-        for (int x = kWTerms - 1; x >= 0; --x)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int w = 0; w < NQ; ++w)
-              mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half],
-                       p[x][w][2 * half + 1]);
-#pragma unroll
-        for (int w = 0; w < NQ; ++w)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[w][m2][e] = kF32 ? o[w][m2][e] + f[w][e] : f[w][e];
-      }
-      __syncwarp();  // the tile's slot may be filled again
+        for (int e = 0; e < 4; ++e) o[w][m2][e] = kF32 ? o[w][m2][e] + f[w][e] : f[w][e];
     }
-    cp_wait<0>();
-
-    // ---- the new rows' own keys: row r by worker r of the user's parts x warps, fp32
-    for (int x = threadIdx.x; x < 8 * NQ * D; x += kThreads) (&sm.self[0][0])[x] = 0.f;
-    __syncthreads();
-    for (int r = split + parts * warp; r < nr; r += parts * kWarps) {
-      constexpr int kPer = D / 32;
-      const int i = L + r0 + r;
-      const size_t row = (size_t)(q0 + r0 + r) * a.qkv_stride + head * D + kPer * lane;
-      float qv[kPer], acc[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        qv[e] = as_f(q[row + e]);
-        acc[e] = 0.f;
-      }
-      const bool cand = i >= hist;
-      const int j_end = cand ? hist : i + 1;
-      const long long ti = ts[i];
-      // its keys L .. j_end - 1, and a candidate's own; four at a time, so that their loads overlap
-      const int count = j_end - L + (cand ? 1 : 0);
-#pragma unroll 1
-      for (int c0 = 0; c0 < count; c0 += 4) {
-        float dot[4], bias[4], vv[4][kPer];
-        long long tj[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int x = min(c0 + c, count - 1), j = L + x < j_end ? L + x : i;
-          const size_t at = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
-          dot[c] = 0.f;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            dot[c] = fmaf(qv[e], as_f(kn[at + e]), dot[c]);
-            vv[c][e] = as_f(vn[at + e]);
-          }
-          bias[c] = a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1];
-          tj[c] = ts[j];
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) dot[c] += __shfl_xor_sync(~0u, dot[c], o);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c0 + c < count) {  // (nothing of a key past the last is used)
-            const float wt =
-                silu_of<T>(a.alpha * dot[c] + bias[c] + time_bias(sm.thr, sm.rts, sm.oct, ti - tj[c]));
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, vv[c][e], acc[e]);
-          }
-      }
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) sm.self[r][kPer * lane + e] = acc[e];
-    }
-    // ---- the warps' sums meet in shared memory (the ring is idle) and go out in order
-#pragma unroll
-    for (int w = 0; w < NQ; ++w)
-#pragma unroll
-      for (int m = 0; m < kTilesM; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int idx = m + (e >> 1) * (D / 16), half = idx >> 2, nib = idx & 3;
-          // 16-bit piece (D / 32) g + half of the row: elements 0, 2, 4, 6 of its word, or 1, 3, 5, 7
-          const int piece = (D / 32) * g + half, dim = 8 * (piece >> 1) + 2 * nib + (piece & 1);
-          sm.red[warp][8 * w + 2 * t + (e & 1)][dim] = o[w][m][e];
-        }
-    __syncthreads();
-    float* out = a.o_ws + (((size_t)split * a.T_q + q0 + r0) * a.H + head) * D;
-    for (int x = threadIdx.x; x < nr * D; x += kThreads) {
-      const int r = x / D, e = x % D;
-      float s = sm.self[r][e];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sm.red[w][r][e];
-      out[(size_t)r * a.H * D + e] = s;
-    }
-    __syncthreads();
+    __syncwarp();  // the tile's slot may be filled again
   }
+  cp_wait<0>();
+
+  // ---- the new rows' own keys: row r by worker r of the user's parts x warps, fp32
+  for (int x = threadIdx.x; x < 8 * NQ * D; x += kThreads) (&sm.self[0][0])[x] = 0.f;
+  __syncthreads();
+  for (int r = split + parts * warp; r < nr; r += parts * kWarps) {
+    constexpr int kPer = D / 32;
+    const int i = L + r0 + r;
+    const size_t row = (size_t)(q0 + r0 + r) * a.qkv_stride + head * D + kPer * lane;
+    float qv[kPer], acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      qv[e] = as_f(q[row + e]);
+      acc[e] = 0.f;
+    }
+    const bool cand = i >= hist;
+    const int j_end = cand ? hist : i + 1;
+    const long long ti = ts[i];
+    // its keys L .. j_end - 1, and a candidate's own; four at a time, so that their loads overlap
+    const int count = j_end - L + (cand ? 1 : 0);
+#pragma unroll 1
+    for (int c0 = 0; c0 < count; c0 += 4) {
+      float dot[4], bias[4], vv[4][kPer];
+      long long tj[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int x = min(c0 + c, count - 1), j = L + x < j_end ? L + x : i;
+        const size_t at = (size_t)(q0 + j - L) * a.qkv_stride + head * D + kPer * lane;
+        dot[c] = 0.f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          dot[c] = fmaf(qv[e], as_f(kn[at + e]), dot[c]);
+          vv[c][e] = as_f(vn[at + e]);
+        }
+        bias[c] = a.rab_pos[min(i, hist) - min(j, hist) + a.n_max - 1];
+        tj[c] = ts[j];
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dot[c] += __shfl_xor_sync(~0u, dot[c], o);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c0 + c < count) {  // (nothing of a key past the last is used)
+          const float wt =
+              silu_of<T>(a.alpha * dot[c] + bias[c] + time_bias(sm.thr, sm.rts, sm.oct, ti - tj[c]));
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[e] = fmaf(wt, vv[c][e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sm.self[r][kPer * lane + e] = acc[e];
+  }
+  // ---- the warps' sums meet in shared memory (the ring is idle) and go out in order
+#pragma unroll
+  for (int w = 0; w < NQ; ++w)
+#pragma unroll
+    for (int m = 0; m < kTilesM; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int idx = m + (e >> 1) * (D / 16), half = idx >> 2, nib = idx & 3;
+        // 16-bit piece (D / 32) g + half of the row: elements 0, 2, 4, 6 of its word, or 1, 3, 5, 7
+        const int piece = (D / 32) * g + half, dim = 8 * (piece >> 1) + 2 * nib + (piece & 1);
+        sm.red[warp][8 * w + 2 * t + (e & 1)][dim] = o[w][m][e];
+      }
+  __syncthreads();
+  float* out = a.o_ws + (((size_t)split * a.T_q + q0 + r0) * a.H + head) * D;
+  for (int x = threadIdx.x; x < nr * D; x += kThreads) {
+    const int r = x / D, e = x % D;
+    float s = sm.self[r][e];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += sm.red[w][r][e];
+    out[(size_t)r * a.H * D + e] = s;
+  }
+  __syncthreads();
 
   if (checks) check_keys();  // (the keys' own loads have them in the caches by now)
 
   // ---- the last CTA of these rows adds the parts, normalises and gates
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[u * row_groups + rg], 1) == a.H * parts - 1;
+  if (threadIdx.x == 0) sm.last = atomicAdd(&counters[tile], 1) == a.H * parts - 1;
   __syncthreads();
   if (!sm.last) return;
   __threadfence();
@@ -612,12 +612,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   float* sums = reinterpret_cast<float*>(sm.ring);  // [kWarps][HD]
   // four rows at a time: all threads add their parts (eight loads each on the way), then a warp finishes a row
 #pragma unroll 1
-  for (int x0 = 0;; x0 += kWarps) {
-    const int base = 8 * NQ * (rg + x0 / (8 * NQ) * row_groups), first = base + x0 % (8 * NQ);
-    if (base >= rows) break;
-    const int nr = min(kWarps, rows - first);
-    if (nr <= 0) continue;
-    const size_t row = q0 + first + min(warp, nr - 1);
+  for (int first = r0; first < r0 + nr; first += kWarps) {
+    const int there = min(kWarps, r0 + nr - first);
+    const size_t row = q0 + first + min(warp, there - 1);
     float2 x[16], uv[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -628,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
       }
     }
 #pragma unroll 1
-    for (int e = 4 * threadIdx.x; e < nr * HD; e += 4 * kThreads) {
+    for (int e = 4 * threadIdx.x; e < there * HD; e += 4 * kThreads) {
       const float* src = a.o_ws + (size_t)(q0 + first) * HD + e;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -652,12 +649,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float* src = sums + min(warp, nr - 1) * HD + 64 * k + 2 * lane;
+      const float* src = sums + min(warp, there - 1) * HD + 64 * k + 2 * lane;
       x[k] = 64 * k + 2 * lane < HD ? *reinterpret_cast<const float2*>(src) : make_float2(0.f, 0.f);
       sum += x[k].x + x[k].y;
     }
     __syncthreads();  // (the next rows' sums go over these)
-    if (warp >= nr) continue;
+    if (warp >= there) continue;
     if (a.out_raw) {
       float* out = static_cast<float*>(a.out) + row * HD + 2 * lane;
 #pragma unroll
@@ -690,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
 }
 
 template <typename T, int D, int NQ, int WT>
-cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order, int row_groups,
+cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles, int n_tiles,
                    cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<T, D, NQ>);
   int dev = 0;
@@ -702,18 +699,20 @@ cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters,
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
-  return launch_dependent(attn_q4_small_kernel<T, D, NQ, WT>, dim3(a.num_splits * row_groups, a.H, a.B), dim3(kThreads),
-                          smem, s, a, thr, counters, order, row_groups);
+  const long long ctas = (long long)n_tiles * a.H * a.num_splits;
+  if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  return launch_dependent(attn_q4_small_kernel<T, D, NQ, WT>, dim3((unsigned)ctas), dim3(kThreads), smem, s, a, thr,
+                          counters, tiles);
 }
 
 template <typename T, int NQ, int WT>
-cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
-                     int row_groups, cudaStream_t s) {
+cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles, int n_tiles,
+                     cudaStream_t s) {
   switch (a.d) {
-    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, order, row_groups, s);
-    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, order, row_groups, s);
-    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, order, row_groups, s);
-    default: return launch<T, 128, 1, WT>(a, thr, counters, order, row_groups, s);
+    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, tiles, n_tiles, s);
+    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, tiles, n_tiles, s);
+    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, tiles, n_tiles, s);
+    default: return launch<T, 128, 1, WT>(a, thr, counters, tiles, n_tiles, s);
   }
 }
 
@@ -723,17 +722,17 @@ bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
   return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535 && pool_rows < 0xFFFFFFFFll;
 }
 
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
-                                 int rows, int groups, int max_seq_len, cudaStream_t s) {
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,
+                                 int n_tiles, int rows, int max_seq_len, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   if (!a.in_bf16)
-    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, order, groups, s)
-                     : launch_d<float, 2, 3>(a, thr, counters, order, groups, s);
+    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, tiles, n_tiles, s)
+                     : launch_d<float, 2, 3>(a, thr, counters, tiles, n_tiles, s);
   if (std::min(max_seq_len, a.n_max) <= kShortSequence)
-    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, order, groups, s)
-                     : launch_d<bf16, 2, 2>(a, thr, counters, order, groups, s);
-  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, order, groups, s)
-                   : launch_d<bf16, 2, 1>(a, thr, counters, order, groups, s);
+    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, tiles, n_tiles, s)
+                     : launch_d<bf16, 2, 2>(a, thr, counters, tiles, n_tiles, s);
+  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, tiles, n_tiles, s)
+                   : launch_d<bf16, 2, 1>(a, thr, counters, tiles, n_tiles, s);
 }
 
 }  // namespace hstu

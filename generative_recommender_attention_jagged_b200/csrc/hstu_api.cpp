@@ -155,30 +155,23 @@ Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
 
 // Rows of one pass of the small kernel over the cached bytes: 16 where users have
 // more than 8 on average (fp32 calls with d > 64: 8, their three-term operands fill
-// the registers; bf16 calls with d = 128 and that many rows are kQ4Tc's), and the CTAs
-// that share a user's passes: room for twice the average number of rows, since users
-// differ (a CTA without rows ends at once).
+// the registers; bf16 calls with d = 128 and that many rows are kQ4Tc's).
 int q4_small_rows(const hstu_attn_params* p) {
   const bool wide = p->head_dim > (p->dtype == HSTU_DT_F32 ? 64 : 96);
   return (long long)p->total_tokens <= 8ll * p->batch || wide ? 8 : 16;
 }
-int q4_small_groups(const hstu_attn_params* p) {
-  const long long rows = q4_small_rows(p), per = (long long)p->batch * rows;
-  const long long avg = (p->total_tokens + per - 1) / per;
-  return (int)std::max<long long>(1, std::min<long long>(64, avg <= 1 ? avg : 2 * avg));
-}
 
-// at most this many 128-row query tiles: sum over users of ceil(rows / 128)
-int q4_tiles(const hstu_attn_params* p) { return p->total_tokens / kTile + p->batch; }
+// at most this many query tiles: sum over users of ceil(rows / tile_rows), at least one each
+int q4_tiles(const hstu_attn_params* p, int tile_rows) { return p->total_tokens / tile_rows + p->batch; }
 
 Layout q4_layout_for(const hstu_attn_params* p, int splits, Q4Kernel kernel) {
   if (kernel == kQ4Simt) return layout_for(p, 1, false, 1);
-  // header, the plan (few rows: users in order, a counter per user and row group; else tiles), partial sums
+  // header, the plan (tiles; few rows: a counter for each), partial sums
   Layout l;
   l.max_items = 0;
   l.items_off = sizeof(WsHeader);
-  const size_t plan = kernel == kQ4Small ? (size_t)p->batch * (1 + q4_small_groups(p)) * sizeof(int32_t)
-                                         : (size_t)q4_tiles(p) * sizeof(int2);
+  const size_t plan = kernel == kQ4Small ? (size_t)q4_tiles(p, q4_small_rows(p)) * (sizeof(int2) + sizeof(int32_t))
+                                         : (size_t)q4_tiles(p, kTile) * sizeof(int2);
   l.o_off = align_up(l.items_off + plan);
   l.total = align_up(l.o_off + (size_t)splits * p->total_tokens * p->num_heads * p->head_dim * sizeof(float));
   return l;
@@ -297,12 +290,11 @@ int run(const hstu_attn_params* p, const Common& c) {
   cudaError_t e = cudaSuccess;
   if (q4_kernel == kQ4Small) {
     a.num_splits = c.splits;
-    int32_t* order = reinterpret_cast<int32_t*>(static_cast<char*>(c.ws) + l.items_off);
-    int32_t* counters = order + a.B;
-    const int groups = q4_small_groups(p);
-    e = launch_plan_q4(a, counters, a.B * groups, order, nullptr, 0, c.stream);
-    if (e == cudaSuccess)
-      e = launch_attn_q4_small(a, thr, counters, order, q4_small_rows(p), groups, p->max_seq_len, c.stream);
+    const int rows = q4_small_rows(p), n_tiles = q4_tiles(p, rows);
+    int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
+    int32_t* counters = reinterpret_cast<int32_t*>(tiles + n_tiles);
+    e = launch_plan_q4(a, counters, tiles, n_tiles, rows, 1, c.stream);
+    if (e == cudaSuccess) e = launch_attn_q4_small(a, thr, counters, tiles, n_tiles, rows, p->max_seq_len, c.stream);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
@@ -311,13 +303,13 @@ int run(const hstu_attn_params* p, const Common& c) {
     CUtensorMap tq;
     if (!encode_rows(&tq, c.q, a.T_q, a.H, a.d, a.qkv_stride)) return HSTU_ERR_CUDA;
     int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
-    e = launch_plan_q4(a, nullptr, 0, nullptr, tiles, q4_tiles(p), c.stream);
+    e = launch_plan_q4(a, nullptr, tiles, q4_tiles(p, kTile), kTile, 0, c.stream);
     if (e == cudaSuccess) e = launch_attn_q4_sm100(a, thr, tiles, tq, p->max_seq_len, c.stream);
     if (e == cudaSuccess) e = launch_epilogue(a, c.stream);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (stages & HSTU_F_STAGE_PLAN) {
-    e = plan_checks_users_first(a) ? launch_plan_q4(a, nullptr, 0, nullptr, nullptr, 0, c.stream)
+    e = plan_checks_users_first(a) ? launch_plan_q4(a, nullptr, nullptr, 0, kTile, 0, c.stream)
                                    : cudaMemsetAsync(c.ws, 0, sizeof(WsHeader), c.stream);
     if (e != cudaSuccess) return HSTU_ERR_CUDA;
     if ((e = launch_plan(a, tc, p->max_seq_len, c.stream)) != cudaSuccess) return HSTU_ERR_CUDA;

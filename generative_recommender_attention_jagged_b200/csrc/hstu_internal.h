@@ -162,16 +162,18 @@ __host__ __device__ inline bool plan_checks_users_first(const AttnArgs& a) {
 }
 
 // Checks of the users and the order of the work for the 4-bit kernels (hstu_kernels.cu).
-cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
-                           int n_tiles, cudaStream_t s);
+// tiles [n_tiles]: user and tile of tile_rows new rows, -1 behind the last (least: the fewest tiles of a user);
+// counters, if any, [n_tiles], are zeroed.
+cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int2* tiles, int n_tiles, int tile_rows, int least,
+                           cudaStream_t s);
 
 // A few new rows a user over a 4-bit pool (attn_q4_small.cu): attention and the
-// LayerNorm gate in one launch behind launch_plan_q4; counters [B * groups] zeroed,
-// order [B] of the users.  bf16 and fp32, d = 32, 64, 96 or 128.  rows: 8 or 16 of a
-// pass over the cached bytes; groups: CTAs that share a user's passes.
+// LayerNorm gate in one launch behind launch_plan_q4, which lists the tiles of rows = 8
+// or 16 new rows (a pass over the cached bytes; users without new rows have one, which
+// is checked) and zeroes their counters.  bf16 and fp32, d = 32, 64, 96 or 128.
 bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
-cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int32_t* order,
-                                 int rows, int groups, int max_seq_len, cudaStream_t s);
+cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,
+                                 int n_tiles, int rows, int max_seq_len, cudaStream_t s);
 
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128, tiles
 // [T_q / 128 + B] as launch_plan_q4 lists them; partial sums to o_ws, then launch_epilogue.

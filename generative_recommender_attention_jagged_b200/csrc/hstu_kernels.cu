@@ -168,33 +168,37 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttnArgs a, in
 // plan of the 4-bit cache's kernels, in one block: clears the header and the
 // counters, checks every user's offsets, lengths and candidate count (hdr->pad[0] =
 // 1 if all are good; the kernels behind return otherwise, so nothing is read by way
-// of offsets that do not hold), and lists the users (order) or their 128-row query
-// tiles (tiles: user and tile; -1 behind the last).  Up to kPlanUsers users come in
-// the order of their lengths, longest first, so that the last CTAs to start are short
-// ones: 64 users of 1000 to 8192 tokens in their own order kept a third of the SMs
-// waiting for the longest (97 us against 81).  Larger batches, whose users each get a
-// small part of the GPU, keep their own order.
+// of offsets that do not hold), and lists the users' tiles of new rows (user and tile;
+// -1 behind the last), so that the work follows what each user really has: 63 users with
+// one new row and one with 449 took 6.8 ms where CTAs were given out by the average.  Up
+// to kPlanUsers users come in the order of their lengths, longest first, so that the last
+// CTAs to start are short ones: 64 users of 1000 to 8192 tokens in their own order kept a
+// third of the SMs waiting for the longest (97 us against 81).  Larger batches, whose
+// users each get a small part of the GPU, keep their own order.
 // ---------------------------------------------------------------------------
 constexpr int kPlanUsers = 512;
 
-__global__ void __launch_bounds__(kPlanUsers) plan_q4_kernel(const AttnArgs a, int32_t* counters, int n_counters,
-                                                             int32_t* order, int2* tiles, int n_tiles) {
+__global__ void __launch_bounds__(kPlanUsers) plan_q4_kernel(const AttnArgs a, int32_t* counters, int2* tiles, int n_tiles,
+                                                             int tile_rows, int least) {
   __shared__ int len[kPlanUsers], user[kPlanUsers], scan[kPlanUsers / 32];
   grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   for (int x = tid; x < (int)(sizeof(WsHeader) / 4); x += threads) reinterpret_cast<int32_t*>(a.hdr)[x] = 0;
-  for (int x = tid; x < n_counters; x += threads) counters[x] = 0;
+  if (counters)
+    for (int x = tid; x < n_tiles; x += threads) counters[x] = 0;
   const bool sorted = a.B <= threads;
   const int mine = sorted && tid < a.B ? a.cached_lens[tid] : 0;
   if (sorted) len[tid] = mine;
   __syncthreads();
-  int bad = 0;
+  auto tiles_of = [&](int u) { return max(least, (a.q_offsets[u + 1] - a.q_offsets[u] + tile_rows - 1) / tile_rows); };
+  int bad = 0, differ = 0;  // differ: a user has more tiles than one, or none
   for (int u = tid; u < a.B; u += threads) {
     int n, tso, pages;
     if (!check_user(a, u, n, tso, pages)) {
       report_error(a.hdr, kErrLength, u);
       bad = 1;
     }
+    differ |= tiles_of(u) != 1;
   }
   if (sorted && tid < a.B) {
     int rank = 0;
@@ -204,12 +208,13 @@ __global__ void __launch_bounds__(kPlanUsers) plan_q4_kernel(const AttnArgs a, i
   bad = __syncthreads_or(bad);
   if (bad) return;
   if (tid == 0) a.hdr->pad[0] = 1;
-  if (order)
-    for (int x = tid; x < a.B; x += threads) order[x] = sorted ? user[x] : x;
   if (!tiles) return;
+  if (!__syncthreads_or(differ)) {  // the common batch of a few rows a user needs no sums
+    for (int x = tid; x < n_tiles; x += threads) tiles[x] = make_int2(x >= a.B ? -1 : sorted ? user[x] : x, 0);
+    return;
+  }
   // thread t lists the tiles of users t * per .. (in the order above) behind those of the threads before
   const int per = (a.B + threads - 1) / threads, lo = min(a.B, tid * per), hi = min(a.B, lo + per);
-  auto tiles_of = [&](int u) { return (a.q_offsets[u + 1] - a.q_offsets[u] + kTile - 1) / kTile; };
   int count = 0;
   for (int x = lo; x < hi; ++x) count += tiles_of(sorted ? user[x] : x);
   int incl = count;
@@ -666,10 +671,10 @@ cudaError_t launch_plan(const AttnArgs& a, bool schedule, int max_seq_len, cudaS
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int n_counters, int32_t* order, int2* tiles,
-                           int n_tiles, cudaStream_t s) {
+cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int2* tiles, int n_tiles, int tile_rows, int least,
+                           cudaStream_t s) {
   const int threads = std::min(kPlanUsers, std::max(64, (a.B + 31) / 32 * 32));
-  plan_q4_kernel<<<1, threads, 0, s>>>(a, counters, n_counters, order, tiles, n_tiles);
+  plan_q4_kernel<<<1, threads, 0, s>>>(a, counters, tiles, n_tiles, tile_rows, least);
   return cudaGetLastError();
 }
 
