@@ -205,8 +205,6 @@ __device__ __forceinline__ int chunk_mode(Walk& w, const long long* ts, int col0
   if (!__all_sync(~0u, uni)) {
     const long long tlim2 = w.b > 0 ? w.t_i + 1 - thr[w.b - 1] : LLONG_MIN;
     const bool one = uni || t_last <= tlim2;              // at most one edge in the chunk
-    // octave mode, which every lane then takes, needs |dt| + 1 < 2^32 at the chunk's first allowed column
-    const bool narrow = none || (w.t_i + 1 - ts[col0]) < (1ll << 32);
     if (__all_sync(~0u, one)) {
       mode = kBiasEdge;
       if (!uni) {
@@ -220,7 +218,8 @@ __device__ __forceinline__ int chunk_mode(Walk& w, const long long* ts, int col0
         w.tsb = rts[w.b];
       }
     } else {
-      mode = __all_sync(~0u, narrow) ? kBiasOct : kBiasWalk;
+      // octave mode, which every lane then takes, needs |dt| + 1 < 2^32 at the chunk's first allowed column
+      mode = __all_sync(~0u, none || (w.t_i + 1 - ts[col0]) < (1ll << 32)) ? kBiasOct : kBiasWalk;
     }
   }
   return mode;
