@@ -718,8 +718,8 @@ cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counter
 
 }  // namespace
 
-bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows) {
-  return head_dim <= 128 && head_dim % 32 == 0 && batch <= 65535 && pool_rows < 0xFFFFFFFFll;
+bool attn_q4_small_supported(int head_dim, long long pool_rows) {
+  return head_dim <= 128 && head_dim % 32 == 0 && pool_rows < 0xFFFFFFFFll;
 }
 
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,

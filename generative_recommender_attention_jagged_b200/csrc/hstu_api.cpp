@@ -149,7 +149,7 @@ enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 // pool_rows: num_pages * H * page_size, 0 where it is not known yet (workspace sizes: the CUDA-core kernel,
 // which pools of 2^32 rows fall back to, needs the least)
 Q4Kernel q4_kernel_for(const hstu_attn_params* p, long long pool_rows = 0) {
-  if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, p->batch, pool_rows)) return kQ4Simt;
+  if ((p->flags & HSTU_F_FORCE_SIMT) || !attn_q4_small_supported(p->head_dim, pool_rows)) return kQ4Simt;
   return use_tensor_cores(p) && (long long)p->total_tokens > 8ll * p->batch ? kQ4Tc : kQ4Small;
 }
 

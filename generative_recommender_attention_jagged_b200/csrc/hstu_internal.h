@@ -171,7 +171,7 @@ cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int2* tiles, in
 // LayerNorm gate in one launch behind launch_plan_q4, which lists the tiles of rows = 8
 // or 16 new rows (a pass over the cached bytes; users without new rows have one, which
 // is checked) and zeroes their counters.  bf16 and fp32, d = 32, 64, 96 or 128.
-bool attn_q4_small_supported(int head_dim, int batch, long long pool_rows);
+bool attn_q4_small_supported(int head_dim, long long pool_rows);
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,
                                  int n_tiles, int rows, int max_seq_len, cudaStream_t s);
 
