@@ -184,7 +184,7 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
   return max(kMinPart, ((L + splits - 1) / splits + kKeys - 1) / kKeys * kKeys);
 }
 
-// (four CTAs an SM for one N tile of bf16 rows: 127 registers; three otherwise)
+// (four CTAs an SM for one N tile of bf16 rows: 125 registers; three otherwise)
 template <typename T, int D, int NQ, int WT>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int2* row_tiles) {

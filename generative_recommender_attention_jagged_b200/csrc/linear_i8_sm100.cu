@@ -245,7 +245,6 @@ struct GemmI8Args {
   long long T;
   int K, N;
   long long out_stride;  // elements
-  int silu;
   const float* x_scale;
   const float* w_scale;
   const float* bias;
@@ -287,15 +286,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
 constexpr float kMinusLog2e = -1.4426950408889634f;
 
 template <typename TOut>
-__device__ __forceinline__ float act_i8(float x, int silu) {
-  if (!silu) return x;
+__device__ __forceinline__ float silu_i8(float x) {
   if constexpr (sizeof(TOut) == 2) return x * rcp_approx(1.f + ex2_approx(kMinusLog2e * x));
   else return x / (1.f + expf(-x));
 }
 
 // One CTA per 128 x BN output tile.  Warp 0: TMA producer; warp 1: MMA issuer
 // and owner of tensor memory; warps 2-5: epilogue (thread = output row).
-template <int BN, typename TOut>
+template <int BN, typename TOut, bool SILU>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_i8_kernel(const GemmI8Args a, const __grid_constant__ CUtensorMap tm_x,
                    const __grid_constant__ CUtensorMap tm_w) {
@@ -382,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float b = a.bias ? __ldg(a.bias + n + i) : 0.f;
-            y[i] = act_i8<TOut>(fmaf(__int2float_rn((int)acc[e + i]), xs * __ldg(a.w_scale + n + i), b), a.silu);
+            const float v = fmaf(__int2float_rn((int)acc[e + i]), xs * __ldg(a.w_scale + n + i), b);
+            y[i] = SILU ? silu_i8<TOut>(v) : v;
           }
           if (row < a.T) store8(out + n, y);
         }
@@ -639,8 +638,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 unpack_pair(add_pair(pack_pair(ex2_approx(n0), ex2_approx(n1)), pack_pair(1.f, 1.f)), d0, d1);
                 unpack_pair(mul_pair(v2, pack_pair(rcp_approx(d0), rcp_approx(d1))), y[k + q], y[k + q + 1]);
               } else {
-                y[k + q] = SILU ? act_i8<TOut>(v0, 1) : v0;
-                y[k + q + 1] = SILU ? act_i8<TOut>(v1, 1) : v1;
+                y[k + q] = SILU ? silu_i8<TOut>(v0) : v0;
+                y[k + q + 1] = SILU ? silu_i8<TOut>(v1) : v1;
               }
             }
           }
@@ -730,12 +729,12 @@ bool encode_codes(CUtensorMap* m, const void* base, long long rows, int K, int b
 
 long long pair_units(long long T, int N) { return ((T + 2 * kBM - 1) / (2 * kBM)) * ((N + kPairBN - 1) / kPairBN); }
 
-template <int BN, typename TOut>
+template <int BN, typename TOut, bool SILU>
 cudaError_t launch_single(const GemmI8Args& a, const void* xq, const void* wq, int dev, cudaStream_t s) {
   constexpr size_t smem = sizeof(SmemI8<BN>) + 1024;
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<BN, TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<BN, TOut, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
@@ -743,7 +742,7 @@ cudaError_t launch_single(const GemmI8Args& a, const void* xq, const void* wq, i
   CUtensorMap tx, tw;
   if (!encode_codes(&tx, xq, a.T, a.K, kBM) || !encode_codes(&tw, wq, a.N, a.K, BN)) return cudaErrorInvalidValue;
   const long long tiles = ((a.T + kBM - 1) / kBM) * ((a.N + BN - 1) / BN);
-  gemm_i8_kernel<BN, TOut><<<(unsigned)tiles, kThreads, smem, s>>>(a, tx, tw);
+  gemm_i8_kernel<BN, TOut, SILU><<<(unsigned)tiles, kThreads, smem, s>>>(a, tx, tw);
   return cudaGetLastError();
 }
 
@@ -867,7 +866,7 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   a.K = p->d_in;
   a.N = p->d_out;
   a.out_stride = p->out_stride ? p->out_stride : p->d_out;
-  a.silu = (p->flags & HSTU_LIN_SILU) ? 1 : 0;
+  const bool silu = (p->flags & HSTU_LIN_SILU) != 0;
   a.x_scale = xscale;
   a.w_scale = w_scale;
   a.bias = bias;
@@ -879,16 +878,18 @@ int hstu_linear_i8(const hstu_linear_i8_params* p, const void* x, const int8_t* 
   // 1024 x 512 x 2048 (128 tiles) 13.8 / 13.3, 2048 x 512 x 2048 (256) 23.2 / 13.8,
   // 16384 x 512 x 512 (512) 44 / 21.
   const long long single_tiles = ((p->rows + kBM - 1) / kBM) * ((p->d_out + 127) / 128);
+  const bool bf16 = p->out_dtype == HSTU_DT_BF16;
   cudaError_t e;
   if (single_tiles > sms)
-    e = p->out_dtype == HSTU_DT_BF16
-            ? (a.silu ? launch_pair<__nv_bfloat16, true>(a, xq, w_q, dev, sms, s)
-                      : launch_pair<__nv_bfloat16, false>(a, xq, w_q, dev, sms, s))
-            : (a.silu ? launch_pair<float, true>(a, xq, w_q, dev, sms, s)
-                      : launch_pair<float, false>(a, xq, w_q, dev, sms, s));
+    e = bf16 ? (silu ? launch_pair<__nv_bfloat16, true>(a, xq, w_q, dev, sms, s)
+                     : launch_pair<__nv_bfloat16, false>(a, xq, w_q, dev, sms, s))
+             : (silu ? launch_pair<float, true>(a, xq, w_q, dev, sms, s)
+                     : launch_pair<float, false>(a, xq, w_q, dev, sms, s));
   else
-    e = p->out_dtype == HSTU_DT_BF16 ? launch_single<128, __nv_bfloat16>(a, xq, w_q, dev, s)
-                                     : launch_single<128, float>(a, xq, w_q, dev, s);
+    e = bf16 ? (silu ? launch_single<128, __nv_bfloat16, true>(a, xq, w_q, dev, s)
+                     : launch_single<128, __nv_bfloat16, false>(a, xq, w_q, dev, s))
+             : (silu ? launch_single<128, float, true>(a, xq, w_q, dev, s)
+                     : launch_single<128, float, false>(a, xq, w_q, dev, s));
   return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
 }
 
