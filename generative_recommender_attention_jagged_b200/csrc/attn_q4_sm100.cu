@@ -13,9 +13,9 @@
 //
 // With 128 rows against a key tile the step is bound by instruction issue and by the
 // latencies of its chain (S, SiLU, P), not by the cache's bytes (16 KB a tile).  16 users
-// of 2048 to 4096 keys with 512 candidates, 4 heads: 156 us with the plan and the epilogue,
-// 340 TFLOP/s, 59% of the issue slots used (75% while a block is in its loop); 8 users of
-// 6144 to 8192 keys with 128 rows: 66 us.
+// of 2048 to 4096 keys with 512 candidates, 4 heads: 173 us with the plan and the epilogue,
+// 300 TFLOP/s, 59% of the issue slots used (75% while a block is in its loop); 8 users of
+// 6144 to 8192 keys with 128 rows: 70 us.
 //
 //   - eight elementwise warps (two 32-key chunks of each tile each) turn S(t) into P(t).
 //     S is double-buffered in tensor memory, so the tensor core does O += P(t - 1) V(t - 1)
@@ -30,14 +30,16 @@
 //     8 stages: page ids, scales and codes each two tiles ahead of the next); one more warp
 //     builds the position window (2 stages), one issues the MMAs.
 //
-// Weights: in packed bf16 (score, tanh, weight and weight times scale are rounded) in calls
-// with long sequences; in fp32 with one rounding at the end where no sequence exceeds
-// kShortSequence, and on request (HSTU_F_PRECISE_SILU): relative error of y 2.0e-3 against
-// 1.8e-3 at 4000 keys, 2.5e-3 against 1.8e-3 at 1500 and 3.4e-3 against 2.2e-3 at 200, for
-// 1-3% of the time in short calls and 5-6% in long ones.  In both, the position bias is in
-// bf16 (as in attn_sm100_single.cu), and where a row's 32 keys lie in more than one time
-// bucket the time bias and the sum of the two are (one packed addition instead of a copy of
-// the weights' code for each mode); in one bucket the time bias is added in fp32.
+// Weights: in fp32, then as two bf16 terms, of which the second takes the other half of the
+// score's columns in tensor memory, with a GEMM each.  What LayerNorm leaves of o is as noisy
+// as the weights however many keys there are, and only means that differ from head to head
+// hide it: with one head the error of y is 1.63e-3 so (its own rounding), 2.3e-3 with one
+// term (up to 1.8 times its own rounding in calls of few rows) and 4.0e-3 with the packed
+// bf16 arithmetic of attn_sm100_single.cu.  16 x 512 candidates take 173 us, 166 and 156; 8 x
+// 128 rows 70, 68 and 65.  The position bias is in bf16 (as there), and where a row's 32 keys
+// lie in more than one time bucket the time bias and the sum of the two are (one packed
+// addition instead of a copy of the weights' code for each mode); in one bucket the time bias
+// is added in fp32.
 //
 // Tiles of new tokens (bf16 rows) take the same path without widening.  A value
 // row that is not finite is stored as zeros and its scale set to NaN: the mask is
@@ -70,7 +72,7 @@ constexpr uint32_t kTmemCols = 512;       // S0 [0,128) S1 [128,256) O [256,384)
 struct KeyInfo {
   long long ts[kTile];    // timestamps (the last one repeated past the tile's width)
   float ks[kTile];        // alpha / 2 times the scale of the key (new tokens: alpha / 2); 0 past the width
-  uint32_t vs[kTile / 2]; // bf16 pairs: scale of the value (new tokens: 1); 0 past the width
+  float vs[kTile];        // scale of the value (new tokens: 1); 0 past the width
 };
 struct Window {
   uint4 win[kWinChunks][8];
@@ -112,11 +114,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -128,6 +125,10 @@ __device__ __forceinline__ uint4 widen8(uint32_t w, uint32_t zz) {
                     sub_bf16x2(((w >> 4) & 0x000F000Fu) | 0x43004300u, zz),
                     sub_bf16x2(((w >> 8) & 0x000F000Fu) | 0x43004300u, zz),
                     sub_bf16x2(((w >> 12) & 0x000F000Fu) | 0x43004300u, zz));
+}
+// a bf16 pair as two fp32
+__device__ __forceinline__ uint64_t widen_pair(uint32_t w) {
+  return pk2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 // whether a bf16 pair holds an infinity or NaN
 __device__ __forceinline__ bool not_finite(uint32_t w) {
@@ -175,34 +176,30 @@ __device__ __forceinline__ float add_time_bias(int mode, uint32_t (&pw)[kCols / 
   return 0.f;
 }
 
-// kCols scores of one row -> weights times the values' scales (bf16 pairs, over the biases in
-// pw).  ks, vs: the columns' factors (the same for every lane).
-template <bool PRECISE>
-__device__ __forceinline__ void weights_of(const uint32_t (&sr)[kCols], uint32_t (&pw)[kCols / 2], float tsb,
-                                           const float* ks, const uint32_t* vs) {
-  const uint64_t tsb2 = pk2(tsb, tsb);
-  float4 ks4 = {};
-  uint4 vs4 = {};
+// kCols scores of one row -> weights times the values' scales, in two bf16 terms (pairs: the
+// first over the biases in pw, the second in lo; a weight that is not finite is NaN).  ks, vs:
+// the columns' factors (the same for every lane).
+__device__ __forceinline__ void weights_of(const uint32_t (&sr)[kCols], uint32_t (&pw)[kCols / 2],
+                                           uint32_t (&lo)[kCols / 2], float tsb, const float* ks, const float* vs) {
+  const uint64_t tsb2 = pk2(tsb, tsb), minus_one2 = pk2(-1.f, -1.f);
+  float4 ks4 = {}, vs4 = {};
 #pragma unroll
   for (int c = 0; c < kCols; c += 2) {
-    if (c % 4 == 0) ks4 = *reinterpret_cast<const float4*>(ks + c);
-    if (c % 8 == 0) vs4 = *reinterpret_cast<const uint4*>(vs + c / 2);
-    const uint64_t f2 = c % 4 == 0 ? pk2(ks4.x, ks4.y) : pk2(ks4.z, ks4.w);
-    const uint32_t v2 = c % 8 == 0 ? vs4.x : c % 8 == 2 ? vs4.y : c % 8 == 4 ? vs4.z : vs4.w;
-    float h0, h1;  // half the score, without the position bias
-    upk2(fma2(pk2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2, tsb2), h0, h1);
-    uint32_t p;
-    if constexpr (PRECISE) {
-      h0 += __uint_as_float(pw[c >> 1] << 16);
-      h1 += __uint_as_float(pw[c >> 1] & 0xFFFF0000u);
-      float p0, p1;
-      upk2(fma2(pk2(h0, h1), pk2(tanh_approx(h0), tanh_approx(h1)), pk2(h0, h1)), p0, p1);
-      p = pack_bf16x2(p0 * __uint_as_float(v2 << 16), p1 * __uint_as_float(v2 & 0xFFFF0000u));
-    } else {
-      const uint32_t hb = add_bf16x2(pack_bf16x2(h0, h1), pw[c >> 1]);
-      p = mul_bf16x2(fma_bf16x2(hb, tanh_bf16x2(hb), hb), v2);
+    if (c % 4 == 0) {
+      ks4 = *reinterpret_cast<const float4*>(ks + c);
+      vs4 = *reinterpret_cast<const float4*>(vs + c);
     }
-    pw[c >> 1] = p;
+    const uint64_t f2 = c % 4 == 0 ? pk2(ks4.x, ks4.y) : pk2(ks4.z, ks4.w);
+    const uint64_t v2 = c % 4 == 0 ? pk2(vs4.x, vs4.y) : pk2(vs4.z, vs4.w);
+    const uint64_t bias2 = add_pair(tsb2, widen_pair(pw[c >> 1]));
+    const uint64_t h = fma2(pk2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), f2, bias2);  // half the score
+    float h0, h1, p0, p1;
+    upk2(h, h0, h1);
+    const uint64_t p = mul_pair(fma2(h, pk2(tanh_approx(h0), tanh_approx(h1)), h), v2);
+    upk2(p, p0, p1);
+    pw[c >> 1] = pack_bf16x2(p0, p1);
+    upk2(fma2(widen_pair(pw[c >> 1]), minus_one2, p), p0, p1);
+    lo[c >> 1] = pack_bf16x2(p0, p1);
   }
 }
 
@@ -251,7 +248,6 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-template <bool PRECISE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_q4_sm100_kernel(const AttnArgs a, const BucketTable tab, const int2* tiles,
                          const __grid_constant__ CUtensorMap tm_q) {
@@ -372,9 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_pv = [&](int t) {
         const uint32_t v_base = smem_u32(sm.v[t & 1]);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256, tmem + (t & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8,
-                 sw128_desc(v_base + kk * 2048, kHalfBytes, 1024), idesc_pv, (t > 0 || kk > 0));
+        for (int term = 1; term >= 0; --term)  // the smaller terms first
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 256, tmem + (t & 1) * 128 + (kk >> 1) * 32 + 16 * term + (kk & 1) * 8,
+                   sw128_desc(v_base + kk * 2048, kHalfBytes, 1024), idesc_pv, (t > 0 || kk > 0 || term == 0));
         mma_commit(&sm.bar_v_empty[t & 1]);
       };
       // Q has landed before anything else uses it (and before the CTA may exit)
@@ -461,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (checks) sorted &= ts >= ts_before && in_range(ts);
         key.ts[kc] = ts;
         key.ks[kc] = held ? 0.5f * a.alpha * meta_scale(km) : fresh ? 0.5f * a.alpha : 0.f;
-        reinterpret_cast<uint16_t*>(key.vs)[kc] = (uint16_t)(held ? vm : fresh ? 0x3F80u : 0u);
+        key.vs[kc] = held ? meta_scale(vm) : fresh ? 1.f : 0.f;
       }
       zz1 = held ? pack_bf16x2(128.f + meta_zero(km), 128.f + meta_zero(vm)) : 0x43004300u;  // exact
       __syncwarp();
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (which) {  // a value row that is not finite: zeros, and a weight of NaN for the rows that see it
             bad = __any_sync(0xFu << (lane & ~3), bad);
-            if (bad && wq == 0) reinterpret_cast<uint16_t*>(sm.key[t % kKeyStages].vs)[r] = 0x7FC0u;
+            if (bad && wq == 0) sm.key[t % kKeyStages].vs[r] = __uint_as_float(0x7FC00000u);
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -630,17 +628,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float tsb = add_time_bias(mode, pw, w, key.ts + col0, pos - col0, tsb_lo, sm.thr, sm.rab_ts_half, sm.oct);
         tmem_wait_ld(sr);
-        weights_of<PRECISE>(sr, pw, tsb, key.ks + col0, key.vs + col0 / 2);
+        uint32_t lo[kCols / 2];
+        weights_of(sr, pw, lo, tsb, key.ks + col0, key.vs + col0);
         if (!__all_sync(~0u, climit >= col0 + kCols - 1)) {
           // the mask comes last: a masked key's scales, and so its weight, may be NaN
 #pragma unroll
           for (int k = 0; k < kCols / 2; ++k) {
             const int left = climit - col0 - 2 * k;  // columns allowed after the pair's first
-            pw[k] &= left >= 1 ? ~0u : left == 0 ? 0x0000FFFFu : 0u;
+            const uint32_t on = left >= 1 ? ~0u : left == 0 ? 0x0000FFFFu : 0u;
+            pw[k] &= on;
+            lo[k] &= on;
           }
         }
-        // the chunk's P goes over the first 16 of its own (read) columns
+        // the chunk's P goes over its own (read) columns: the first terms, then the second
         tmem_st16(s_tmem + col0, pw);
+        tmem_st16(s_tmem + col0 + 16, lo);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -697,25 +699,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const int2* tiles, const CUtensorMap& tm_q,
-                                 int max_seq_len, cudaStream_t s) {
+                                 cudaStream_t s) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    cudaError_t e = cudaFuncSetAttribute(attn_q4_sm100_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemBytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_q4_sm100_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)kSmemBytes);
+    const cudaError_t e =
+        cudaFuncSetAttribute(attn_q4_sm100_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   // a CTA per listed tile, head and split
   const long long ctas = ((long long)a.T_q / kTile + a.B) * a.H * a.num_splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  const bool precise = a.precise_silu || std::min(max_seq_len, a.n_max) <= kShortSequence;
-  return launch_dependent(precise ? attn_q4_sm100_kernel<true> : attn_q4_sm100_kernel<false>,
-                          dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, a, thr, tiles, tm_q);
+  return launch_dependent(attn_q4_sm100_kernel, dim3((unsigned)ctas), dim3(kThreads), kSmemBytes, s, a, thr, tiles, tm_q);
 }
 
 }  // namespace hstu

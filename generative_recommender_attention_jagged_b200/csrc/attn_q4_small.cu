@@ -8,7 +8,7 @@
 // history of thousands of cached tokens, so every cached byte is read once for
 // a handful of rows (136 bytes a token and head at d = 128).  With a quarter of
 // bf16's bytes to read, widening the codes counts as much as reading them: 64
-// users of 1000 to 8192 keys, 4 heads of 128, one row each take 77 us (2.3 TB/s),
+// users of 1000 to 8192 keys, 4 heads of 128, one row each take 80 us (2.2 TB/s),
 // with 45% of the issue slots used.  What follows from that:
 //
 //   - A CTA takes one (user, head, part of the cached keys); its warps walk
@@ -38,11 +38,15 @@
 //     (D / 16 sums of 16 products, each to 2^-22 of them).  fp32 calls, which need
 //     more, subtract first.  For V it is taken off before the product (the sum runs
 //     over thousands of keys), one packed subtraction.
-//   - Weights: SiLU in fp32, sums in fp32.  a_ij vs_j goes into the second product
-//     as one bf16 term in calls with long histories, where its roundings average out
-//     (relative error of y 1.8e-3, of which 1.7e-3 is its own rounding), and as two
-//     where no sequence exceeds kShortSequence (with one: 2.3e-3 at 100 keys).  Two
-//     terms for all took 90 us instead of 77 for 64 users of 1000 to 8192 keys.
+//   - Weights: SiLU in fp32, sums in fp32.  a_ij vs_j goes into the second product in
+//     fp16, with codes - vz (integers) in fp16 too: a power of two for each row and
+//     tile of 32 keys brings its largest weight to 2^14 .. 2^15, so that fp16's range is
+//     no limit, and is taken back where the tile's O^T joins the running sum.  The
+//     rounding of 2^-11 is not seen in y (1.64e-3 of it with one head, where 1.63e-3 is
+//     its own rounding).  One bf16 term, 2^-8, is: what LayerNorm leaves of o is as
+//     noisy as the weights however many keys there are (up to 3.2e-3), and only means
+//     that differ from head to head hide it.  64 users of 1000 to 8192 keys, 1 row: 80 us
+//     in fp16, 77 with one bf16 term, 90 with two.
 //   - fp32 calls split each row element and each weight into three bf16 terms
 //     (8 + 8 + 8 bits: what is left is below 2^-24 of it) and run each product
 //     three times, smallest terms first; code - zero is exact as it is, and every
@@ -57,6 +61,7 @@
 // finishes a tile of rows last (a counter in the workspace) adds the parts in order,
 // normalises and gates: one launch behind the plan (plan_q4_kernel), which lists the tiles.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -133,6 +138,38 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the same with fp16 operands
+__device__ __forceinline__ void mma16816_half(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t sub_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// fp16 pair 1024 + nibble i of each 16-bit half
+__device__ __forceinline__ uint32_t widen_half(uint32_t w, int i) {
+  return ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
+}
+
+// The power of two that brings a row's largest weight of a tile to 2^14 .. 2^15 (fp16 holds 65504; smaller weights keep
+// their 11 bits down to 2^-28 of it), and its inverse, both normal numbers.  NaN weights do not count.
+__device__ __forceinline__ float half_scale(float weight) {
+  float m;
+  asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(weight));
+  const uint32_t e = __float_as_uint(m) & 0x7F800000u;
+  return __uint_as_float(min(max(0x7F000000u + (14u << 23) - e, 0x00800000u), 0x7E800000u));
+}
+__device__ __forceinline__ float inverse_scale(float scale) {
+  return __uint_as_float(0x7F000000u - __float_as_uint(scale));
+}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -184,13 +221,12 @@ __device__ __forceinline__ int part_keys(int L, int splits) {
   return max(kMinPart, ((L + splits - 1) / splits + kKeys - 1) / kKeys * kKeys);
 }
 
-// (four CTAs an SM for one N tile of bf16 rows: 125 registers; three otherwise)
-template <typename T, int D, int NQ, int WT>
+// (four CTAs an SM for one N tile of bf16 rows: 128 registers; three otherwise)
+template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     attn_q4_small_kernel(const AttnArgs a, const BucketTable tab, int32_t* counters, const int2* row_tiles) {
   constexpr bool kF32 = sizeof(T) == 4;
-  constexpr int kTerms = kF32 ? 3 : 1;   // bf16 terms of a row element
-  constexpr int kWTerms = kF32 ? 3 : WT; // and of a weight
+  constexpr int kTerms = kF32 ? 3 : 1;  // terms of a row element, and of a weight (bf16 calls: one, in fp16)
   constexpr int kWords = D / 32;   // words of a K row a thread reads (its quarter of the dimensions)
   constexpr int kSteps = D / 16;   // products of 16 dimensions
   constexpr int kTilesM = D / 16;  // 16-dimension tiles of O^T
@@ -401,7 +437,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
     }
     __syncwarp();
     // ---- weights: lane = key, only the rows there are
-    uint32_t p[kWTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
+    uint32_t p[kTerms][NQ][4];  // B fragments of P^T: keys 8 x .. 8 x + 7 against rows 8 w .. 8 w + 7
+    float back[NQ][2];          // fp16 weights: what undoes the scales of rows 8 w + 2 t, 8 w + 2 t + 1
+#pragma unroll
+    for (int w = 0; w < NQ; ++w) back[w][0] = back[w][1] = 0.f;
     {
       const int j = j0 + lane;
       const uint32_t km = st.km[lane], vm = st.vm[lane];
@@ -416,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
         if (r >= nr) break;
         pos_bias[r] = __ldg(bias_of + sm.rp[r]);
       }
-      uint32_t pk[kWTerms][4 * NQ];
+      uint32_t pk[kTerms][4 * NQ];
 #pragma unroll
       for (int r = 0; r < 8 * NQ; r += 2) {
         float wt[2] = {0.f, 0.f};
@@ -426,27 +465,32 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
             const float bias = pos_bias[r + e] + time_bias(sm.thr, sm.rts, sm.oct, sm.t_i[r + e] - tj);
             const float raw = kF32 ? sc_of[r + e] : fmaf(kz, sm.qsum[r + e], sc_of[r + e]);
             wt[e] = j < k_hi ? silu_of<T>(fmaf(ks, raw, bias)) * vs : 0.f;
+            if constexpr (!kF32) {
+              const float scale = half_scale(wt[e]);
+              wt[e] *= scale;
+              if (t == ((r / 2) & 3)) back[r / 8][e] = inverse_scale(scale);
+            }
           }
-        if constexpr (kWTerms > 1) {
-          float y[2][kWTerms];
+        if constexpr (kF32) {
+          float y[2][kTerms];
           split_bf16(wt[0], y[0]);
           split_bf16(wt[1], y[1]);
 #pragma unroll
-          for (int x = 0; x < kWTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
+          for (int x = 0; x < kTerms; ++x) pk[x][r / 2] = pack_bf16x2(y[0][x], y[1][x]);
         } else {
-          pk[0][r / 2] = pack_bf16x2(wt[0], wt[1]);
+          pk[0][r / 2] = pack_half2(wt[0], wt[1]);
         }
       }
       // the lane's weights over its own scores, then transposed by ldmatrix
 #pragma unroll
-      for (int x = 0; x < kWTerms; ++x)
+      for (int x = 0; x < kTerms; ++x)
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
           *reinterpret_cast<uint4*>(xs[lane] + 16 * (NQ * x + w)) =
               make_uint4(pk[x][4 * w], pk[x][4 * w + 1], pk[x][4 * w + 2], pk[x][4 * w + 3]);
       __syncwarp();
 #pragma unroll
-      for (int x = 0; x < kWTerms; ++x)
+      for (int x = 0; x < kTerms; ++x)
 #pragma unroll
         for (int w = 0; w < NQ; ++w)
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -488,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
                              ((uint32_t)reinterpret_cast<const uint16_t*>(vb)[c] << 16);
         }
         vz[half][x] = add_bf16x2_(__byte_perm(st.vm[key], st.vm[key + 1], 0x7632), 0x43004300u);
+        if constexpr (!kF32) vz[half][x] = (vz[half][x] & 0x000F000Fu) | 0x64006400u;  // 128 + zero -> 1024 + zero
       }
     // row g of tile m is the thread's nibble m of its D / 8, row g + 8 its nibble m + D / 16
 #pragma unroll
@@ -497,27 +542,40 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
 #pragma unroll
       for (int w = 0; w < NQ; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[w][e] = kF32 ? 0.f : o[w][m2][e];
+        for (int e = 0; e < 4; ++e) f[w][e] = 0.f;  // a tile is summed by itself
       uint32_t av[2][4];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        av[half][0] = sub_bf16x2(widen(vh[half][0][m2 >> 2], m2 & 3), vz[half][0]);
-        av[half][1] = sub_bf16x2(widen(vh[half][0][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][0]);
-        av[half][2] = sub_bf16x2(widen(vh[half][1][m2 >> 2], m2 & 3), vz[half][1]);
-        av[half][3] = sub_bf16x2(widen(vh[half][1][(m2 + kSecond) >> 2], (m2 + kSecond) & 3), vz[half][1]);
+        auto value = [&](int x, int m) {
+          return kF32 ? sub_bf16x2(widen(vh[half][x][m >> 2], m & 3), vz[half][x])
+                      : sub_half2(widen_half(vh[half][x][m >> 2], m & 3), vz[half][x]);
+        };
+        av[half][0] = value(0, m2);
+        av[half][1] = value(0, m2 + kSecond);
+        av[half][2] = value(1, m2);
+        av[half][3] = value(1, m2 + kSecond);
       }
 #pragma unroll
-      for (int x = kWTerms - 1; x >= 0; --x)
+      for (int x = kTerms - 1; x >= 0; --x)
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
           for (int w = 0; w < NQ; ++w)
-            mma16816(f[w], av[half][0], av[half][1], av[half][2], av[half][3], p[x][w][2 * half],
-                     p[x][w][2 * half + 1]);
+            (kF32 ? mma16816 : mma16816_half)(f[w], av[half][0], av[half][1], av[half][2], av[half][3],
+                                               p[x][w][2 * half], p[x][w][2 * half + 1]);
 #pragma unroll
-      for (int w = 0; w < NQ; ++w)
+      for (int w = 0; w < NQ; ++w) {
+        if constexpr (!kF32) {
+          const uint64_t back2 = pack_pair(back[w][0], back[w][1]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[w][m2][e] = kF32 ? o[w][m2][e] + f[w][e] : f[w][e];
+          for (int e = 0; e < 4; e += 2)
+            unpack_pair(fma_pair(pack_pair(f[w][e], f[w][e + 1]), back2, pack_pair(o[w][m2][e], o[w][m2][e + 1])),
+                        o[w][m2][e], o[w][m2][e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[w][m2][e] += f[w][e];
+        }
+      }
     }
     __syncwarp();  // the tile's slot may be filled again
   }
@@ -686,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 && NQ == 1 ? 4 : 3)
   }
 }
 
-template <typename T, int D, int NQ, int WT>
+template <typename T, int D, int NQ>
 cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles, int n_tiles,
                    cudaStream_t s) {
   constexpr size_t smem = sizeof(SmallSmem<T, D, NQ>);
@@ -694,25 +752,25 @@ cudaError_t launch(const AttnArgs& a, const BucketTable& thr, int32_t* counters,
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   static unsigned long long attr_set = 0;  // one bit per device
   if (!(attr_set & (1ull << dev))) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<T, D, NQ, WT>,
+    const cudaError_t e = cudaFuncSetAttribute(attn_q4_small_kernel<T, D, NQ>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     attr_set |= 1ull << dev;
   }
   const long long ctas = (long long)n_tiles * a.H * a.num_splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-  return launch_dependent(attn_q4_small_kernel<T, D, NQ, WT>, dim3((unsigned)ctas), dim3(kThreads), smem, s, a, thr,
+  return launch_dependent(attn_q4_small_kernel<T, D, NQ>, dim3((unsigned)ctas), dim3(kThreads), smem, s, a, thr,
                           counters, tiles);
 }
 
-template <typename T, int NQ, int WT>
+template <typename T, int NQ>
 cudaError_t launch_d(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles, int n_tiles,
                      cudaStream_t s) {
   switch (a.d) {
-    case 32: return launch<T, 32, NQ, WT>(a, thr, counters, tiles, n_tiles, s);
-    case 64: return launch<T, 64, NQ, WT>(a, thr, counters, tiles, n_tiles, s);
-    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ, WT>(a, thr, counters, tiles, n_tiles, s);
-    default: return launch<T, 128, 1, WT>(a, thr, counters, tiles, n_tiles, s);
+    case 32: return launch<T, 32, NQ>(a, thr, counters, tiles, n_tiles, s);
+    case 64: return launch<T, 64, NQ>(a, thr, counters, tiles, n_tiles, s);
+    case 96: return launch<T, 96, sizeof(T) == 4 ? 1 : NQ>(a, thr, counters, tiles, n_tiles, s);
+    default: return launch<T, 128, 1>(a, thr, counters, tiles, n_tiles, s);
   }
 }
 
@@ -723,16 +781,13 @@ bool attn_q4_small_supported(int head_dim, long long pool_rows) {
 }
 
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,
-                                 int n_tiles, int rows, int max_seq_len, cudaStream_t s) {
+                                 int n_tiles, int rows, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
-  if (!a.in_bf16)
-    return rows == 8 ? launch_d<float, 1, 3>(a, thr, counters, tiles, n_tiles, s)
-                     : launch_d<float, 2, 3>(a, thr, counters, tiles, n_tiles, s);
-  if (std::min(max_seq_len, a.n_max) <= kShortSequence)
-    return rows == 8 ? launch_d<bf16, 1, 2>(a, thr, counters, tiles, n_tiles, s)
-                     : launch_d<bf16, 2, 2>(a, thr, counters, tiles, n_tiles, s);
-  return rows == 8 ? launch_d<bf16, 1, 1>(a, thr, counters, tiles, n_tiles, s)
-                   : launch_d<bf16, 2, 1>(a, thr, counters, tiles, n_tiles, s);
+  if (a.in_bf16)
+    return rows == 8 ? launch_d<bf16, 1>(a, thr, counters, tiles, n_tiles, s)
+                     : launch_d<bf16, 2>(a, thr, counters, tiles, n_tiles, s);
+  return rows == 8 ? launch_d<float, 1>(a, thr, counters, tiles, n_tiles, s)
+                   : launch_d<float, 2>(a, thr, counters, tiles, n_tiles, s);
 }
 
 }  // namespace hstu

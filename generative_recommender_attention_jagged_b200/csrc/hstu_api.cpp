@@ -142,8 +142,8 @@ Layout layout_for(const hstu_attn_params* p, int splits, bool tc, int item_tiles
 // kQ4Tc: bf16, d = 128 and on average more than 8 new rows a user: 128-row
 // tiles on tcgen05.  kQ4Small: the others up to d = 128, 8 or 16 rows a pass.
 // kQ4Simt: d > 128, or on request.  Small against Tc in us, 4 heads: 9 rows of one
-// user of 100 keys 34 / 23, of 8 users of 4000 keys 61 / 45, 12 rows of 64 users of up
-// to 8192 keys 180 / 189; with 8 rows 27 / 23, 43 / 45 and 119 / 189.
+// user of 100 keys 27 / 23, of 8 users of 4000 keys 56 / 45, 12 rows of 64 users of up
+// to 8192 keys 181 / 216; with 8 rows 26 / 23, 42 / 45 and 129 / 229.
 enum Q4Kernel { kQ4Simt, kQ4Small, kQ4Tc };
 
 // pool_rows: num_pages * H * page_size, 0 where it is not known yet (workspace sizes: the CUDA-core kernel,
@@ -294,7 +294,7 @@ int run(const hstu_attn_params* p, const Common& c) {
     int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
     int32_t* counters = reinterpret_cast<int32_t*>(tiles + n_tiles);
     e = launch_plan_q4(a, counters, tiles, n_tiles, rows, 1, c.stream);
-    if (e == cudaSuccess) e = launch_attn_q4_small(a, thr, counters, tiles, n_tiles, rows, p->max_seq_len, c.stream);
+    if (e == cudaSuccess) e = launch_attn_q4_small(a, thr, counters, tiles, n_tiles, rows, c.stream);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }
   if (q4_kernel == kQ4Tc) {
@@ -304,7 +304,7 @@ int run(const hstu_attn_params* p, const Common& c) {
     if (!encode_rows(&tq, c.q, a.T_q, a.H, a.d, a.qkv_stride)) return HSTU_ERR_CUDA;
     int2* tiles = reinterpret_cast<int2*>(static_cast<char*>(c.ws) + l.items_off);
     e = launch_plan_q4(a, nullptr, tiles, q4_tiles(p, kTile), kTile, 0, c.stream);
-    if (e == cudaSuccess) e = launch_attn_q4_sm100(a, thr, tiles, tq, p->max_seq_len, c.stream);
+    if (e == cudaSuccess) e = launch_attn_q4_sm100(a, thr, tiles, tq, c.stream);
     if (e == cudaSuccess) e = launch_epilogue(a, c.stream);
     return e == cudaSuccess ? HSTU_OK : HSTU_ERR_CUDA;
   }

@@ -149,10 +149,6 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-// 4-bit bf16 calls in which no sequence exceeds this take the finer rounding of the weights (see the kernels): over
-// more keys the roundings average out.
-constexpr int kShortSequence = 2048;
-
 // Whether a launch of its own (launch_plan_q4) checks all users before the plan reads anything by way of their offsets:
 // for 4-bit calls, and in large paged batches, where each block of the plan checking the users before its own grows with
 // the square (10,000 users of 100 keys: 3.23 ms against 3.11, 1000 users: 0.34 either way).
@@ -173,12 +169,12 @@ cudaError_t launch_plan_q4(const AttnArgs& a, int32_t* counters, int2* tiles, in
 // is checked) and zeroes their counters.  bf16 and fp32, d = 32, 64, 96 or 128.
 bool attn_q4_small_supported(int head_dim, long long pool_rows);
 cudaError_t launch_attn_q4_small(const AttnArgs& a, const BucketTable& thr, int32_t* counters, const int2* tiles,
-                                 int n_tiles, int rows, int max_seq_len, cudaStream_t s);
+                                 int n_tiles, int rows, cudaStream_t s);
 
 // Many new rows a user over a 4-bit pool (attn_q4_sm100.cu): bf16, d = 128, tiles
 // [T_q / 128 + B] as launch_plan_q4 lists them; partial sums to o_ws, then launch_epilogue.
 cudaError_t launch_attn_q4_sm100(const AttnArgs& a, const BucketTable& thr, const int2* tiles, const CUtensorMap& tm_q,
-                                 int max_seq_len, cudaStream_t s);
+                                 cudaStream_t s);
 
 // Backward of the attention core on CUDA cores (hstu_bwd.cu); gradients fp32,
 // d_rp / d_rt must be zeroed by the caller.

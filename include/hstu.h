@@ -220,15 +220,14 @@ int hstu_attn_fwd_paged(const hstu_attn_params* p, const void* q_new, const void
  * The products use the codes as exact integers (code - zero is exact in bf16).
  * A key's scale is applied to the fp32 score, a value's scale to the weight a.  What
  * bf16 calls round to bf16:
- *   head_dim 128 and more than 8 new rows a user on average: a with its scale, once,
- *     where no sequence exceeds 2048 (max_seq_len, n_max) or with HSTU_F_PRECISE_SILU;
- *     otherwise half the score, its tanh, a, and a with its scale.  In both, tanh is the
- *     hardware's (2^-11), the position bias is bf16, and so are the time bias and the sum
- *     of the two where a row's 32 neighbouring keys lie in more than one time bucket.
- *   other calls up to head_dim 128: a with its scale, once, or to two bf16 terms where no
- *     sequence exceeds 2048; biases are fp32.  The codes go into the product as 128 + code
- *     and (128 + zero) sum_e q_e is taken off in fp32: an error of the score of up to
- *     2^-11 alpha scale sum_e |q_e|, whatever the score.
+ *   head_dim 128 and more than 8 new rows a user on average: a with its scale, to two
+ *     bf16 terms (HSTU_F_PRECISE_SILU changes nothing).  tanh is the hardware's (2^-11), the
+ *     position bias is bf16, and so are the time bias and the sum of the two where a row's
+ *     32 neighbouring keys lie in more than one time bucket.
+ *   other calls up to head_dim 128: a with its scale, to the 11 bits of fp16 (scaled by a
+ *     power of two for each row and 32 keys); biases are fp32.  The codes go into the
+ *     product as 128 + code and (128 + zero) sum_e q_e is taken off in fp32: an error of
+ *     the score of up to 2^-11 alpha scale sum_e |q_e|, whatever the score.
  *   head_dim > 128, HSTU_F_FORCE_SIMT: nothing (fp32).
  * fp32 calls keep 24 bits throughout.
  */

@@ -20,7 +20,7 @@ def test_one_long_user_among_short_ones(at, acts, cands):
     a[7], a[30] = 0, 9                       # one without new rows, one with a row more than a pass takes
     rng = np.random.default_rng(at)
     pb, p4, val = batch(rng.integers(0, 90, size=40), a, c, 1, 128, 1024, 16, seed=acts, gamma=True)
-    check(pb, p4, val, "two")
+    check(pb, p4, val, "few")
     pb, p4, val = batch(rng.integers(0, 90, size=40), a, c, 2, 64, 1024, 16, "f32", seed=acts)
     check_raw(pb, p4, val, False)
 
